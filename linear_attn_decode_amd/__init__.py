@@ -280,3 +280,7 @@ def damp_select(samples, s, k_hi=16, block=32, tau=0.01, stream=None):
                                   _P(cost.data_ptr()), _P(perm.data_ptr()), _stream(stream)),
           "state_damp_select")
     return perm, cost
+
+
+from .serve import (SERVE_SIGNATURES, KVCacheDesc, kv_append, kv_attend, norm_quant,  # noqa: E402,F401
+                    plan_pages, release_pages)

@@ -1,0 +1,82 @@
+// Device helpers of the serving operators (gfx950, wave64): 16-bit and e4m3 conversions,
+// lane reductions and scans.
+#pragma once
+
+#include "serve_kernels.hpp"
+#include "wb_device.hpp"
+
+namespace wb {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr float kE4M3Max = 448.0f;
+
+// Element type T of the WB_* code: conversions of a 16-bit pattern and a pair of values
+template <int T>
+struct Elem;
+template <>
+struct Elem<WB_BF16> {
+    static constexpr int size = 2;
+    static __device__ __forceinline__ float get(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
+    static __device__ __forceinline__ uint16_t put(float x) { return __builtin_bit_cast(uint16_t, (__bf16)x); }
+};
+template <>
+struct Elem<WB_F16> {
+    static constexpr int size = 2;
+    static __device__ __forceinline__ float get(uint16_t b) { return float(__builtin_bit_cast(_Float16, b)); }
+    static __device__ __forceinline__ uint16_t put(float x) { return __builtin_bit_cast(uint16_t, (_Float16)x); }
+};
+template <>
+struct Elem<WB_F32> {
+    static constexpr int size = 4;
+};
+
+// Four e4m3 codes of four values already scaled into [-448, 448], to nearest with ties to
+// the even code (NaN and values past the range give the NaN code)
+__device__ __forceinline__ uint32_t e4m3_pack4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    return uint32_t(w);
+}
+
+// The scale of a group whose largest magnitude is `top`, and what its quotients are taken
+// with. A scale below the normal numbers would be rounded so coarsely that quotients pass
+// 448: there it is the smallest normal number. A zero group divides by 1 (every code is 0).
+__device__ __forceinline__ float e4m3_scale(float top) {
+    const float s = top / kE4M3Max;
+    return s < 0x1p-126f && top > 0.f ? 0x1p-126f : s;
+}
+__device__ __forceinline__ float e4m3_divisor(float scale) { return scale == 0.f ? 1.f : scale; }
+
+// Larger of two magnitudes, a NaN winning
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+
+// Lane swaps: v combined with the value the lane 32 / 16 apart holds
+__device__ __forceinline__ float max_xor32(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float max_xor16(float v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+// Inclusive sum over the lanes of a wavefront
+__device__ __forceinline__ int wave_scan(int v) {
+    const int lane = int(threadIdx.x) & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d, 64);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+}  // namespace wb
