@@ -277,14 +277,13 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs A) {
         float x[8];
         load8<SRC>(src, from, x);
         if constexpr (DST == WB_E4M3) {
-            float top = 0.f;
+            uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(x[j]));
+            for (int j = 0; j < 8; ++j) top = OpMax::of(top, magnitude(x[j]));
+            const float scale = e4m3_scale(__uint_as_float(lanes_reduce<OpMax, L>(top))), by = e4m3_divisor(scale);
+            const float rcp = __builtin_amdgcn_rcpf(by);
 #pragma unroll
-            for (int d = 1; d < L; d <<= 1) top = max_nan(top, __shfl_xor(top, d, 64));
-            const float scale = e4m3_scale(top), by = e4m3_divisor(scale);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = x[j] / by;
+            for (int j = 0; j < 8; ++j) x[j] = quotient(x[j], by, rcp);
             u32x2 w;
             w[0] = e4m3_pack4(x[0], x[1], x[2], x[3]);
             w[1] = e4m3_pack4(x[4], x[5], x[6], x[7]);

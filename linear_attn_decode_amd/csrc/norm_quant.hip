@@ -1,76 +1,209 @@
 // Root-mean-square norm with the residual's addition and an e4m3 output (wbserve.h).
+//
+// One pass: a row's h = x + residual stays in registers (8 columns a chunk, V chunks a lane)
+// between the sum of squares, the groups' maxima and the codes, so every input is read once
+// and every output written once; HBM bounds it (a single row: the launch). The 128 columns
+// of a group are 16 neighbouring lanes of one chunk, so a group's maximum is four DPP steps.
+// Rows of up to 512 columns take 16, 32 or 64 lanes, several rows a wavefront; wider ones a
+// workgroup of as many wavefronts as their chunks need. Strides and alignment are free: the
+// 16-byte accesses need only the element's alignment on this hardware, and the chunk that
+// holds a row's ragged end goes by single elements.
 #include "serve_device.hpp"
 
 namespace wb {
 namespace {
 
-template <int T>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-    if constexpr (T == WB_F32) return static_cast<const float*>(p)[i];
-    else return Elem<T>::get(static_cast<const uint16_t*>(p)[i]);
-}
-template <int T>
-__device__ __forceinline__ void store1(void* p, int64_t i, float x) {
-    if constexpr (T == WB_F32) static_cast<float*>(p)[i] = x;
-    else static_cast<uint16_t*>(p)[i] = Elem<T>::put(x);
-}
-
-// Any width, stride and alignment: a workgroup per row, one column a lane.
-constexpr int kRowThreads = 256;
+typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 
 template <int T>
-__global__ void __launch_bounds__(kRowThreads) norm_any_kernel(const NormArgs A) {
-    __shared__ float red[kRowThreads / 64];
-    const int tid = threadIdx.x, D = A.D;
-    const int64_t n = blockIdx.x;
-    auto h_at = [&](int j) {
-        const float x = load1<T>(A.x, n * A.x_row + j);
-        return A.residual ? x + load1<T>(A.residual, n * A.r_row + j) : x;
+__device__ __forceinline__ void load_chunk(const void* p, int64_t at, int n, float x[8]) {
+    if constexpr (T == WB_F32) {
+        const float* s = static_cast<const float*>(p) + at;
+        if (n >= 8) {
+            const f32x4 a = *reinterpret_cast<const f32x4_a4*>(s), b = *reinterpret_cast<const f32x4_a4*>(s + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = a[i];
+                x[4 + i] = b[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = i < n ? s[i] : 0.f;
+        }
+    } else {
+        const uint16_t* s = static_cast<const uint16_t*>(p) + at;
+        if (n >= 8) {
+            const u32x4 w = *reinterpret_cast<const u32x4_a2*>(s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = Elem<T>::get(uint16_t(w[i]));
+                x[2 * i + 1] = Elem<T>::get(uint16_t(w[i] >> 16));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = i < n ? Elem<T>::get(s[i]) : 0.f;
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void store_chunk(void* p, int64_t at, int n, const float x[8]) {
+    if constexpr (T == WB_F32) {
+        float* s = static_cast<float*>(p) + at;
+        if (n >= 8) {
+            *reinterpret_cast<f32x4_a4*>(s) = f32x4{x[0], x[1], x[2], x[3]};
+            *reinterpret_cast<f32x4_a4*>(s + 4) = f32x4{x[4], x[5], x[6], x[7]};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) s[i] = x[i];
+        }
+    } else {
+        uint16_t* s = static_cast<uint16_t*>(p) + at;
+        if (n >= 8) {
+            u32x4 w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = uint32_t(Elem<T>::put(x[2 * i])) | uint32_t(Elem<T>::put(x[2 * i + 1])) << 16;
+            *reinterpret_cast<u32x4_a2*>(s) = w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) s[i] = Elem<T>::put(x[i]);
+        }
+    }
+}
+
+// LR: lanes of a row (16, 32, 64), or 0 for the whole workgroup. V: chunks of a lane.
+template <int T, int LR, int V>
+__global__ void __launch_bounds__(LR ? 256 : 1024) norm_kernel(const NormArgs A) {
+    __shared__ uint32_t red[16];
+    const int lanes = LR ? LR : int(blockDim.x);
+    const int lane = LR ? int(threadIdx.x) % LR : int(threadIdx.x);
+    const int64_t n = LR ? int64_t(blockIdx.x) * (256 / (LR ? LR : 1)) + threadIdx.x / (LR ? LR : 1) : int64_t(blockIdx.x);
+    if (LR && n >= A.N) return;
+    const int D = A.D;
+
+    // over the row's lanes; `red` is free again when the next one starts (two barriers each)
+    auto row_reduce = [&](auto op, uint32_t v) {
+        using OP = decltype(op);
+        if constexpr (LR != 0) {
+            return lanes_reduce<OP, LR>(v);
+        } else {
+            v = lanes_reduce<OP, 64>(v);
+            const int waves = int(blockDim.x) >> 6;
+            if (waves == 1) return v;
+            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+            __syncthreads();
+            // (sums in one order whatever the wavefront)
+            uint32_t all = red[0];
+            for (int w = 1; w < waves; ++w) all = OP::of(all, red[w]);
+            __syncthreads();
+            return all;
+        }
     };
-    float sum = 0.f;
-    for (int j = tid; j < D; j += kRowThreads) {
-        const float h = h_at(j);
-        sum = __builtin_fmaf(h, h, sum);
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    if ((tid & 63) == 0) red[tid >> 6] = sum;
-    __syncthreads();
-    sum = (red[0] + red[1]) + (red[2] + red[3]);
-    const float rstd = 1.f / sqrtf(sum / float(D) + A.eps);
-    auto y_at = [&](int j) { return h_at(j) * rstd * (A.weight ? load1<T>(A.weight, j) : 1.f); };
 
-    const int group = A.group ? A.group : D, groups = (D + group - 1) / group;
-    for (int g = 0; g < groups; ++g) {
-        const int from = g * group, to = min(D, from + group);
-        float top = 0.f;
-        for (int j = from + tid; j < to; j += kRowThreads) top = max_nan(top, fabsf(y_at(j)));
+    float h[V][8];
+    float sum = 0.f;
 #pragma unroll
-        for (int d = 32; d; d >>= 1) top = max_nan(top, __shfl_xor(top, d, 64));
-        __syncthreads();
-        if ((tid & 63) == 0) red[tid >> 6] = top;
-        __syncthreads();
-        top = max_nan(max_nan(red[0], red[1]), max_nan(red[2], red[3]));
-        const float scale = e4m3_scale(top), by = e4m3_divisor(scale);
-        for (int j = from + tid; j < to; j += kRowThreads)
-            A.codes[n * A.c_row + j] = uint8_t(e4m3_pack4(y_at(j) / by, 0.f, 0.f, 0.f));
-        if (tid == 0) A.scales[n * groups + g] = scale;
+    for (int c = 0; c < V; ++c) {
+        const int j = (c * lanes + lane) * 8, left = D - j;
+        if (left > 0) {
+            load_chunk<T>(A.x, n * A.x_row + j, left, h[c]);
+            if (A.residual) {
+                float r[8];
+                load_chunk<T>(A.residual, n * A.r_row + j, left, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[c][i] += r[i];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[c][i] = 0.f;
+        }
     }
-    // (last: the residual may be stored over the one that was read)
-    if (A.residual) {
-        __syncthreads();
-        for (int j = tid; j < D; j += kRowThreads) store1<T>(A.residual_out, n * A.ro_row + j, h_at(j));
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        const int j = (c * lanes + lane) * 8, left = D - j;
+        if (A.residual && left > 0) store_chunk<T>(A.residual_out, n * A.ro_row + j, left, h[c]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[c][i], h[c][i], sum);
     }
+    sum = __uint_as_float(row_reduce(OpAdd{}, __float_as_uint(sum)));
+    const float rstd = 1.f / sqrtf(sum / float(D) + A.eps);
+
+    uint32_t top[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        const int j = (c * lanes + lane) * 8, left = D - j;
+        float w[8];
+        if (A.weight && left > 0) load_chunk<T>(A.weight, j, left, w);
+        top[c] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            h[c][i] *= rstd;
+            if (A.weight && left > 0) h[c][i] *= w[i];
+            // (columns behind the row are 0 * rstd: NaN where the row's sum is)
+            top[c] = OpMax::of(top[c], i < left ? magnitude(h[c][i]) : 0u);
+        }
+    }
+    if (A.group == 0) {
+        uint32_t all = top[0];
+#pragma unroll
+        for (int c = 1; c < V; ++c) all = OpMax::of(all, top[c]);
+        all = row_reduce(OpMax{}, all);
+#pragma unroll
+        for (int c = 0; c < V; ++c) top[c] = all;
+    } else {
+#pragma unroll
+        for (int c = 0; c < V; ++c) top[c] = lanes_reduce<OpMax, 16>(top[c]);
+    }
+    const int groups = A.group ? (D + 127) / 128 : 1;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+        const int j = (c * lanes + lane) * 8, left = D - j;
+        if (left <= 0) continue;
+        const float scale = e4m3_scale(__uint_as_float(top[c])), by = e4m3_divisor(scale);
+        const float rcp = __builtin_amdgcn_rcpf(by);
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = quotient(h[c][i], by, rcp);
+        u32x2 w;
+        w[0] = e4m3_pack4(q[0], q[1], q[2], q[3]);
+        w[1] = e4m3_pack4(q[4], q[5], q[6], q[7]);
+        uint8_t* out = A.codes + n * A.c_row + j;
+        if (left >= 8) {
+            *reinterpret_cast<u32x2_a1*>(out) = w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left) out[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
+        }
+        if (A.group ? (lane & 15) == 0 : c == 0 && lane == 0) A.scales[n * groups + (A.group ? j >> 7 : 0)] = scale;
+    }
+}
+
+template <int T>
+hipError_t norm_t(const NormArgs& a, hipStream_t s) {
+    const int chunks = (a.D + 7) / 8;
+    auto rows = [&](int per) { return unsigned((a.N + per - 1) / per); };
+    auto threads = [&](int v) { return unsigned(((chunks + v - 1) / v + 63) / 64 * 64); };
+    if (chunks <= 16) norm_kernel<T, 16, 1><<<rows(16), 256, 0, s>>>(a);
+    else if (chunks <= 32) norm_kernel<T, 32, 1><<<rows(8), 256, 0, s>>>(a);
+    else if (chunks <= 64) norm_kernel<T, 64, 1><<<rows(4), 256, 0, s>>>(a);
+    else if (chunks <= 2048) norm_kernel<T, 0, 2><<<a.N, threads(2), 0, s>>>(a);
+    else if (chunks <= 4096) norm_kernel<T, 0, 4><<<a.N, threads(4), 0, s>>>(a);
+    else norm_kernel<T, 0, 8><<<a.N, threads(8), 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
     if (a.N == 0) return hipSuccess;
-    if (a.dtype == WB_BF16) norm_any_kernel<WB_BF16><<<a.N, kRowThreads, 0, s>>>(a);
-    else if (a.dtype == WB_F16) norm_any_kernel<WB_F16><<<a.N, kRowThreads, 0, s>>>(a);
-    else norm_any_kernel<WB_F32><<<a.N, kRowThreads, 0, s>>>(a);
-    return hipGetLastError();
+    if (a.dtype == WB_BF16) return norm_t<WB_BF16>(a, s);
+    if (a.dtype == WB_F16) return norm_t<WB_F16>(a, s);
+    return norm_t<WB_F32>(a, s);
 }
 
 }  // namespace wb

@@ -55,8 +55,49 @@ __device__ __forceinline__ float e4m3_scale(float top) {
 }
 __device__ __forceinline__ float e4m3_divisor(float scale) { return scale == 0.f ? 1.f : scale; }
 
-// Larger of two magnitudes, a NaN winning
-__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+// y / by for a divisor whose reciprocal (rcp = 1 / by) is taken once per group: the product
+// corrected by its remainder, which is the quotient rounded to nearest but for rare ties.
+// An infinite divisor gives NaN.
+__device__ __forceinline__ float quotient(float y, float by, float rcp) {
+    const float q = y * rcp;
+    return __builtin_fmaf(__builtin_fmaf(-q, by, y), rcp, q);
+}
+
+// Magnitudes are compared as their bit patterns: for non-negative floats the order is the
+// same, and a NaN is larger than everything, so that a maximum keeps it.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// Reductions over 2^k neighbouring lanes (every lane gets the result): DPP inside rows of 16,
+// lane swaps across them.
+struct OpMax {
+    static __device__ __forceinline__ uint32_t of(uint32_t a, uint32_t b) { return a > b ? a : b; }
+};
+struct OpAdd {
+    static __device__ __forceinline__ uint32_t of(uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }
+};
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, false));
+}
+template <typename OP, int LANES>
+__device__ __forceinline__ uint32_t lanes_reduce(uint32_t v) {
+    static_assert(LANES == 8 || LANES == 16 || LANES == 32 || LANES == 64, "lanes of a reduction");
+    v = OP::of(v, dpp_u32<0xB1>(v));       // quad_perm: xor 1
+    v = OP::of(v, dpp_u32<0x4E>(v));       // quad_perm: xor 2
+    v = OP::of(v, dpp_u32<0x141>(v));      // row_half_mirror: the other quad of 8
+    if constexpr (LANES >= 16) v = OP::of(v, dpp_u32<0x140>(v));      // row_mirror: the other 8 of 16
+    if constexpr (LANES >= 32) {
+        const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = OP::of(p[0], p[1]);
+    }
+    if constexpr (LANES == 64) {
+        const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = OP::of(p[0], p[1]);
+    }
+    return v;
+}
 
 // Lane swaps: v combined with the value the lane 32 / 16 apart holds
 __device__ __forceinline__ float max_xor32(float v) {
