@@ -153,8 +153,12 @@ struct Attend {
     }
 };
 
+// Wavefronts a SIMD is to hold: a tile in flight of 256 columns takes more than half the registers
 template <int KV, int QT, int D>
-__global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A) {
+constexpr int kWavesPerSimd = D == 256 && (KV != WB_E4M3 || QT == WB_F16) ? 1 : 2;
+
+template <int KV, int QT, int D>
+__global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_kernel(const AttendArgs A) {
     using T = Attend<KV, QT, D>;
     using M = typename T::M;
     constexpr int KQ = T::KQ, VB = T::VB, VN = T::VN, LD = T::LD;
@@ -164,13 +168,15 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A)
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int head = lane & 15, g = lane >> 4;
-    const int hb = blockIdx.y;
+    // heads vary fastest: the workgroups that run together read whole pages, all heads of them
+    // (one head's rows of every page lie in the same few memory channels)
+    const int chunk = blockIdx.x / A.head_blocks, hb = blockIdx.x - chunk * A.head_blocks;
     const int blocks_of_kv = A.head_blocks / A.c.H;
     const int kvh = hb / blocks_of_kv, qb = hb - kvh * blocks_of_kv;
     const int heads = min(16, A.G - 16 * qb);                   // query heads of this workgroup
     const int head0 = kvh * A.G + 16 * qb;
 
-    const Span sp = find_span(A, blockIdx.x);
+    const Span sp = find_span(A, chunk);
     if (sp.r < 0) return;
     const int n = A.lens[sp.r];
     const bool bad_len = n < 0 || n > (A.width << A.page_log2);
@@ -190,35 +196,92 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A)
     const int32_t* pages = A.table + size_t(sp.r) * A.width;
     const int page_mask = (1 << A.page_log2) - 1;
 
-    // Row of the stored array that holds the 8 tokens from t (clamped into the request; a bad
-    // page id is noted and page 0 read instead)
-    auto row_of = [&](int t) -> size_t {
-        t = min(t, (n - 1) & ~7);
-        int page = pages[t >> A.page_log2];
+    // Page of the 8 tokens from t (clamped into the request), and the row of the stored arrays
+    // that holds them (a bad page id is noted and page 0 read instead)
+    auto page_at = [&](int t) { return pages[min(t, (n - 1) & ~7) >> A.page_log2]; };
+    auto row_in = [&](int page, int t) -> size_t {
         if (page < 0 || page >= A.c.pages) {
             bad = 1;
             page = 0;
         }
-        return ((size_t(page) * A.c.H + kvh) << A.page_log2) + (t & page_mask);
+        return ((size_t(page) * A.c.H + kvh) << A.page_log2) + (min(t, (n - 1) & ~7) & page_mask);
     };
 
-    if (!bad_len && n > 0)
-        for (int turn = t0; turn < t1; ++turn) {
-            const int base = from + turn * kTurn + wave * kTile;
-            if (base >= n) break;
-            const size_t krow = row_of(base + 8 * (head >> 2)), vrow = row_of(base + 8 * g);
+    // A tile's keys and values as they are stored, and the scales of the lane's 8 tokens. The
+    // keys of the next tile are requested as soon as the scores have taken this one's, its
+    // values behind the product with this one's, its page ids a tile earlier: a wavefront
+    // keeps a tile in flight while it computes.
+    constexpr int KL = KV == WB_E4M3 ? KQ / 2 : KQ;             // 16-byte loads of a key
+    constexpr int VW = KV == WB_E4M3 ? VB / 4 : VB / 2;         // words of a value block
+    u32x4 kr[2][KL];
+    uint32_t vr[VN][8][VW];
+    f32x4 ks[2], vs[2];
+    const int koff = 8 * (head >> 2), voff = 8 * g;
+    auto load_keys = [&](int page, int page_v, int base) {
+        const size_t row = row_in(page, base + koff);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const size_t at = (row + 4 * t + (head & 3)) * D;
+            if constexpr (KV == WB_E4M3) {
+                const uint8_t* k = static_cast<const uint8_t*>(A.c.k) + at + 16 * g;
+#pragma unroll
+                for (int i = 0; i < KL; ++i) kr[t][i] = *reinterpret_cast<const u32x4*>(k + 64 * i);
+            } else {
+                const uint16_t* k = static_cast<const uint16_t*>(A.c.k) + at + 8 * g;
+#pragma unroll
+                for (int i = 0; i < KL; ++i) kr[t][i] = *reinterpret_cast<const u32x4*>(k + 32 * i);
+            }
+        }
+        if constexpr (KV == WB_E4M3) {
+            const f32x4* s = reinterpret_cast<const f32x4*>(A.c.k_scale + row_in(page_v, base + voff));
+            ks[0] = s[0];
+            ks[1] = s[1];
+        }
+    };
+    auto load_values = [&](int page, int base) {
+        const size_t row = row_in(page, base + voff);
+#pragma unroll
+        for (int vn = 0; vn < VN; ++vn)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const size_t at = (row + j) * D + vn * 16 * VB + head * VB;
+                const uint8_t* v = static_cast<const uint8_t*>(A.c.v) + at * (KV == WB_E4M3 ? 1 : 2);
+                if constexpr (VW == 4) {
+                    *reinterpret_cast<u32x4*>(vr[vn][j]) = *reinterpret_cast<const u32x4*>(v);
+                } else if constexpr (VW == 2) {
+                    *reinterpret_cast<u32x2*>(vr[vn][j]) = *reinterpret_cast<const u32x2*>(v);
+                } else {
+                    vr[vn][j][0] = *reinterpret_cast<const uint32_t*>(v);
+                }
+            }
+        if constexpr (KV == WB_E4M3) {
+            const f32x4* s = reinterpret_cast<const f32x4*>(A.c.v_scale + row);
+            vs[0] = s[0];
+            vs[1] = s[1];
+        }
+    };
 
-            // scores: s[4 t + i] of token base + 8 g + 4 t + i
+    const int end = min(n, from + t1 * kTurn);                   // (n > 0 where it is used)
+    int base = from + t0 * kTurn + wave * kTile;
+    if (!bad_len && n > 0 && base < end) {
+        int pk = page_at(base + koff), pv = page_at(base + voff);
+        int pk_next = page_at(base + kTurn + koff), pv_next = page_at(base + kTurn + voff);
+        load_keys(pk, pv, base);
+        load_values(pv, base);
+        for (; base < end; base += kTurn) {
+            // (the last tile requests itself again, from the caches: a condition around the
+            // loads would make the waits below cover them)
+            const int next = base + kTurn < end ? base + kTurn : base;
+
+            // scores: s[t][i] of token base + 8 g + 4 t + i
             f32x4 s[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 s[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                const size_t row = (krow + 4 * t + (head & 3)) * D;
-                if constexpr (KV == WB_E4M3) {
-                    const uint8_t* k = static_cast<const uint8_t*>(A.c.k) + row + 16 * g;
 #pragma unroll
-                    for (int i = 0; i < KQ / 2; ++i) {
-                        const u32x4 w = *reinterpret_cast<const u32x4*>(k + 64 * i);
+                for (int i = 0; i < KL; ++i) {
+                    const u32x4 w = kr[t][i];
+                    if constexpr (KV == WB_E4M3) {
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const u32x4 a = {e4m3_to_bf16x2<false>(w[2 * e]), e4m3_to_bf16x2<true>(w[2 * e]),
@@ -226,33 +289,40 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A)
                             s[t] = M::mul(a, qh[2 * i + e], s[t]);
                             if constexpr (T::kTwoQ) s[t] = M::mul(a, ql[2 * i + e], s[t]);
                         }
+                    } else {
+                        s[t] = M::mul(w, qh[i], s[t]);
                     }
-                } else {
-                    const uint16_t* k = static_cast<const uint16_t*>(A.c.k) + row + 8 * g;
-#pragma unroll
-                    for (int i = 0; i < KQ; ++i)
-                        s[t] = M::mul(*reinterpret_cast<const u32x4*>(k + 32 * i), qh[i], s[t]);
                 }
             }
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = s[j >> 2][j & 3] * mul;
-            f32x4 vs[2];
-            if constexpr (KV == WB_E4M3) {
-                const f32x4* ks = reinterpret_cast<const f32x4*>(A.c.k_scale + vrow);
-                const f32x4* v4 = reinterpret_cast<const f32x4*>(A.c.v_scale + vrow);
-                const f32x4 k0 = ks[0], k1 = ks[1];
-                vs[0] = v4[0];
-                vs[1] = v4[1];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= j < 4 ? k0[j & 3] : k1[j & 3];
+            for (int j = 0; j < 8; ++j) {
+                x[j] = s[j >> 2][j & 3] * mul;
+                if constexpr (KV == WB_E4M3) x[j] *= ks[j >> 2][j & 3];
             }
+            // (loads return in order: the page ids of the tile after next are requested before
+            // the values of the next, or waiting for them would wait for those too)
+            if (next != base) {
+                pk = pk_next;
+                pv = pv_next;
+            }
+            load_keys(pk, pv, next);
+            pk_next = page_at(next + kTurn + koff);
+            pv_next = page_at(next + kTurn + voff);
+
             const bool whole = base >= seen && base + kTile <= n;
             const int tok = base + 8 * g;
             if (!whole) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (tok + j < seen || tok + j >= n) x[j] = -INFINITY;
+                    if (tok + j < seen || tok + j >= n) {
+                        x[j] = -INFINITY;
+                        if constexpr (KV == WB_E4M3) vs[j >> 2][j & 3] = 0.f;
+#pragma unroll
+                        for (int vn = 0; vn < VN; ++vn)          // 0 * NaN is not 0
+#pragma unroll
+                            for (int c = 0; c < VW; ++c) vr[vn][j][c] = 0;
+                    }
             }
 
             // running maximum of the head (its 4 lanes agree), weights in two limbs
@@ -275,10 +345,6 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A)
                 if constexpr (KV == WB_E4M3) {
                     a *= vs[j >> 1][(2 * j) & 3];
                     b *= vs[j >> 1][(2 * j + 1) & 3];
-                    if (!whole) {           // (scales of masked tokens are not used either)
-                        if (x[2 * j] == -INFINITY) a = 0.f;
-                        if (x[2 * j + 1] == -INFINITY) b = 0.f;
-                    }
                 }
                 const uint16_t ah = Elem<T::MT>::put(a), bh = Elem<T::MT>::put(b);
                 ph[j] = uint32_t(ah) | uint32_t(bh) << 16;
@@ -288,41 +354,31 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A)
 
             // values
 #pragma unroll
-            for (int vn = 0; vn < VN; ++vn) {
-                uint32_t w[8][VB / 2];                 // [token][pair of columns], 16 bits each
+            for (int vn = 0; vn < VN; ++vn)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const size_t at = (vrow + j) * D + vn * 16 * VB + head * VB;
-                    if constexpr (KV == WB_E4M3) {
-                        const uint8_t* v = static_cast<const uint8_t*>(A.c.v) + at;
+                for (int c2 = 0; c2 < VB / 2; ++c2) {              // a pair of columns
+                    uint32_t w[8];
 #pragma unroll
-                        for (int c = 0; c < VB / 4; ++c) {
-                            const uint32_t b = reinterpret_cast<const uint32_t*>(v)[c];
-                            w[j][2 * c] = e4m3_to_bf16x2<false>(b);
-                            w[j][2 * c + 1] = e4m3_to_bf16x2<true>(b);
-                        }
-                    } else {
-                        const uint32_t* v = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(A.c.v) + at);
-#pragma unroll
-                        for (int c = 0; c < VB / 2; ++c) w[j][c] = v[c];
+                    for (int j = 0; j < 8; ++j) {
+                        if constexpr (KV == WB_E4M3)
+                            w[j] = c2 & 1 ? e4m3_to_bf16x2<true>(vr[vn][j][c2 / 2]) : e4m3_to_bf16x2<false>(vr[vn][j][c2 / 2]);
+                        else
+                            w[j] = vr[vn][j][c2];
                     }
-                    if (!whole && (tok + j < seen || tok + j >= n)) {     // 0 * NaN is not 0
 #pragma unroll
-                        for (int c = 0; c < VB / 2; ++c) w[j][c] = 0;
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t sel = e ? 0x07060302u : 0x05040100u;
+                        u32x4 a;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) a[j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], sel);
+                        f32x4& s4 = acc[vn * VB + 2 * c2 + e];
+                        s4 = M::mul(a, ph, s4);
+                        s4 = M::mul(a, pl, s4);
                     }
                 }
-#pragma unroll
-                for (int c = 0; c < VB; ++c) {
-                    const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
-                    u32x4 a;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) a[j] = __builtin_amdgcn_perm(w[2 * j + 1][c / 2], w[2 * j][c / 2], sel);
-                    f32x4& s4 = acc[vn * VB + c];
-                    s4 = M::mul(a, ph, s4);
-                    s4 = M::mul(a, pl, s4);
-                }
-            }
+            load_values(pv, next);
         }
+    }
 
     // join the wavefronts: everything relative to the workgroup's maximum
     l = add_xor32_f32(add_xor16_f32(l));
@@ -378,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A)
             *reinterpret_cast<u32x2*>(o) = w;
             if (A.lse && d == 0) A.lse[size_t(sp.r) * A.Hq + head0 + h] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
         } else {
-            const size_t at = (size_t(blockIdx.x) * A.head_blocks + hb) * 16 + h;
+            const size_t at = (size_t(chunk) * A.head_blocks + hb) * 16 + h;
             *reinterpret_cast<f32x4*>(A.part_o + at * D + d) = v;
             if (d == 0) {
                 A.part_ml[2 * at] = mm;
@@ -392,14 +448,29 @@ __global__ void __launch_bounds__(kThreads, 2) attend_kernel(const AttendArgs A)
     }
 }
 
-// Joins the chunks of a request: a workgroup per (request, query head), D / 4 lanes across
-// the columns and the rest along the chunks.
-constexpr int kJoinThreads = 256;
+// One lane's 4 columns of the joined row (sum v, weight sum l, maximum m) out to o and lse.
+template <int QT>
+__device__ __forceinline__ void finish(const AttendArgs& A, f32x4 v, float l, float m, size_t row, int D, int col) {
+    const float by = l == 0.f ? 1.f : l;
+    u32x2 out;
+    out[0] = uint32_t(Elem<QT>::put(v[0] / by)) | uint32_t(Elem<QT>::put(v[1] / by)) << 16;
+    out[1] = uint32_t(Elem<QT>::put(v[2] / by)) | uint32_t(Elem<QT>::put(v[3] / by)) << 16;
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(A.o) + row * D + col) = out;
+    if (A.lse && col == 0) A.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+}
+
+// Joins the chunks of a request. Few requests (which may have hundreds of chunks each): a
+// workgroup per (request, query head, 64 columns), 16 lanes across the columns and 16 along
+// the chunks, whose factors are worked out once in LDS.
+constexpr int kJoinThreads = 256, kJoinCols = 64, kJoinStep = 1024;
+constexpr int kLongWorkgroups = 2048;
 template <int QT, int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) {
-    constexpr int L = D / 4, N = kJoinThreads / L;
+__global__ void __launch_bounds__(kJoinThreads) join_long_kernel(const AttendArgs A) {
+    constexpr int NT = kJoinThreads, L = kJoinCols / 4, N = NT / L;
+    __shared__ float factor[kJoinStep];
     __shared__ f32x4 part[N][L];
-    __shared__ float stat[N];
+    __shared__ float red_m[NT / 64], red_l[NT / 64];
+    const int tid = threadIdx.x;
     const int r = blockIdx.x, h = blockIdx.y;
     const int first = A.spans[2 * r], count = A.spans[2 * r + 1];
     if (count == 1) return;
@@ -407,40 +478,86 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) 
     const int hb = kvh * (A.head_blocks / A.c.H) + in_kv / 16;
     const size_t at0 = (size_t(first) * A.head_blocks + hb) * 16 + (in_kv & 15);
     const size_t step = size_t(A.head_blocks) * 16;
+
     float m = -INFINITY;
-    for (int c = 0; c < count; ++c) m = fmaxf(m, A.part_ml[2 * (at0 + c * step)]);
+    for (int c = tid; c < count; c += NT) m = fmaxf(m, A.part_ml[2 * (at0 + c * step)]);
+    m = max_xor32(max_xor16(m));
+#pragma unroll
+    for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+    if ((tid & 63) == 0) red_m[tid >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
     const float ref = m == -INFINITY ? 0.f : m;
-    const int d = threadIdx.x % L, w = threadIdx.x / L;
+
+    const int d = tid % L, w = tid / L;
+    const float* col = A.part_o + at0 * D + blockIdx.z * kJoinCols + 4 * d;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
-    for (int c = w; c < count; c += N) {
-        const size_t at = at0 + c * step;
-        const float f = __builtin_amdgcn_exp2f(A.part_ml[2 * at] - ref);
-        l += A.part_ml[2 * at + 1] * f;
-        v += *reinterpret_cast<const f32x4*>(A.part_o + at * D + 4 * d) * f;
+    for (int base = 0; base < count; base += kJoinStep) {
+        const int upto = min(kJoinStep, count - base);
+        __syncthreads();
+        for (int c = tid; c < upto; c += NT) {
+            const size_t at = at0 + (base + c) * step;
+            const float f = __builtin_amdgcn_exp2f(A.part_ml[2 * at] - ref);
+            factor[c] = f;
+            l += A.part_ml[2 * at + 1] * f;
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int c = w; c < upto; c += N) v += *reinterpret_cast<const f32x4*>(col + (base + c) * step * D) * factor[c];
     }
+    l = __uint_as_float(lanes_reduce<OpAdd, 64>(__float_as_uint(l)));
+    if ((tid & 63) == 0) red_l[tid >> 6] = l;
     part[w][d] = v;
-    if (d == 0) stat[w] = l;
     __syncthreads();
     if (w) return;
-    for (int i = 1; i < N; ++i) {
-        v += part[i][d];
-        l += stat[i];
+#pragma unroll
+    for (int i = 1; i < N; ++i) v += part[i][d];
+    l = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
+    finish<QT>(A, v, l, m, size_t(r) * A.Hq + h, D, blockIdx.z * kJoinCols + 4 * d);
+}
+
+// Many requests (of few chunks each, most of them one, which has nothing to join): a
+// workgroup per request and block of heads, a lane per 4 columns.
+template <int QT, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) {
+    const int r = blockIdx.x, hb = blockIdx.y;
+    const int first = A.spans[2 * r], count = A.spans[2 * r + 1];
+    if (count == 1) return;
+    const int blocks_of_kv = A.head_blocks / A.c.H;
+    const int kvh = hb / blocks_of_kv, qb = hb - kvh * blocks_of_kv;
+    const int heads = min(16, A.G - 16 * qb);
+    const size_t step = size_t(A.head_blocks) * 16;
+    for (int e = threadIdx.x; e < heads * (D / 4); e += kJoinThreads) {
+        const int h = e / (D / 4), d = e - h * (D / 4);
+        const size_t at0 = (size_t(first) * A.head_blocks + hb) * 16 + h;
+        const float* ml = A.part_ml + 2 * at0;
+        const float* col = A.part_o + at0 * D + 4 * d;
+        float m = -INFINITY;
+#pragma unroll 4
+        for (int c = 0; c < count; ++c) m = fmaxf(m, ml[2 * c * step]);
+        const float ref = m == -INFINITY ? 0.f : m;
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
+        float l = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < count; ++c) {
+            const float f = __builtin_amdgcn_exp2f(ml[2 * c * step] - ref);
+            l += ml[2 * c * step + 1] * f;
+            v += *reinterpret_cast<const f32x4*>(col + c * step * D) * f;
+        }
+        finish<QT>(A, v, l, m, size_t(r) * A.Hq + kvh * A.G + 16 * qb + h, D, 4 * d);
     }
-    const float by = l == 0.f ? 1.f : l;
-    u32x2 out;
-    out[0] = uint32_t(Elem<QT>::put(v[0] / by)) | uint32_t(Elem<QT>::put(v[1] / by)) << 16;
-    out[1] = uint32_t(Elem<QT>::put(v[2] / by)) | uint32_t(Elem<QT>::put(v[3] / by)) << 16;
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(A.o) + (size_t(r) * A.Hq + h) * D + 4 * d) = out;
-    if (A.lse && d == 0) A.lse[size_t(r) * A.Hq + h] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 template <int KV, int QT, int D>
 hipError_t attend_d(const AttendArgs& a, hipStream_t s) {
-    attend_kernel<KV, QT, D><<<dim3(a.chunks, a.head_blocks), kThreads, 0, s>>>(a);
+    attend_kernel<KV, QT, D><<<unsigned(a.chunks) * unsigned(a.head_blocks), kThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.spans) return e;
-    join_kernel<QT, D><<<dim3(a.R, a.Hq), kJoinThreads, 0, s>>>(a);
+    if (int64_t(a.R) * a.Hq * (D / kJoinCols) <= kLongWorkgroups)
+        join_long_kernel<QT, D><<<dim3(a.R, a.Hq, D / kJoinCols), kJoinThreads, 0, s>>>(a);
+    else
+        join_kernel<QT, D><<<dim3(a.R, a.head_blocks), kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int KV, int QT>
@@ -454,13 +571,14 @@ hipError_t attend_t(const AttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
+constexpr int kTarget = 1024;
 // Chunks: `target` workgroups fill the card; R more because every request rounds its own up,
 // and never more than all requests at full width have turns.
 AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width) {
     const int G = Hq / c.H;
     AttendPlan p;
     p.head_blocks = c.H * ((G + 15) / 16);
-    p.target = 1024;
+    p.target = kTarget;
     const int64_t turns = (int64_t(width) * c.page + kTurn - 1) / kTurn;
     const int64_t spread = (p.target + p.head_blocks - 1) / p.head_blocks + R;
     const int64_t most = int64_t(R) * turns;
