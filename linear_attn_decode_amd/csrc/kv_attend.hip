@@ -20,12 +20,14 @@
 //     over all c each lane ends with contiguous columns of its head.
 //   * The weights enter as two 16-bit limbs, p = hi + lo: the second product costs matrix
 //     time that is idle anyway and keeps their rounding (2^-9 in bfloat16) out of the result.
-// Work is split along the cache: a workgroup (4 wavefronts, 128 tokens a turn) takes a chunk
-// of one request's tokens for one key-value head. The chunk length follows from the lengths
-// on the device (every workgroup sums them), so that ragged batches and single long requests
-// fill the card alike and captured graphs keep working as lengths grow. A request of one
-// chunk is finished by its workgroup; others leave their sums in the caller's workspace for
-// a second, small launch.
+// Work is split along the cache. Its units are turns of 128 tokens (a tile for each of a
+// workgroup's 4 wavefronts) of one request for one block of heads, in the order (request,
+// block, turn); as many workgroups as the card holds at once take equal runs of them, found
+// from the lengths on the device, so that ragged batches and single long requests fill the
+// card alike and captured graphs keep working as lengths grow. A run may cover several
+// segments (all turns, or the rest, or the first of a request's block). Segments that are
+// whole are finished by their workgroup; the others, at most two a workgroup, leave their
+// sums in the caller's workspace for a second, small launch.
 #include "serve_device.hpp"
 
 namespace wb {
@@ -45,14 +47,25 @@ __device__ __forceinline__ int turns_of(int n, int window, int most) {
     return (n - first_token(n, window) + kTurn - 1) / kTurn;
 }
 
-struct Span {
-    int r, first, count, index;     // request, its first chunk, its chunks, this chunk among them
-    int turns;
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v)))) |
+                   uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32);
+}
+
+// Run of workgroup w of n: units [total w / n, total (w + 1) / n)
+__device__ __forceinline__ int64_t run_start(int64_t total, int64_t w, int64_t n) { return total * w / n; }
+// The workgroup whose run holds unit u
+__device__ __forceinline__ int64_t run_of(int64_t total, int64_t u, int64_t n) { return ((u + 1) * n - 1) / total; }
+
+struct Run {
+    int64_t total, from, to;        // all units; this workgroup's
+    int64_t start;                  // first unit of request r
+    int r, turns;                   // the request of unit `from`, its turns
+    int n;                          // workgroups with work
 };
 
-// The request that chunk x works for (r < 0: none) -- by every wavefront for itself, 64
-// requests at a time.
-__device__ __forceinline__ Span find_span(const AttendArgs& A, int x) {
+// This workgroup's run (from == to: none) -- every wavefront for itself, 64 requests at a time.
+__device__ __forceinline__ Run find_run(const AttendArgs& A) {
     const int lane = threadIdx.x & 63;
     const int most = A.width << A.page_log2;
     int64_t total = 0;
@@ -62,30 +75,51 @@ __device__ __forceinline__ Span find_span(const AttendArgs& A, int x) {
     }
 #pragma unroll
     for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d, 64);
-    // turns of a chunk: as many as spread all turns over `target` workgroups
-    const int64_t each64 = (total * A.head_blocks + A.target - 1) / A.target;
-    const int each = int(each64 < 1 ? 1 : each64);
-    Span s{-1, 0, 0, 0, 0};
-    int before = 0;
+    Run s;
+    s.total = uniform(total) * A.head_blocks;
+    s.n = int(s.total < gridDim.x ? s.total : int64_t(gridDim.x));
+    s.r = s.turns = 0;
+    s.from = s.to = s.start = 0;
+    if (int(blockIdx.x) >= s.n) return s;
+    s.from = run_start(s.total, blockIdx.x, s.n);
+    s.to = run_start(s.total, int64_t(blockIdx.x) + 1, s.n);
+    const int64_t at = s.from / A.head_blocks;          // in turns of all requests before
+    int64_t before = 0;
     for (int base = 0; base < A.R; base += 64) {
         const int r = base + lane;
         const int turns = r < A.R ? turns_of(A.lens[r], A.window, most) : 0;
-        const int count = (turns + each - 1) / each;
-        const int upto = before + wave_scan(count);
-        const uint64_t past = __ballot(upto > x);
+        int64_t upto = turns;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t o = __shfl_up(upto, d, 64);
+            if (lane >= d) upto += o;
+        }
+        upto += before;
+        const uint64_t past = __ballot(upto > at);
         if (past) {
             const int who = __ffsll((unsigned long long)past) - 1;
             s.r = base + who;
-            s.count = __shfl(count, who, 64);
-            s.first = __shfl(upto, who, 64) - s.count;
-            s.turns = __shfl(turns, who, 64);
-            s.index = x - s.first;
+            s.turns = __builtin_amdgcn_readlane(turns, who);
+            s.start = uniform((__shfl(upto, who, 64) - s.turns) * A.head_blocks);
             break;
         }
         before = __shfl(upto, 63, 64);
     }
     return s;
 }
+
+// Wavefronts a SIMD holds, which is workgroups a compute unit holds: what the registers of a
+// tile in flight leave room for (256 columns of 16 bits take more than half of them)
+constexpr int waves_per_simd(int kv, int qt, int D) {
+    return D == 64 ? 3 : D == 128 ? 2 : kv == WB_E4M3 && qt == WB_BF16 ? 2 : 1;
+}
+
+// A place in a run: turn `turn` of request r for block of heads hb
+struct Place {
+    int r, hb, kvh, turn, turns;    // (turns: of the request; kvh: the block's key-value head)
+    int n, from;                    // the request's tokens (0 if its length is bad), the first that is read
+    bool bad_len;
+};
 
 // 16-bit matrix operands
 template <int T>
@@ -127,9 +161,9 @@ struct Attend {
     using M = Mat<MT>;
 
     // q's operands: lane l holds head l % 16, the 8 values that meet the keys' 8 of each product
-    static __device__ __forceinline__ void load_q(const AttendArgs& A, int r, int head0, int heads, u32x4 hi[KQ],
-                                                  u32x4 lo[KQ]) {
+    static __device__ __forceinline__ void load_q(const AttendArgs& A, int r, int kvh, int qb, u32x4 hi[KQ], u32x4 lo[KQ]) {
         const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+        const int heads = min(16, A.G - 16 * qb), head0 = kvh * A.G + 16 * qb;
         const uint16_t* q = static_cast<const uint16_t*>(A.q) + int64_t(r) * A.q_row + int64_t(head0 + n) * A.q_head;
 #pragma unroll
         for (int i = 0; i < KQ; ++i) {
@@ -153,12 +187,19 @@ struct Attend {
     }
 };
 
-// Wavefronts a SIMD is to hold: a tile in flight of 256 columns takes more than half the registers
-template <int KV, int QT, int D>
-constexpr int kWavesPerSimd = D == 256 && (KV != WB_E4M3 || QT == WB_F16) ? 1 : 2;
+// 4 columns of a finished row (sum v, weight sum l, maximum m) out to o and lse.
+template <int QT>
+__device__ __forceinline__ void finish(const AttendArgs& A, f32x4 v, float l, float m, size_t row, int D, int col) {
+    const float by = l == 0.f ? 1.f : l;
+    u32x2 out;
+    out[0] = uint32_t(Elem<QT>::put(v[0] / by)) | uint32_t(Elem<QT>::put(v[1] / by)) << 16;
+    out[1] = uint32_t(Elem<QT>::put(v[2] / by)) | uint32_t(Elem<QT>::put(v[3] / by)) << 16;
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(A.o) + row * D + col) = out;
+    if (A.lse && col == 0) A.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+}
 
 template <int KV, int QT, int D>
-__global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_kernel(const AttendArgs A) {
+__global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_kernel(const AttendArgs A) {
     using T = Attend<KV, QT, D>;
     using M = typename T::M;
     constexpr int KQ = T::KQ, VB = T::VB, VN = T::VN, LD = T::LD;
@@ -168,57 +209,74 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int head = lane & 15, g = lane >> 4;
-    // heads vary fastest: the workgroups that run together read whole pages, all heads of them
-    // (one head's rows of every page lie in the same few memory channels)
-    const int chunk = blockIdx.x / A.head_blocks, hb = blockIdx.x - chunk * A.head_blocks;
     const int blocks_of_kv = A.head_blocks / A.c.H;
-    const int kvh = hb / blocks_of_kv, qb = hb - kvh * blocks_of_kv;
-    const int heads = min(16, A.G - 16 * qb);                   // query heads of this workgroup
-    const int head0 = kvh * A.G + 16 * qb;
-
-    const Span sp = find_span(A, chunk);
-    if (sp.r < 0) return;
-    const int n = A.lens[sp.r];
-    const bool bad_len = n < 0 || n > (A.width << A.page_log2);
-    const int from = first_token(n, A.window);                  // first token that is read
-    const int seen = A.window && n > A.window ? n - A.window : 0;   // first token that counts
-    const int t0 = int(int64_t(sp.turns) * sp.index / sp.count), t1 = int(int64_t(sp.turns) * (sp.index + 1) / sp.count);
-
-    u32x4 qh[KQ], ql[KQ];
-    T::load_q(A, sp.r, head0, heads, qh, ql);
-
-    f32x4 acc[VN * VB];
-#pragma unroll
-    for (int i = 0; i < VN * VB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
-    int bad = 0;
-    const float mul = A.scale * kLog2e;
-    const int32_t* pages = A.table + size_t(sp.r) * A.width;
     const int page_mask = (1 << A.page_log2) - 1;
+    const float mul = A.scale * kLog2e;
+    const Run run = find_run(A);
+    if (A.spans && blockIdx.x == 0 && tid == 0) A.spans[A.R] = run.total;
+    if (run.from == run.to) return;
 
-    // Page of the 8 tokens from t (clamped into the request), and the row of the stored arrays
-    // that holds them (a bad page id is noted and page 0 read instead)
-    auto page_at = [&](int t) { return pages[min(t, (n - 1) & ~7) >> A.page_log2]; };
-    auto row_in = [&](int page, int t) -> size_t {
-        if (page < 0 || page >= A.c.pages) {
-            bad = 1;
-            page = 0;
+    // The run as a sequence of turns. Three places of it are in work at a time: the turn that
+    // is computed, the next one, whose keys and values are requested, and the one after it,
+    // whose page ids are. Requests' ends make no difference to the sequence: at the start of
+    // a request or block the loads have been in flight as long as inside one.
+    int lens_at = run.r & ~63;
+    int lens64 = lens_at + lane < A.R ? A.lens[lens_at + lane] : 0;
+    Place cur;
+    auto enter = [&](Place& p, int r) {
+        if (r - lens_at >= 64) {
+            lens_at = r & ~63;
+            lens64 = lens_at + lane < A.R ? A.lens[lens_at + lane] : 0;
         }
-        return ((size_t(page) * A.c.H + kvh) << A.page_log2) + (min(t, (n - 1) & ~7) & page_mask);
+        const int n = __builtin_amdgcn_readlane(lens64, r - lens_at), most = A.width << A.page_log2;
+        p.r = r;
+        p.bad_len = n < 0 || n > most;
+        p.n = p.bad_len ? 0 : n;
+        p.turns = turns_of(p.n, A.window, most);
+        p.from = first_token(p.n, A.window);
+    };
+    auto advance = [&](Place& p) {
+        if (++p.turn < p.turns) return;
+        p.turn = 0;
+        if (++p.hb == A.head_blocks) {
+            p.hb = 0;
+            enter(p, p.r + 1);
+        }
+        p.kvh = p.hb / blocks_of_kv;
+    };
+    const int64_t units = run.to - run.from;
+    enter(cur, run.r);
+    cur.hb = int((run.from - run.start) / cur.turns);
+    cur.kvh = cur.hb / blocks_of_kv;
+    cur.turn = int(run.from - run.start - int64_t(cur.hb) * cur.turns);
+    Place next = cur;
+    if (units > 1) advance(next);
+    Place after = next;
+    if (units > 2) advance(after);
+
+    // First token of the lane's group (8 tokens of a tile, from `off`) at a place, clamped into
+    // the request; the page id there; and the row of the stored arrays that holds it: a bad
+    // page id is noted and page 0 read instead
+    auto token_at = [&](const Place& p, int off) {
+        return max(0, min(p.from + p.turn * kTurn + wave * kTile + off, (p.n - 1) & ~7));
+    };
+    auto page_at = [&](const Place& p, int off) { return A.table[size_t(p.r) * A.width + (token_at(p, off) >> A.page_log2)]; };
+    int bad = 0;
+    auto row_in = [&](const Place& p, int page, int off) -> size_t {
+        const bool ok = page >= 0 && page < A.c.pages;
+        bad |= !ok && p.n > 0;
+        page = ok && p.n > 0 ? page : 0;
+        return ((size_t(page) * A.c.H + p.kvh) << A.page_log2) + (token_at(p, off) & page_mask);
     };
 
-    // A tile's keys and values as they are stored, and the scales of the lane's 8 tokens. The
-    // keys of the next tile are requested as soon as the scores have taken this one's, its
-    // values behind the product with this one's, its page ids a tile earlier: a wavefront
-    // keeps a tile in flight while it computes.
+    // A tile's keys and values as they are stored, and the scales of the lane's 8 tokens
     constexpr int KL = KV == WB_E4M3 ? KQ / 2 : KQ;             // 16-byte loads of a key
     constexpr int VW = KV == WB_E4M3 ? VB / 4 : VB / 2;         // words of a value block
     u32x4 kr[2][KL];
     uint32_t vr[VN][8][VW];
     f32x4 ks[2], vs[2];
     const int koff = 8 * (head >> 2), voff = 8 * g;
-    auto load_keys = [&](int page, int page_v, int base) {
-        const size_t row = row_in(page, base + koff);
+    auto load_keys = [&](size_t row, size_t row_v) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const size_t at = (row + 4 * t + (head & 3)) * D;
@@ -233,13 +291,12 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
             }
         }
         if constexpr (KV == WB_E4M3) {
-            const f32x4* s = reinterpret_cast<const f32x4*>(A.c.k_scale + row_in(page_v, base + voff));
+            const f32x4* s = reinterpret_cast<const f32x4*>(A.c.k_scale + row_v);
             ks[0] = s[0];
             ks[1] = s[1];
         }
     };
-    auto load_values = [&](int page, int base) {
-        const size_t row = row_in(page, base + voff);
+    auto load_values = [&](size_t row) {
 #pragma unroll
         for (int vn = 0; vn < VN; ++vn)
 #pragma unroll
@@ -261,17 +318,35 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
         }
     };
 
-    const int end = min(n, from + t1 * kTurn);                   // (n > 0 where it is used)
-    int base = from + t0 * kTurn + wave * kTile;
-    if (!bad_len && n > 0 && base < end) {
-        int pk = page_at(base + koff), pv = page_at(base + voff);
-        int pk_next = page_at(base + kTurn + koff), pv_next = page_at(base + kTurn + voff);
-        load_keys(pk, pv, base);
-        load_values(pv, base);
-        for (; base < end; base += kTurn) {
-            // (the last tile requests itself again, from the caches: a condition around the
-            // loads would make the waits below cover them)
-            const int next = base + kTurn < end ? base + kTurn : base;
+    u32x4 qh[KQ], ql[KQ];
+    T::load_q(A, cur.r, cur.kvh, cur.hb - cur.kvh * blocks_of_kv, qh, ql);
+    size_t row_v;
+    {
+        const int pk = page_at(cur, koff), pv = page_at(cur, voff);
+        const size_t row_k = row_in(cur, pk, koff);
+        row_v = row_in(cur, pv, voff);
+        load_keys(row_k, row_v);
+        load_values(row_v);
+    }
+    int pk = page_at(next, koff), pv = page_at(next, voff);
+
+    f32x4 acc[VN * VB];
+    float m, l;
+    auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < VN * VB; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        m = -INFINITY;
+        l = 0.f;
+    };
+    clear();
+    bool first_segment = true;
+    int t0 = cur.turn;                                          // of the segment
+
+    for (int64_t k = 0; k < units; ++k) {
+            const int n = cur.n, base = cur.from + cur.turn * kTurn + wave * kTile;
+            const int seen = A.window && n > A.window ? n - A.window : 0;     // first token that counts
+            const bool new_block = next.hb != cur.hb || next.r != cur.r;
+            if (A.spans && cur.hb == 0 && cur.turn == 0 && tid == 0) A.spans[cur.r] = run.from + k;
 
             // scores: s[t][i] of token base + 8 g + 4 t + i
             f32x4 s[2];
@@ -300,15 +375,18 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
                 x[j] = s[j >> 2][j & 3] * mul;
                 if constexpr (KV == WB_E4M3) x[j] *= ks[j >> 2][j & 3];
             }
-            // (loads return in order: the page ids of the tile after next are requested before
-            // the values of the next, or waiting for them would wait for those too)
-            if (next != base) {
-                pk = pk_next;
-                pv = pv_next;
-            }
-            load_keys(pk, pv, next);
-            pk_next = page_at(next + kTurn + koff);
-            pv_next = page_at(next + kTurn + voff);
+            // The next tile's keys, as soon as the scores have taken this one's. (Behind the last
+            // tile this is the same tile again, from the caches. Loads return in order: the page
+            // ids of the place after are requested before the values of the next, or waiting
+            // for them would wait for those too.)
+            const int bad_here = bad;
+            bad = 0;
+            if (new_block) T::load_q(A, next.r, next.kvh, next.hb - next.kvh * blocks_of_kv, qh, ql);
+            const size_t row_k = row_in(next, pk, koff);
+            row_v = row_in(next, pv, voff);
+            load_keys(row_k, row_v);
+            pk = page_at(after, koff);
+            pv = page_at(after, voff);
 
             const bool whole = base >= seen && base + kTile <= n;
             const int tok = base + 8 * g;
@@ -376,18 +454,23 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
                         s4 = M::mul(a, pl, s4);
                     }
                 }
-            load_values(pv, next);
-        }
-    }
+            load_values(row_v);
 
-    // join the wavefronts: everything relative to the workgroup's maximum
+            const bool last_turn = cur.turn + 1 == cur.turns;
+            if (last_turn || k + 1 == units) {
+    // end of a segment: join the wavefronts, everything relative to the workgroup's maximum
+    const bool alone = t0 == 0 && last_turn;
+    const int slot = 2 * int(blockIdx.x) + !first_segment;      // of its sums, if it is not whole
+    const int r = cur.r, kvh = cur.kvh, qb = cur.hb - kvh * blocks_of_kv;
+    const int heads = min(16, A.G - 16 * qb), head0 = kvh * A.G + 16 * qb;
     l = add_xor32_f32(add_xor16_f32(l));
+    if (!first_segment) __syncthreads();                        // (the last segment's have been read)
     if (g == 0) {
         stat_m[wave][head] = m;
         stat_l[wave][head] = l;
     }
-    bad = __any(bad);
-    if (lane == 0) bad_page[wave] = bad;
+    const int any_bad = __any(bad_here);
+    if (lane == 0) bad_page[wave] = any_bad;
     __syncthreads();
     float M_ = stat_m[0][head];
 #pragma unroll
@@ -407,11 +490,10 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
                 }
     }
     __syncthreads();
-    int poison = bad_len;
+    int poison = cur.bad_len;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) poison |= bad_page[w];
 
-    const bool alone = sp.count == 1;
     for (int e = tid; e < heads * (D / 4); e += kThreads) {
         const int h = e / (D / 4), d = (e - h * (D / 4)) * 4;
         float mm = stat_m[0][h], ll = 0.f;
@@ -426,15 +508,9 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
         }
         if (poison) ll = __builtin_nanf("");
         if (alone) {
-            const float by = ll == 0.f ? 1.f : ll;
-            uint16_t* o = static_cast<uint16_t*>(A.o) + (size_t(sp.r) * A.Hq + head0 + h) * D + d;
-            u32x2 w;
-            w[0] = uint32_t(Elem<QT>::put(v[0] / by)) | uint32_t(Elem<QT>::put(v[1] / by)) << 16;
-            w[1] = uint32_t(Elem<QT>::put(v[2] / by)) | uint32_t(Elem<QT>::put(v[3] / by)) << 16;
-            *reinterpret_cast<u32x2*>(o) = w;
-            if (A.lse && d == 0) A.lse[size_t(sp.r) * A.Hq + head0 + h] = ll == 0.f ? -INFINITY : mm * kLn2 + logf(ll);
+            finish<QT>(A, v, ll, mm, size_t(r) * A.Hq + head0 + h, D, d);
         } else {
-            const size_t at = (size_t(chunk) * A.head_blocks + hb) * 16 + h;
+            const size_t at = size_t(slot) * 16 + h;
             *reinterpret_cast<f32x4*>(A.part_o + at * D + d) = v;
             if (d == 0) {
                 A.part_ml[2 * at] = mm;
@@ -442,26 +518,38 @@ __global__ void __launch_bounds__(kThreads, (kWavesPerSimd<KV, QT, D>)) attend_k
             }
         }
     }
-    if (A.spans && hb == 0 && sp.index == 0 && tid == 0) {
-        A.spans[2 * sp.r] = sp.first;
-        A.spans[2 * sp.r + 1] = sp.count;
+
+    clear();
+    first_segment = false;
+    t0 = next.turn;
+            } else {
+                bad |= bad_here;
+            }
+            cur = next;
+            next = after;
+            if (k + 3 < units) advance(after);
     }
 }
 
-// One lane's 4 columns of the joined row (sum v, weight sum l, maximum m) out to o and lse.
-template <int QT>
-__device__ __forceinline__ void finish(const AttendArgs& A, f32x4 v, float l, float m, size_t row, int D, int col) {
-    const float by = l == 0.f ? 1.f : l;
-    u32x2 out;
-    out[0] = uint32_t(Elem<QT>::put(v[0] / by)) | uint32_t(Elem<QT>::put(v[1] / by)) << 16;
-    out[1] = uint32_t(Elem<QT>::put(v[2] / by)) | uint32_t(Elem<QT>::put(v[3] / by)) << 16;
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(A.o) + row * D + col) = out;
-    if (A.lse && col == 0) A.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-}
+// The unfinished segments of a request's block of heads: `count` (1: it was finished) in the
+// slots at(c) of the workspace.
+struct Parts {
+    int64_t first;
+    int w0, count;
+    __device__ __forceinline__ Parts(const AttendArgs& A, int r, int hb) {
+        const int64_t total = A.spans[A.R], start = A.spans[r], end = r + 1 < A.R ? A.spans[r + 1] : total;
+        const int64_t turns = (end - start) / A.head_blocks, a = start + hb * turns;
+        const int64_t n = total < A.groups ? total : A.groups;
+        w0 = int(run_of(total, a, n));
+        count = int(run_of(total, a + turns - 1, n)) - w0 + 1;
+        first = 2 * int64_t(w0) + (run_start(total, w0, n) != a);
+    }
+    __device__ __forceinline__ size_t at(int c) const { return size_t(c ? 2 * (int64_t(w0) + c) : first); }
+};
 
-// Joins the chunks of a request. Few requests (which may have hundreds of chunks each): a
-// workgroup per (request, query head, 64 columns), 16 lanes across the columns and 16 along
-// the chunks, whose factors are worked out once in LDS.
+// Joins the segments of a request. Few requests (which may have hundreds each): a workgroup
+// per (request, query head, 64 columns), 16 lanes across the columns and 16 along the
+// segments, whose factors are worked out once in LDS.
 constexpr int kJoinThreads = 256, kJoinCols = 64, kJoinStep = 1024;
 constexpr int kLongWorkgroups = 2048;
 template <int QT, int D>
@@ -472,15 +560,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_long_kernel(const AttendArg
     __shared__ float red_m[NT / 64], red_l[NT / 64];
     const int tid = threadIdx.x;
     const int r = blockIdx.x, h = blockIdx.y;
-    const int first = A.spans[2 * r], count = A.spans[2 * r + 1];
-    if (count == 1) return;
     const int kvh = h / A.G, in_kv = h - kvh * A.G;
-    const int hb = kvh * (A.head_blocks / A.c.H) + in_kv / 16;
-    const size_t at0 = (size_t(first) * A.head_blocks + hb) * 16 + (in_kv & 15);
-    const size_t step = size_t(A.head_blocks) * 16;
+    const Parts parts(A, r, kvh * (A.head_blocks / A.c.H) + in_kv / 16);
+    const int count = parts.count, in_block = in_kv & 15;
+    if (count == 1) return;
 
     float m = -INFINITY;
-    for (int c = tid; c < count; c += NT) m = fmaxf(m, A.part_ml[2 * (at0 + c * step)]);
+    for (int c = tid; c < count; c += NT) m = fmaxf(m, A.part_ml[2 * (parts.at(c) * 16 + in_block)]);
     m = max_xor32(max_xor16(m));
 #pragma unroll
     for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
@@ -490,21 +576,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_long_kernel(const AttendArg
     const float ref = m == -INFINITY ? 0.f : m;
 
     const int d = tid % L, w = tid / L;
-    const float* col = A.part_o + at0 * D + blockIdx.z * kJoinCols + 4 * d;
+    const float* col = A.part_o + blockIdx.z * kJoinCols + 4 * d;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;
     for (int base = 0; base < count; base += kJoinStep) {
         const int upto = min(kJoinStep, count - base);
         __syncthreads();
         for (int c = tid; c < upto; c += NT) {
-            const size_t at = at0 + (base + c) * step;
+            const size_t at = parts.at(base + c) * 16 + in_block;
             const float f = __builtin_amdgcn_exp2f(A.part_ml[2 * at] - ref);
             factor[c] = f;
             l += A.part_ml[2 * at + 1] * f;
         }
         __syncthreads();
 #pragma unroll 8
-        for (int c = w; c < upto; c += N) v += *reinterpret_cast<const f32x4*>(col + (base + c) * step * D) * factor[c];
+        for (int c = w; c < upto; c += N) v += *reinterpret_cast<const f32x4*>(col + (parts.at(base + c) * 16 + in_block) * D) * factor[c];
     }
     l = __uint_as_float(lanes_reduce<OpAdd, 64>(__float_as_uint(l)));
     if ((tid & 63) == 0) red_l[tid >> 6] = l;
@@ -517,33 +603,31 @@ __global__ void __launch_bounds__(kJoinThreads) join_long_kernel(const AttendArg
     finish<QT>(A, v, l, m, size_t(r) * A.Hq + h, D, blockIdx.z * kJoinCols + 4 * d);
 }
 
-// Many requests (of few chunks each, most of them one, which has nothing to join): a
-// workgroup per request and block of heads, a lane per 4 columns.
+// Many requests (of few segments each, most of them whole, with nothing to join): a workgroup
+// per request and block of heads, a lane per 4 columns.
 template <int QT, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) {
-    const int r = blockIdx.x, hb = blockIdx.y;
-    const int first = A.spans[2 * r], count = A.spans[2 * r + 1];
+    const int r = blockIdx.x / A.head_blocks, hb = blockIdx.x - r * A.head_blocks;
+    const Parts parts(A, r, hb);
+    const int count = parts.count;
     if (count == 1) return;
     const int blocks_of_kv = A.head_blocks / A.c.H;
     const int kvh = hb / blocks_of_kv, qb = hb - kvh * blocks_of_kv;
     const int heads = min(16, A.G - 16 * qb);
-    const size_t step = size_t(A.head_blocks) * 16;
     for (int e = threadIdx.x; e < heads * (D / 4); e += kJoinThreads) {
         const int h = e / (D / 4), d = e - h * (D / 4);
-        const size_t at0 = (size_t(first) * A.head_blocks + hb) * 16 + h;
-        const float* ml = A.part_ml + 2 * at0;
-        const float* col = A.part_o + at0 * D + 4 * d;
         float m = -INFINITY;
 #pragma unroll 4
-        for (int c = 0; c < count; ++c) m = fmaxf(m, ml[2 * c * step]);
+        for (int c = 0; c < count; ++c) m = fmaxf(m, A.part_ml[2 * (parts.at(c) * 16 + h)]);
         const float ref = m == -INFINITY ? 0.f : m;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
         float l = 0.f;
 #pragma unroll 4
         for (int c = 0; c < count; ++c) {
-            const float f = __builtin_amdgcn_exp2f(ml[2 * c * step] - ref);
-            l += ml[2 * c * step + 1] * f;
-            v += *reinterpret_cast<const f32x4*>(col + c * step * D) * f;
+            const size_t at = parts.at(c) * 16 + h;
+            const float f = __builtin_amdgcn_exp2f(A.part_ml[2 * at] - ref);
+            l += A.part_ml[2 * at + 1] * f;
+            v += *reinterpret_cast<const f32x4*>(A.part_o + at * D + 4 * d) * f;
         }
         finish<QT>(A, v, l, m, size_t(r) * A.Hq + kvh * A.G + 16 * qb + h, D, 4 * d);
     }
@@ -551,13 +635,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) 
 
 template <int KV, int QT, int D>
 hipError_t attend_d(const AttendArgs& a, hipStream_t s) {
-    attend_kernel<KV, QT, D><<<unsigned(a.chunks) * unsigned(a.head_blocks), kThreads, 0, s>>>(a);
+    attend_kernel<KV, QT, D><<<a.groups, kThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.spans) return e;
     if (int64_t(a.R) * a.Hq * (D / kJoinCols) <= kLongWorkgroups)
         join_long_kernel<QT, D><<<dim3(a.R, a.Hq, D / kJoinCols), kJoinThreads, 0, s>>>(a);
     else
-        join_kernel<QT, D><<<dim3(a.R, a.head_blocks), kJoinThreads, 0, s>>>(a);
+        join_kernel<QT, D><<<unsigned(a.R) * unsigned(a.head_blocks), kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int KV, int QT>
@@ -571,24 +655,22 @@ hipError_t attend_t(const AttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-constexpr int kTarget = 1024;
-// Chunks: `target` workgroups fill the card; R more because every request rounds its own up,
-// and never more than all requests at full width have turns.
-AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width) {
+// As many workgroups as the card's 256 compute units hold at once, and no more than all
+// requests at full width have units.
+AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width, int q_dtype) {
     const int G = Hq / c.H;
     AttendPlan p;
     p.head_blocks = c.H * ((G + 15) / 16);
-    p.target = kTarget;
+    const int per_cu = waves_per_simd(c.dtype, q_dtype, c.D);
     const int64_t turns = (int64_t(width) * c.page + kTurn - 1) / kTurn;
-    const int64_t spread = (p.target + p.head_blocks - 1) / p.head_blocks + R;
-    const int64_t most = int64_t(R) * turns;
-    p.chunks = int(most < spread ? most : spread);
+    const int64_t most = int64_t(R) * turns * p.head_blocks;
+    p.groups = int(most < 256 * per_cu ? most : 256 * per_cu);
     p.part_o_bytes = p.part_ml_bytes = p.spans_bytes = 0;
     if (turns > 1) {
-        const size_t rows = size_t(p.chunks) * p.head_blocks * 16;
+        const size_t rows = size_t(p.groups) * 2 * 16;
         p.part_o_bytes = rows * c.D * 4;
         p.part_ml_bytes = rows * 8;
-        p.spans_bytes = (size_t(R) * 8 + 15) / 16 * 16;
+        p.spans_bytes = (size_t(R) + 1) * 8;
     }
     return p;
 }

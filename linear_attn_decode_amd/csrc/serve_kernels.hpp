@@ -55,21 +55,20 @@ struct AttendArgs {
     const int32_t* lens = nullptr;
     void* o = nullptr;
     float* lse = nullptr;
-    float* part_o = nullptr;      // [chunks][heads blocks][16][D] sums of an unfinished row
-    float* part_ml = nullptr;     // [chunks][heads blocks][16][2] their maximum and weight sum
-    int32_t* spans = nullptr;     // [R][2] first chunk and number of chunks of a request
+    float* part_o = nullptr;      // [groups][2][16][D] sums of unfinished segments
+    float* part_ml = nullptr;     // [groups][2][16][2] their maximum and weight sum
+    int64_t* spans = nullptr;     // [R + 1] first unit of each request, all units
     float scale = 0.f;
     int R = 0, Hq = 0, width = 0, window = 0, q_dtype = 0, page_log2 = 0;
     int G = 1;                    // query heads of a key-value head
     int head_blocks = 1;          // key-value heads times blocks of 16 of their query heads
-    int chunks = 0;               // launched chunks: an upper bound of what any lengths need
-    int target = 0;               // chunks that fill the card
+    int groups = 0;               // workgroups
 };
 struct AttendPlan {
-    int head_blocks, chunks, target;
-    size_t part_o_bytes, part_ml_bytes, spans_bytes;     // all 0: no request can take two chunks
+    int head_blocks, groups;
+    size_t part_o_bytes, part_ml_bytes, spans_bytes;     // all 0: no request can take two turns
 };
-AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width);
+AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width, int q_dtype);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);
 
 struct NormArgs {

@@ -144,7 +144,8 @@ int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes
     if (!bytes) return WB_EINVAL;
     const int v = check_attend(c, R, Hq, width);
     if (v) return v;
-    *bytes = work_bytes_of(wb::attend_plan(*c, R, Hq, width));
+    // (either type of q: the one with more workgroups)
+    *bytes = work_bytes_of(wb::attend_plan(*c, R, Hq, width, WB_BF16));
     return WB_OK;
 }
 
@@ -159,7 +160,7 @@ int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head
     if (!aligned(q, 16) || !aligned(o, 16) || q_row % 8 || q_head % 8 || !aligned(table, 4) || !aligned(lens, 4) ||
         !aligned(lse, 4))
         return WB_EALIGN;
-    const wb::AttendPlan p = wb::attend_plan(*c, R, Hq, width);
+    const wb::AttendPlan p = wb::attend_plan(*c, R, Hq, width, q_dtype);
     const size_t need = work_bytes_of(p);
     if (need) {
         if (!work) return WB_EINVAL;
@@ -179,7 +180,7 @@ int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head
         uint8_t* w = static_cast<uint8_t*>(work);
         a.part_o = reinterpret_cast<float*>(w);
         a.part_ml = reinterpret_cast<float*>(w + p.part_o_bytes);
-        a.spans = reinterpret_cast<int32_t*>(w + p.part_o_bytes + p.part_ml_bytes);
+        a.spans = reinterpret_cast<int64_t*>(w + p.part_o_bytes + p.part_ml_bytes);
     }
     a.scale = scale;
     a.R = R;
@@ -190,8 +191,7 @@ int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head
     a.page_log2 = page_log2(c->page);
     a.G = Hq / c->H;
     a.head_blocks = p.head_blocks;
-    a.chunks = p.chunks;
-    a.target = p.target;
+    a.groups = p.groups;
     return hip_status(wb::launch_attend(a, static_cast<hipStream_t>(stream)));
 }
 

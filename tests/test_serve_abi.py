@@ -84,28 +84,42 @@ def test_attend_refusals(lib):
     assert attend(lib, e, q_dtype=serve.E4M3) == EINVAL
 
 
-@pytest.mark.parametrize("R,Hq,H,width", [(1, 32, 8, 8192), (256, 32, 4, 512), (65536, 1, 1, 100), (3, 40, 2, 7)])
-def test_attend_workspace_holds_every_split(lib, R, Hq, H, width):
-    """Chunks of a batch never pass what the workspace was sized for: target / blocks spread
-    chunks and one more per request (sum of ceil(t_r / each) <= sum t_r / each + R)."""
+@pytest.mark.parametrize("groups", [1, 2, 7, 256, 768, 1024])
+@pytest.mark.parametrize("seed", range(6))
+def test_attend_runs_and_segments(groups, seed):
+    """The split along the cache, in whole numbers as the kernels take it: workgroup w of n
+    takes units [total w // n, total (w + 1) // n); the workgroup of unit u is
+    ((u + 1) n - 1) // total; every unit is in one run, an unfinished segment is its
+    workgroup's first or last, and a request's block joins one segment per workgroup."""
+    rng = np.random.default_rng(seed)
+    blocks = int(rng.integers(1, 9))
+    turns = rng.integers(1, 1 + 10 ** int(rng.integers(0, 4)), int(rng.integers(1, 40)))
+    total = int(turns.sum()) * blocks
+    n = min(total, groups)
+    start = [total * w // n for w in range(n + 1)]
+    assert all(b > a for a, b in zip(start, start[1:])) and start[0] == 0 and start[n] == total
+    bounds = [0]
+    for t in turns:
+        bounds += [bounds[-1] + int(t) * (b + 1) for b in range(blocks)]
+    for a, b in zip(bounds, bounds[1:]):
+        w0, w1 = ((a + 1) * n - 1) // total, (b * n - 1) // total
+        assert start[w0] <= a < start[w0 + 1] and start[w1] <= b - 1 < start[w1 + 1]
+        for w in range(w0, w1 + 1):
+            if w0 < w1:                                          # unfinished: first or last of w's run
+                assert max(a, start[w]) == start[w] or min(b, start[w + 1]) == start[w + 1]
+                assert w == w0 or start[w] > a                   # (slot 0 of every workgroup but the first)
+
+
+def test_attend_workspace(lib):
+    """Two segments of 16 rows of D sums, their maximum and weight sum for each workgroup,
+    and a first unit for each request and the end."""
     n = ctypes.c_size_t()
-    c = cache(H=H)
-    assert lib.kv_attend_work(c, R, Hq, width, n) == OK
-    blocks = H * -(-(Hq // H) // 16)
-    per_chunk = blocks * 16 * (128 * 4 + 8)
-    turns = -(-width * 16 // 128)
-    chunks = (n.value - -(-R * 8 // 16) * 16) // per_chunk if n.value else R
-    rng = np.random.default_rng(R)
-    for lens in ([width * 16] * min(R, 4096), rng.integers(1, width * 16 + 1, min(R, 4096)), [1] * min(R, 4096)):
-        t = -(-np.asarray(lens, np.int64) // 128)
-        t = np.concatenate([t, np.ones(R - len(t), np.int64)])
-        if n.value == 0:
-            assert t.max() == 1
-            continue
-        # no chunk length the kernel can choose (>= total * blocks / target) needs more
-        target = (chunks - R) * blocks if chunks < R * turns else 1 << 62
-        each = max(1, -(-int(t.sum()) * blocks // max(target, 1)))
-        assert int((-(-t // each)).sum()) <= chunks
+    for R, Hq, H, width, D, groups in ((1, 32, 8, 8192, 128, 768), (256, 32, 4, 512, 128, 768), (3, 40, 2, 9, 64, 3 * 2 * 2 * 2),
+                                       (65536, 1, 1, 100, 64, 1024), (2, 8, 8, 4096, 256, 256)):
+        assert lib.kv_attend_work(cache(H=H, D=D), R, Hq, width, n) == OK
+        blocks = H * -(-(Hq // H) // 16)
+        groups = min(groups, R * blocks * -(-width * 16 // 128))
+        assert n.value == groups * 2 * 16 * (4 * D + 8) + 8 * (R + 1)
 
 
 def test_append_refusals(lib):
