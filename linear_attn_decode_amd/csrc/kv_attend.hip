@@ -52,60 +52,78 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
                    uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32);
 }
 
+// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division is some 150
+// dependent instructions)
+__device__ __forceinline__ int64_t quotient64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
+    return a / b;
+}
 // Run of workgroup w of n: units [total w / n, total (w + 1) / n)
-__device__ __forceinline__ int64_t run_start(int64_t total, int64_t w, int64_t n) { return total * w / n; }
+__device__ __forceinline__ int64_t run_start(int64_t total, int64_t w, int64_t n) { return quotient64(total * w, n); }
 // The workgroup whose run holds unit u
-__device__ __forceinline__ int64_t run_of(int64_t total, int64_t u, int64_t n) { return ((u + 1) * n - 1) / total; }
+__device__ __forceinline__ int64_t run_of(int64_t total, int64_t u, int64_t n) { return quotient64((u + 1) * n - 1, total); }
 
 struct Run {
     int64_t total, from, to;        // all units; this workgroup's
     int64_t start;                  // first unit of request r
-    int r, turns;                   // the request of unit `from`, its turns
-    int n;                          // workgroups with work
+    int r;                          // the request of unit `from`
 };
 
-// This workgroup's run (from == to: none) -- every wavefront for itself, 64 requests at a time.
+// Inclusive sum over the lanes (DPP: shifts inside rows of 16, then the rows' last lanes)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t dpp_i64(int64_t v) {
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(v >> 32), CTRL, ROWS, 0xF, false));
+    return int64_t(uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ int64_t wave_scan64(int64_t v) {
+    v += dpp_i64<0x111, 0xF>(v);    // row_shr:1, 2, 4, 8
+    v += dpp_i64<0x112, 0xF>(v);
+    v += dpp_i64<0x114, 0xF>(v);
+    v += dpp_i64<0x118, 0xF>(v);
+    v += dpp_i64<0x142, 0xA>(v);    // row_bcast:15 into rows 1 and 3
+    v += dpp_i64<0x143, 0xC>(v);    // row_bcast:31 into rows 2 and 3
+    return v;
+}
+__device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
+    return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v), lane))) |
+                   uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32);
+}
+
+// This workgroup's run (from == to: none), by every wavefront for itself: lane l sums the
+// turns of requests [l R / 64, (l + 1) R / 64), one scan finds the lane whose requests hold
+// the run's first unit, another the request among them.
 __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     const int lane = threadIdx.x & 63;
-    const int most = A.width << A.page_log2;
-    int64_t total = 0;
-    for (int base = 0; base < A.R; base += 64) {
-        const int r = base + lane;
-        total += r < A.R ? turns_of(A.lens[r], A.window, most) : 0;
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d, 64);
+    const int most = A.width << A.page_log2, per = (A.R + 63) / 64;
+    auto turns_at = [&](int r) { return r < A.R ? turns_of(A.lens[r], A.window, most) : 0; };
+    int64_t mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i) mine += turns_at(lane * per + i);
+    const int64_t upto = wave_scan64(mine);
     Run s;
-    s.total = uniform(total) * A.head_blocks;
-    s.n = int(s.total < gridDim.x ? s.total : int64_t(gridDim.x));
-    s.r = s.turns = 0;
+    s.total = lane64(upto, 63) * A.head_blocks;
+    const int n = int(s.total < gridDim.x ? s.total : int64_t(gridDim.x));
+    s.r = 0;
     s.from = s.to = s.start = 0;
-    if (int(blockIdx.x) >= s.n) return s;
-    s.from = run_start(s.total, blockIdx.x, s.n);
-    s.to = run_start(s.total, int64_t(blockIdx.x) + 1, s.n);
-    const int64_t at = s.from / A.head_blocks;          // in turns of all requests before
-    int64_t before = 0;
-    for (int base = 0; base < A.R; base += 64) {
-        const int r = base + lane;
-        const int turns = r < A.R ? turns_of(A.lens[r], A.window, most) : 0;
-        int64_t upto = turns;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t o = __shfl_up(upto, d, 64);
-            if (lane >= d) upto += o;
-        }
-        upto += before;
-        const uint64_t past = __ballot(upto > at);
+    if (int(blockIdx.x) >= n) return s;
+    s.from = run_start(s.total, blockIdx.x, n);
+    s.to = run_start(s.total, int64_t(blockIdx.x) + 1, n);
+    const int64_t at = quotient64(s.from, A.head_blocks);          // in turns of all requests before
+    const int who = __ffsll((unsigned long long)__ballot(upto > at)) - 1;
+    int64_t before = lane64(upto, who) - lane64(mine, who);
+    for (int base = who * per;; base += 64) {           // (a lane of it passes `at`)
+        const int turns = base + lane < (who + 1) * per ? turns_at(base + lane) : 0;
+        const int64_t sum = before + wave_scan64(turns);
+        const uint64_t past = __ballot(sum > at);
         if (past) {
-            const int who = __ffsll((unsigned long long)past) - 1;
-            s.r = base + who;
-            s.turns = __builtin_amdgcn_readlane(turns, who);
-            s.start = uniform((__shfl(upto, who, 64) - s.turns) * A.head_blocks);
-            break;
+            const int l = __ffsll((unsigned long long)past) - 1;
+            s.r = base + l;
+            s.start = (lane64(sum, l) - __builtin_amdgcn_readlane(turns, l)) * A.head_blocks;
+            return s;
         }
-        before = __shfl(upto, 63, 64);
+        before = lane64(sum, 63);
     }
-    return s;
 }
 
 // Wavefronts a SIMD holds, which is workgroups a compute unit holds: what the registers of a
@@ -240,13 +258,13 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
         p.turn = 0;
         if (++p.hb == A.head_blocks) {
             p.hb = 0;
-            enter(p, p.r + 1);
+            enter(p, min(p.r + 1, A.R - 1));             // (the run ends before, unless lengths change under it)
         }
         p.kvh = p.hb / blocks_of_kv;
     };
     const int64_t units = run.to - run.from;
     enter(cur, run.r);
-    cur.hb = int((run.from - run.start) / cur.turns);
+    cur.hb = int(quotient64(run.from - run.start, cur.turns));
     cur.kvh = cur.hb / blocks_of_kv;
     cur.turn = int(run.from - run.start - int64_t(cur.hb) * cur.turns);
     Place next = cur;
@@ -538,7 +556,7 @@ struct Parts {
     int w0, count;
     __device__ __forceinline__ Parts(const AttendArgs& A, int r, int hb) {
         const int64_t total = A.spans[A.R], start = A.spans[r], end = r + 1 < A.R ? A.spans[r + 1] : total;
-        const int64_t turns = (end - start) / A.head_blocks, a = start + hb * turns;
+        const int64_t turns = quotient64(end - start, A.head_blocks), a = start + hb * turns;
         const int64_t n = total < A.groups ? total : A.groups;
         w0 = int(run_of(total, a, n));
         count = int(run_of(total, a + turns - 1, n)) - w0 + 1;
@@ -616,18 +634,19 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) 
     const int heads = min(16, A.G - 16 * qb);
     for (int e = threadIdx.x; e < heads * (D / 4); e += kJoinThreads) {
         const int h = e / (D / 4), d = e - h * (D / 4);
-        float m = -INFINITY;
-#pragma unroll 4
-        for (int c = 0; c < count; ++c) m = fmaxf(m, A.part_ml[2 * (parts.at(c) * 16 + h)]);
-        const float ref = m == -INFINITY ? 0.f : m;
+        // in one pass with a running maximum: a segment's sums are requested with its maximum
+        float m = -INFINITY, l = 0.f;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        float l = 0.f;
 #pragma unroll 4
         for (int c = 0; c < count; ++c) {
             const size_t at = parts.at(c) * 16 + h;
-            const float f = __builtin_amdgcn_exp2f(A.part_ml[2 * at] - ref);
-            l += A.part_ml[2 * at + 1] * f;
-            v += *reinterpret_cast<const f32x4*>(A.part_o + at * D + 4 * d) * f;
+            const float mc = A.part_ml[2 * at], lc = A.part_ml[2 * at + 1];
+            const f32x4 vc = *reinterpret_cast<const f32x4*>(A.part_o + at * D + 4 * d);
+            const float top = fmaxf(m, mc), ref = top == -INFINITY ? 0.f : top;
+            const float f = __builtin_amdgcn_exp2f(m - ref), fc = __builtin_amdgcn_exp2f(mc - ref);
+            l = l * f + lc * fc;
+            v = v * f + vc * fc;
+            m = top;
         }
         finish<QT>(A, v, l, m, size_t(r) * A.Hq + kvh * A.G + 16 * qb + h, D, 4 * d);
     }
