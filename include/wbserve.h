@@ -74,8 +74,9 @@ int kv_plan_pages(const int32_t* lens, const int32_t* more, int R, int32_t* tabl
                   int free_size, const int32_t* n_free, int page, int64_t* slots, int64_t n_slots, int32_t* starts,
                   int32_t* lens_out, int32_t* n_free_out, int32_t* status, int32_t* work, void* stream);
 
-/* int32 values of workspace that kv_plan_pages needs (0: `work` may be NULL). Host only. */
-int kv_plan_work(int R, int64_t n_slots);
+/* int32 values of workspace that kv_plan_pages needs (0: `work` may be NULL); in_place: whether
+ * lens_out is lens or n_free_out is n_free. Host only. */
+int kv_plan_work(int R, int64_t n_slots, int in_place);
 
 /* Requests with ended[r] != 0 (uint8 [R]) give their ceil(lens[r] / page) pages back: they
  * are pushed onto the stack of free pages in the order of (request, page), *n_free grows by

@@ -69,22 +69,6 @@ struct Run {
     int r;                          // the request of unit `from`
 };
 
-// Inclusive sum over the lanes (DPP: shifts inside rows of 16, then the rows' last lanes)
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int64_t dpp_i64(int64_t v) {
-    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
-    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(v >> 32), CTRL, ROWS, 0xF, false));
-    return int64_t(uint64_t(hi) << 32 | lo);
-}
-__device__ __forceinline__ int64_t wave_scan64(int64_t v) {
-    v += dpp_i64<0x111, 0xF>(v);    // row_shr:1, 2, 4, 8
-    v += dpp_i64<0x112, 0xF>(v);
-    v += dpp_i64<0x114, 0xF>(v);
-    v += dpp_i64<0x118, 0xF>(v);
-    v += dpp_i64<0x142, 0xA>(v);    // row_bcast:15 into rows 1 and 3
-    v += dpp_i64<0x143, 0xC>(v);    // row_bcast:31 into rows 2 and 3
-    return v;
-}
 __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
     return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v), lane))) |
                    uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32);
@@ -100,7 +84,7 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     int64_t mine = 0;
 #pragma unroll 4
     for (int i = 0; i < per; ++i) mine += turns_at(lane * per + i);
-    const int64_t upto = wave_scan64(mine);
+    const int64_t upto = wave_scan(mine);
     Run s;
     s.total = lane64(upto, 63) * A.head_blocks;
     const int n = int(s.total < gridDim.x ? s.total : int64_t(gridDim.x));
@@ -114,7 +98,7 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     int64_t before = lane64(upto, who) - lane64(mine, who);
     for (int base = who * per;; base += 64) {           // (a lane of it passes `at`)
         const int turns = base + lane < (who + 1) * per ? turns_at(base + lane) : 0;
-        const int64_t sum = before + wave_scan64(turns);
+        const int64_t sum = before + wave_scan(turns);
         const uint64_t past = __ballot(sum > at);
         if (past) {
             const int l = __ffsll((unsigned long long)past) - 1;

@@ -5,20 +5,25 @@ namespace wb {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Planning is two sums over the requests (pages taken, new tokens) and a scatter. One
-// workgroup takes the sums for any number of requests: it first decides whether the whole
-// plan can be carried out (nothing has been written by then, so an output may be its
-// input), then writes it. Up to kPlanSlots slots it also writes the slots, so that a
-// decode step's plan is one launch; more are written by a second launch of many
-// workgroups, which takes the pages before each request from `work`.
+// Planning is two sums over the requests (pages taken, new tokens) and a scatter; it is bound
+// by latency, and by the 8 bytes a slot for plans of whole prompts. Three forms:
+//   * Few slots (a decode step): one workgroup takes the sums and writes everything. It first
+//     decides whether the whole plan can be carried out, so an output may be its input.
+//   * Many slots of up to kPlanRows requests, outputs apart from inputs: every workgroup takes
+//     the sums for itself (1.5 us, while one more launch costs the host 3.5 us and the GPU 5)
+//     and writes its share of the slots; the first also writes the rest.
+//   * Otherwise one workgroup takes the sums, which may be in place, and a second launch of many
+//     workgroups writes the slots, with the pages before each request in `work`.
+// Measured for 256 requests and 698 368 new tokens: 7.6 us in the second form, 13 us in the
+// third (5.9 and 6.9 us of kernels and a gap).
 constexpr int kPlanRows = 1024;        // requests whose sums are kept in LDS
 constexpr int64_t kPlanSlots = 4096;
-constexpr int kFillPerThread = 4, kFillThreads = 256;
+constexpr int kFillPerThread = 8, kFillThreads = 256;
 
 struct PlanShared {
     int starts[kPlanRows + 1];
     int first[kPlanRows];
-    int old[kPlanRows];
+    int old[kPlanRows], more[kPlanRows];
 };
 
 __device__ __forceinline__ int pages_of(int64_t tokens, int log2) {
@@ -37,117 +42,175 @@ __device__ __forceinline__ int row_of(const int* starts, int n, int i) {
     return lo;
 }
 
-// Slot of new token i of request r, and the table entry where it begins a new page.
-__device__ __forceinline__ int64_t place(const PlanArgs& A, int n_free, int r, int i, int start, int old, int first) {
-    const int64_t pos = int64_t(old) + (i - start);
+// Page j of request r, which holds its token at `pos`: one of those taken, entered into the
+// table at its first token (those held end at or before it), or one the request held.
+__device__ __forceinline__ int page_for(const PlanArgs& A, int n_free, int r, int64_t pos, int old, int first) {
     const int j = int(pos >> A.page_log2), have = pages_of(old, A.page_log2);
     const size_t at = size_t(r) * A.width + j;
-    int page;
-    if (j >= have) {
-        page = A.free_pages[n_free - 1 - first - (j - have)];
-        // (a new page is entered at its first token: those held end at or before it)
-        if ((pos & ((int64_t(1) << A.page_log2) - 1)) == 0) A.table[at] = page;
-    } else {
-        page = A.table[at];
+    if (j < have) return A.table[at];
+    const int page = A.free_pages[n_free - 1 - first - (j - have)];
+    if ((pos & ((int64_t(1) << A.page_log2) - 1)) == 0) A.table[at] = page;
+    return page;
+}
+
+// kFillPerThread slots from i0: starts, first (pages before) and old length of the requests by
+// the functions given; new tokens end at `total`. A page is looked up once for its slots.
+template <typename START, typename FIRST, typename OLD>
+__device__ __forceinline__ void fill_slots(const PlanArgs& A, int n_free, int64_t i0, int total, int r, START start,
+                                           FIRST first, OLD old, int64_t slot[kFillPerThread]) {
+    const int mask = (1 << A.page_log2) - 1;
+    int64_t pos = 0, page = 0;
+    int left = 0;                                    // new tokens of request r from i on
+    bool look = true;
+#pragma unroll
+    for (int x = 0; x < kFillPerThread; ++x) {
+        const int64_t i = i0 + x;
+        slot[x] = -1;
+        if (i >= total) continue;
+        if (x == 0 || left == 0) {
+            while (start(r + 1) <= i) ++r;
+            left = int(start(r + 1) - i);
+            pos = int64_t(old(r)) + (i - start(r));
+            look = true;
+        }
+        if (look || (pos & mask) == 0) page = page_for(A, n_free, r, pos, old(r), first(r));
+        look = false;
+        slot[x] = (page << A.page_log2) + (pos & mask);
+        ++pos;
+        --left;
     }
-    return (int64_t(page) << A.page_log2) + (pos & ((int64_t(1) << A.page_log2) - 1));
 }
 
+// Over a workgroup of NT threads: exclusive sums of two counts and the bits any thread set,
+// behind what `sum` holds already (all threads agree on it).
+struct Sums {
+    int64_t a, b;
+    int bits;
+};
 template <int NT>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* lds) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    int64_t s = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 64; ++w) s += lds[w];
-    return s;
-}
-
-// Exclusive sum over the workgroup's threads; *total their sum.
+struct ScanLds {
+    int64_t a[NT / 64], b[NT / 64];
+    int bits[NT / 64];
+};
 template <int NT>
-__device__ __forceinline__ int block_scan(int v, int* lds, int* total) {
-    const int inc = wave_scan(v);
+__device__ __forceinline__ Sums block_scan(int64_t a, int64_t b, int bits, Sums& sum, ScanLds<NT>& lds) {
+    const int wave = threadIdx.x >> 6;
+    const int64_t ia = wave_scan(a), ib = wave_scan(b);
+    const int any = (__any(bits & 1) ? 1 : 0) | (__any(bits & 2) ? 2 : 0);
+    __syncthreads();                                 // (the last scan's have been read)
+    if ((threadIdx.x & 63) == 63) {
+        lds.a[wave] = ia;
+        lds.b[wave] = ib;
+        lds.bits[wave] = any;
+    }
     __syncthreads();
-    if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = inc;
-    __syncthreads();
-    int before = 0, sum = 0;
+    Sums before = sum;
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) {
-        const int x = lds[w];
-        if (w < int(threadIdx.x >> 6)) before += x;
-        sum += x;
+        if (w < wave) {
+            before.a += lds.a[w];
+            before.b += lds.b[w];
+        }
+        sum.a += lds.a[w];
+        sum.b += lds.b[w];
+        sum.bits |= lds.bits[w];
     }
-    *total = sum;
-    return before + inc - v;
+    before.a += ia - a;
+    before.b += ib - b;
+    return before;
 }
 
-template <int NT, bool SLOTS>
+// A thread's slots in a row, 16 bytes at a time where they are all inside.
+__device__ __forceinline__ void store_slots(const PlanArgs& A, int64_t i0, const int64_t slot[kFillPerThread]) {
+    if (i0 + kFillPerThread <= A.n_slots) {
+        int64_t* out = A.slots + i0;
+#pragma unroll
+        for (int x = 0; x < kFillPerThread; x += 2)
+            *reinterpret_cast<longlong2*>(out + x) = make_longlong2(slot[x], slot[x + 1]);
+    } else {
+#pragma unroll
+        for (int x = 0; x < kFillPerThread; ++x)
+            if (i0 + x < A.n_slots) A.slots[i0 + x] = slot[x];
+    }
+}
+
+enum PlanForm { kPlanOne, kPlanSpread, kPlanSums };     // one workgroup; one launch; sums for the second launch
+
+template <int NT, PlanForm FORM>
 __global__ void __launch_bounds__(NT) plan_kernel(const PlanArgs A) {
+    constexpr bool kRows = FORM != kPlanSums;        // the sums stay in LDS
     __shared__ PlanShared sh;
-    __shared__ int64_t red[NT / 64];
-    __shared__ int scan[NT / 64];
+    __shared__ ScanLds<NT> lds;
     const int tid = threadIdx.x, R = A.R;
+    const bool writer = FORM != kPlanSpread || blockIdx.x == 0;
     const int n_free = *A.n_free;
 
-    int64_t tokens = 0, pages = 0;
-    int bad = 0;                                     // bit 0: status 1, bit 1: status 2
-    for (int r = tid; r < R; r += NT) {
-        const int old = A.lens[r], more = A.more[r];
-        if (old < 0 || more < 0) {
-            bad |= 1;
-            continue;
-        }
-        const int want = pages_of(int64_t(old) + more, A.page_log2);
-        if (want > A.width) bad |= 2;
-        tokens += more;
-        pages += want - pages_of(old, A.page_log2);
-    }
-    if (n_free < 0 || n_free > A.free_size) bad |= 1;
-    const int any1 = __syncthreads_or(bad & 1), any2 = __syncthreads_or(bad & 2);
-    tokens = block_sum<NT>(tokens, red);
-    pages = block_sum<NT>(pages, red);
-    const int status = any1 ? 1 : any2 ? 2 : tokens > A.n_slots ? 3 : pages > n_free ? 4 : 0;
-
-    int before_tok = 0, before_pages = 0;
+    // new tokens and pages taken; bits: status 1, status 2. A request that is out of range
+    // counts nothing (the plan is not carried out), so that the sums cannot overflow.
+    Sums sum{0, 0, n_free < 0 || n_free > A.free_size ? 1 : 0};
     for (int base = 0; base < R; base += NT) {
         const int r = base + tid;
-        const int old = r < R ? A.lens[r] : 0, more = r < R && !status ? A.more[r] : 0;
-        const int take = status ? 0 : pages_of(int64_t(old) + more, A.page_log2) - pages_of(old, A.page_log2);
-        int sum_tok, sum_pages;
-        const int start = before_tok + block_scan<NT>(more, scan, &sum_tok);
-        const int first = before_pages + block_scan<NT>(take, scan, &sum_pages);
-        before_tok += sum_tok;
-        before_pages += sum_pages;
-        if (r < R) {
-            A.starts[r] = start;
-            A.lens_out[r] = old + more;
-            if constexpr (SLOTS) {
-                sh.starts[r] = start;
-                sh.first[r] = first;
-                sh.old[r] = old;
-            } else {
-                A.work[r] = first;
+        int old = r < R ? A.lens[r] : 0, more = r < R ? A.more[r] : 0, bits = 0;
+        if (old < 0 || more < 0) bits = 1;
+        else if (pages_of(int64_t(old) + more, A.page_log2) > A.width) bits = 2;
+        const int take = bits ? 0 : pages_of(int64_t(old) + more, A.page_log2) - pages_of(old, A.page_log2);
+        const Sums at = block_scan<NT>(bits ? 0 : more, take, bits, sum, lds);
+        if (kRows && r < R) {
+            sh.starts[r] = int(at.a);
+            sh.first[r] = int(at.b);
+            sh.old[r] = old;
+            sh.more[r] = more;
+        }
+    }
+    const int status = sum.bits & 1 ? 1 : sum.bits ? 2 : sum.a > A.n_slots ? 3 : sum.b > n_free ? 4 : 0;
+    const int before_tok = status ? 0 : int(sum.a), before_pages = status ? 0 : int(sum.b);
+    if constexpr (kRows) {
+        if (writer)
+            for (int r = tid; r < R; r += NT) {      // (a thread's own rows)
+                A.starts[r] = status ? 0 : sh.starts[r];
+                A.lens_out[r] = sh.old[r] + (status ? 0 : sh.more[r]);
+            }
+    } else {
+        Sums again{0, 0, 0};
+        for (int base = 0; base < R; base += NT) {
+            const int r = base + tid;
+            const int old = r < R ? A.lens[r] : 0, more = r < R && !status ? A.more[r] : 0;
+            const int take = status ? 0 : pages_of(int64_t(old) + more, A.page_log2) - pages_of(old, A.page_log2);
+            const Sums at = block_scan<NT>(more, take, 0, again, lds);
+            if (r < R) {
+                A.starts[r] = int(at.a);
+                A.lens_out[r] = old + more;
+                A.work[r] = int(at.b);
             }
         }
     }
-    if (tid == 0) {
+    if (tid == 0 && writer) {
         A.starts[R] = before_tok;
         *A.n_free_out = n_free - before_pages;
         *A.status = status;
     }
-    if constexpr (SLOTS) {
+    if constexpr (FORM == kPlanOne) {
         __syncthreads();
         for (int i = tid; i < A.n_slots; i += NT) {
             int64_t slot = -1;
             if (i < before_tok) {
                 const int r = row_of(sh.starts, R, i);
-                slot = place(A, n_free, r, i, sh.starts[r], sh.old[r], sh.first[r]);
+                const int64_t pos = int64_t(sh.old[r]) + (i - sh.starts[r]);
+                slot = (int64_t(page_for(A, n_free, r, pos, sh.old[r], sh.first[r])) << A.page_log2) +
+                       (pos & ((int64_t(1) << A.page_log2) - 1));
             }
             A.slots[i] = slot;
         }
+    } else if constexpr (FORM == kPlanSpread) {
+        if (tid == 0) sh.starts[R] = before_tok;
+        __syncthreads();
+        const int64_t i0 = (int64_t(blockIdx.x) * NT + tid) * kFillPerThread;
+        if (i0 >= A.n_slots) return;
+        int64_t slot[kFillPerThread];
+        const int r = before_tok ? row_of(sh.starts, R, int(i0 < before_tok ? i0 : before_tok - 1)) : 0;
+        fill_slots(A, n_free, i0, before_tok, r, [&](int x) { return sh.starts[x]; }, [&](int x) { return sh.first[x]; },
+                   [&](int x) { return sh.old[x]; }, slot);
+        store_slots(A, i0, slot);
     }
 }
 
@@ -158,63 +221,38 @@ __global__ void __launch_bounds__(kFillThreads) plan_slots_kernel(const PlanArgs
     // (n_free_out may be n_free: the stack's height before the pages were taken)
     const int last = A.R - 1;
     int64_t slot[kFillPerThread];
-    int r = total ? row_of(A.starts, A.R, int(i0 < total ? i0 : total - 1)) : last;
+    const int r = total ? row_of(A.starts, A.R, int(i0 < total ? i0 : total - 1)) : last;
     int n_free = 0;
     if (total) {
         const int more = A.starts[last + 1] - A.starts[last], len = A.lens_out[last];
         n_free = *A.n_free_out + A.work[last] + pages_of(len, A.page_log2) - pages_of(len - more, A.page_log2);
     }
-#pragma unroll
-    for (int x = 0; x < kFillPerThread; ++x) {
-        const int64_t i = i0 + x;
-        slot[x] = -1;
-        if (i < total) {
-            while (A.starts[r + 1] <= i) ++r;
-            const int start = A.starts[r], old = A.lens_out[r] - (A.starts[r + 1] - start);
-            slot[x] = place(A, n_free, r, int(i), start, old, A.work[r]);
-        }
-    }
-    if (i0 + kFillPerThread <= A.n_slots) {
-        int64_t* out = A.slots + i0;
-#pragma unroll
-        for (int x = 0; x < kFillPerThread; x += 2)
-            *reinterpret_cast<longlong2*>(out + x) = make_longlong2(slot[x], slot[x + 1]);
-    } else {
-        for (int x = 0; i0 + x < A.n_slots; ++x) A.slots[i0 + x] = slot[x];
-    }
+    fill_slots(A, n_free, i0, total, r, [&](int x) { return A.starts[x]; }, [&](int x) { return A.work[x]; },
+               [&](int x) { return A.lens_out[x] - (A.starts[x + 1] - A.starts[x]); }, slot);
+    store_slots(A, i0, slot);
 }
 
 constexpr int kReleaseThreads = 1024;
 __global__ void __launch_bounds__(kReleaseThreads) release_kernel(const ReleaseArgs A) {
     constexpr int NT = kReleaseThreads;
-    __shared__ int64_t red[NT / 64];
-    __shared__ int scan[NT / 64];
+    __shared__ ScanLds<NT> lds;
     __shared__ int at[NT], count[NT];
     const int tid = threadIdx.x, R = A.R;
     const int n_free = *A.n_free;
-    int64_t pages = 0;
-    int bad = n_free < 0 || n_free > A.free_size;
-    for (int r = tid; r < R; r += NT) {
-        const int len = A.lens[r];
-        if (len < 0) bad |= 1;
-        else if (A.ended[r]) {
-            const int n = pages_of(len, A.page_log2);
-            if (n > A.width) bad |= 2;
-            pages += n;
-        }
+    auto pages_in = [&](int r) { return r < R && A.ended[r] && A.lens[r] > 0 ? pages_of(A.lens[r], A.page_log2) : 0; };
+    Sums sum{0, 0, n_free < 0 || n_free > A.free_size ? 1 : 0};
+    for (int base = 0; base < R; base += NT) {
+        const int n = pages_in(base + tid);
+        const int bits = base + tid < R && A.lens[base + tid] < 0 ? 1 : n > A.width ? 2 : 0;
+        block_scan<NT>(n, 0, bits, sum, lds);
     }
-    const int any1 = __syncthreads_or(bad & 1), any2 = __syncthreads_or(bad & 2);
-    pages = block_sum<NT>(pages, red);
-    const int status = any1 ? 1 : any2 ? 2 : n_free + pages > A.free_size ? 4 : 0;
+    const int status = sum.bits & 1 ? 1 : sum.bits ? 2 : n_free + sum.a > A.free_size ? 4 : 0;
     if (tid == 0) *A.status = status;
     if (status) return;
-    int before = n_free;
+    Sums again{n_free, 0, 0};
     for (int base = 0; base < R; base += NT) {
-        const int r = base + tid;
-        const int n = r < R && A.ended[r] ? pages_of(A.lens[r], A.page_log2) : 0;
-        int sum;
-        const int mine = before + block_scan<NT>(n, scan, &sum);
-        before += sum;
+        const int r = base + tid, n = pages_in(r);
+        const int mine = int(block_scan<NT>(n, 0, 0, again, lds).a);
         at[tid] = mine;
         count[tid] = n;
         if (r < R && A.ended[r]) A.lens[r] = 0;
@@ -225,7 +263,7 @@ __global__ void __launch_bounds__(kReleaseThreads) release_kernel(const ReleaseA
                 A.free_pages[at[x] + j] = A.table[size_t(base + x) * A.width + j];
         __syncthreads();
     }
-    if (tid == 0) *A.n_free = before;
+    if (tid == 0) *A.n_free = int(again.a);
 }
 
 // ---------------------------------------------------------------------------
@@ -313,19 +351,24 @@ hipError_t append_d(const AppendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-bool plan_in_one_launch(int R, int64_t n_slots) { return R <= kPlanRows && n_slots <= kPlanSlots; }
+int plan_work(int R, int64_t n_slots, bool in_place) {
+    return R <= kPlanRows && (n_slots <= kPlanSlots || !in_place) ? 0 : R;
+}
 
 hipError_t launch_plan(const PlanArgs& a, hipStream_t s) {
-    if (plan_in_one_launch(a.R, a.n_slots)) {
-        if (a.R <= 256 && a.n_slots <= 1024) plan_kernel<256, true><<<1, 256, 0, s>>>(a);
-        else plan_kernel<1024, true><<<1, 1024, 0, s>>>(a);
+    const bool in_place = a.lens_out == a.lens || a.n_free_out == a.n_free;
+    constexpr int64_t per = kFillThreads * kFillPerThread;
+    const unsigned fill = unsigned((a.n_slots + per - 1) / per);
+    if (plan_work(a.R, a.n_slots, in_place) == 0) {
+        if (a.R <= 256 && a.n_slots <= 1024) plan_kernel<256, kPlanOne><<<1, 256, 0, s>>>(a);
+        else if (a.n_slots <= kPlanSlots) plan_kernel<1024, kPlanOne><<<1, 1024, 0, s>>>(a);
+        else plan_kernel<kFillThreads, kPlanSpread><<<fill, kFillThreads, 0, s>>>(a);
         return hipGetLastError();
     }
-    plan_kernel<1024, false><<<1, 1024, 0, s>>>(a);
+    plan_kernel<1024, kPlanSums><<<1, 1024, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.n_slots == 0) return e;
-    constexpr int64_t per = kFillThreads * kFillPerThread;
-    plan_slots_kernel<<<unsigned((a.n_slots + per - 1) / per), kFillThreads, 0, s>>>(a);
+    plan_slots_kernel<<<fill, kFillThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 

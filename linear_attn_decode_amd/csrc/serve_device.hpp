@@ -109,14 +109,20 @@ __device__ __forceinline__ float max_xor16(float v) {
     return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
-// Inclusive sum over the lanes of a wavefront
-__device__ __forceinline__ int wave_scan(int v) {
-    const int lane = int(threadIdx.x) & 63;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d, 64);
-        if (lane >= d) v += o;
-    }
+// Inclusive sum over the lanes of a wavefront (DPP: shifts inside rows of 16, then the rows' last lanes)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t dpp_i64(int64_t v) {
+    const uint32_t lo = uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_update_dpp(0, int(v >> 32), CTRL, ROWS, 0xF, false));
+    return int64_t(uint64_t(hi) << 32 | lo);
+}
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+    v += dpp_i64<0x111, 0xF>(v);    // row_shr:1, 2, 4, 8
+    v += dpp_i64<0x112, 0xF>(v);
+    v += dpp_i64<0x114, 0xF>(v);
+    v += dpp_i64<0x118, 0xF>(v);
+    v += dpp_i64<0x142, 0xA>(v);    // row_bcast:15 into rows 1 and 3
+    v += dpp_i64<0x143, 0xC>(v);    // row_bcast:31 into rows 2 and 3
     return v;
 }
 

@@ -23,7 +23,8 @@ struct PlanArgs {
     int R = 0, width = 0, free_size = 0, page_log2 = 0;
     int64_t n_slots = 0;
 };
-bool plan_in_one_launch(int R, int64_t n_slots);
+// int32 values of workspace; in_place: lens_out is lens, or n_free_out is n_free
+int plan_work(int R, int64_t n_slots, bool in_place);
 hipError_t launch_plan(const PlanArgs& a, hipStream_t stream);
 
 struct ReleaseArgs {

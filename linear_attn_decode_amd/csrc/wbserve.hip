@@ -52,7 +52,7 @@ size_t work_bytes_of(const wb::AttendPlan& p) { return p.part_o_bytes + p.part_m
 
 extern "C" {
 
-int kv_plan_work(int R, int64_t n_slots) { return wb::plan_in_one_launch(R, n_slots) ? 0 : R; }
+int kv_plan_work(int R, int64_t n_slots, int in_place) { return wb::plan_work(R, n_slots, in_place != 0); }
 
 int kv_plan_pages(const int32_t* lens, const int32_t* more, int R, int32_t* table, int width, const int32_t* free_pages,
                   int free_size, const int32_t* n_free, int page, int64_t* slots, int64_t n_slots, int32_t* starts,
@@ -62,7 +62,7 @@ int kv_plan_pages(const int32_t* lens, const int32_t* more, int R, int32_t* tabl
     const int v = check_table(R, width, page);
     if (v) return v;
     if (n_slots > 0x7FFFFFFF) return WB_EUNSUPPORTED;
-    if (kv_plan_work(R, n_slots) && !work) return WB_EINVAL;
+    if (wb::plan_work(R, n_slots, lens_out == lens || n_free_out == n_free) && !work) return WB_EINVAL;
     if (!aligned(slots, 16)) return WB_EALIGN;
     for (const void* p : {(const void*)lens, (const void*)more, (const void*)table, (const void*)free_pages,
                           (const void*)n_free, (const void*)starts, (const void*)lens_out, (const void*)n_free_out,

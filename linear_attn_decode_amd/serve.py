@@ -34,7 +34,7 @@ class KVCacheDesc(ctypes.Structure):
 _C = ctypes.POINTER(KVCacheDesc)
 SERVE_SIGNATURES = {
     "kv_plan_pages": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I64, _P, _P, _P, _P, _P, _P]),
-    "kv_plan_work": (_I, [_I, _I64]),
+    "kv_plan_work": (_I, [_I, _I64, _I]),
     "kv_release_pages": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _P, _P]),
     "kv_append": (_I, [_C, _P, _P, _I64, _I64, _I, _P, _I, _P]),
     "kv_attend": (_I, [_C, _P, _I64, _I64, _I, _I, _I, _P, _I, _P, _F, _I, _P, _P, _P, _SZ, _P]),
@@ -134,16 +134,19 @@ def _workspace(n, dtype, device, stream):
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale):
-    """The cache's descriptor, its device, shape and type."""
+    """The cache's descriptor, its device, shape and element code."""
     if _torch is None:
         _load()
-    dev = _device(k_cache, "k_cache")
-    kind, shape = k_cache.dtype, k_cache.shape
+    kind, shape, dev = k_cache.dtype, k_cache.shape, k_cache.get_device()
     code = _codes.get(kind, F32)
-    if code == F32 or len(shape) != 4:
-        raise ValueError(f"k_cache: expected bfloat16, float16 or float8_e4m3fn [pages, H, page, D], got {kind} "
-                         f"{tuple(shape)}")
-    k, v = _ptr(k_cache, "k_cache", kind, shape, dev), _ptr(v_cache, "v_cache", kind, shape, dev)
+    if not (dev >= 0 and code != F32 and len(shape) == 4 and v_cache.dtype is kind and v_cache.shape == shape
+            and v_cache.get_device() == dev and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        dev = _device(k_cache, "k_cache")
+        if code == F32 or len(shape) != 4:
+            raise ValueError(f"k_cache: expected bfloat16, float16 or float8_e4m3fn [pages, H, page, D], got {kind} "
+                             f"{tuple(shape)}")
+        _ptr(k_cache, "k_cache", kind, shape, dev)
+        _ptr(v_cache, "v_cache", kind, shape, dev)
     ks = vs = 0
     if code == E4M3:
         if k_scale is None or v_scale is None:
@@ -155,15 +158,15 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
     pages, H, page, D = shape
     if H > _MAX or page > _MAX or D > _MAX:
         raise ValueError(f"k_cache: {tuple(shape)} is too large")
-    return _desc.pack(k, v, ks, vs, pages, page, H, D, code), dev, shape
+    return _desc.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, page, H, D, code), dev, shape, code
 
 
 _MAX = 0x7FFFFFFF
 
 
 @functools.lru_cache(maxsize=1024)
-def _plan_work(R, n):
-    return _fn["kv_plan_work"](R, n)
+def _plan_work(R, n, in_place):
+    return _fn["kv_plan_work"](R, n, in_place)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -197,15 +200,29 @@ def plan_pages(lens, more, table, free, n_free, page: int, slots, starts, status
     lens_out = lens if lens_out is None else lens_out
     n_free_out = n_free if n_free_out is None else n_free_out
     n = slots.shape[0]
-    if R > _MAX or width > _MAX or free.shape[0] > _MAX:
+    size = free.shape[0]
+    if R > _MAX or width > _MAX or size > _MAX:
         raise ValueError(f"table, free: {tuple(table.shape)}, {tuple(free.shape)} are too large")
-    work = _plan_work(R, n)
+    # (one expression for what _ptr checks of each: twelve calls are 2 us)
+    rows, one = (R,), (1,)
+    if not (lens.dtype is i32 and more.dtype is i32 and table.dtype is i32 and free.dtype is i32 and n_free.dtype is i32
+            and starts.dtype is i32 and lens_out.dtype is i32 and n_free_out.dtype is i32 and status.dtype is i32
+            and slots.dtype is _torch.int64 and lens.shape == rows and more.shape == rows and lens_out.shape == rows
+            and n_free.shape == one and n_free_out.shape == one and status.shape == one and starts.shape == (R + 1,)
+            and more.get_device() == table.get_device() == free.get_device() == n_free.get_device() == slots.get_device()
+            == starts.get_device() == lens_out.get_device() == n_free_out.get_device() == status.get_device() == dev
+            and lens.is_contiguous() and more.is_contiguous() and table.is_contiguous() and free.is_contiguous()
+            and slots.is_contiguous() and starts.is_contiguous() and lens_out.is_contiguous()):
+        for t, name, shape in ((lens, "lens", rows), (more, "more", rows), (table, "table", (R, width)), (free, "free", (size,)),
+                               (n_free, "n_free", one), (starts, "starts", (R + 1,)), (lens_out, "lens_out", rows),
+                               (n_free_out, "n_free_out", one), (status, "status", one)):
+            _ptr(t, name, i32, shape, dev)
+        _ptr(slots, "slots", _torch.int64, (n,), dev)
+    lens_p, n_free_p, lens_out_p, n_free_out_p = lens.data_ptr(), n_free.data_ptr(), lens_out.data_ptr(), n_free_out.data_ptr()
+    work = _plan_work(R, n, lens_out_p == lens_p or n_free_out_p == n_free_p)
     held = _workspace(work, i32, dev, stream) if work else None
-    _call("kv_plan_pages", dev, _ptr(lens, "lens", i32, (R,), dev), _ptr(more, "more", i32, (R,), dev), R,
-          _ptr(table, "table", i32, (R, width), dev), width, _ptr(free, "free", i32, free.shape, dev), free.shape[0],
-          _ptr(n_free, "n_free", i32, (1,), dev), page, _ptr(slots, "slots", _torch.int64, (n,), dev), n,
-          _ptr(starts, "starts", i32, (R + 1,), dev), _ptr(lens_out, "lens_out", i32, (R,), dev),
-          _ptr(n_free_out, "n_free_out", i32, (1,), dev), _ptr(status, "status", i32, (1,), dev),
+    _call("kv_plan_pages", dev, lens_p, more.data_ptr(), R, table.data_ptr(), width, free.data_ptr(), size, n_free_p, page,
+          slots.data_ptr(), n, starts.data_ptr(), lens_out_p, n_free_out_p, status.data_ptr(),
           held.data_ptr() if work else None, _stream_of(dev, stream))
 
 
@@ -233,7 +250,7 @@ def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=
     ``slots`` (int64 [N]) of the cache; tokens with a slot outside the cache (-1: padding)
     are not stored. They are of the cache's type or float32, for a float8_e4m3fn cache also
     bfloat16 or float16: each vector is then stored as max|x| / 448 and the nearest codes."""
-    c, dev, shape = _cache(k_cache, v_cache, k_scale, v_scale)
+    c, dev, shape, _ = _cache(k_cache, v_cache, k_scale, v_scale)
     kind = k.dtype
     if kind not in _codes:
         raise ValueError(f"k: {kind} is not supported")
@@ -242,8 +259,13 @@ def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=
     N, H, D = slots.shape[0], shape[1], shape[3]
     if N > _MAX:
         raise ValueError(f"slots: {N} are too many")
-    kp, k_row = _rows(k, "k", kind, (N, H, D), dev, H * D)
-    vp, v_row = _rows(v, "v", kind, (N, H, D), dev, H * D)
+    rows = (N, H, D)
+    if (v.dtype is kind and k.shape == rows and v.shape == rows and k.get_device() == v.get_device() == dev
+            and k.is_contiguous() and v.is_contiguous()):
+        kp, vp, k_row, v_row = k.data_ptr(), v.data_ptr(), H * D, H * D
+    else:
+        kp, k_row = _rows(k, "k", kind, rows, dev, H * D)
+        vp, v_row = _rows(v, "v", kind, rows, dev, H * D)
     _call("kv_append", dev, c, kp, vp, k_row, v_row, _codes[kind], _ptr(slots, "slots", _torch.int64, (N,), dev), N,
           _stream_of(dev, stream))
 
@@ -258,7 +280,7 @@ def kv_attend(q, k_cache, v_cache, table, lens, o, scale=None, window: int = 0, 
     int32 [R]: the stored tokens of each request, the new one's among them. ``scale``
     defaults to 1 / sqrt(D). A request without tokens has o = 0 and lse = -inf; one whose
     length or page ids are out of range has NaN."""
-    c, dev, shape = _cache(k_cache, v_cache, k_scale, v_scale)
+    c, dev, shape, code = _cache(k_cache, v_cache, k_scale, v_scale)
     kind = q.dtype
     if q.dim() != 3 or table.dim() != 2 or kind not in _codes:
         raise ValueError(f"q, table: expected [R, Hq, D] and [R, width], got {kind} {tuple(q.shape)}, {tuple(table.shape)}")
@@ -271,14 +293,18 @@ def kv_attend(q, k_cache, v_cache, table, lens, o, scale=None, window: int = 0, 
     if R > _MAX or Hq > _MAX or width > _MAX or not 0 <= window:
         raise ValueError(f"q, table, window: {tuple(q.shape)}, {tuple(table.shape)}, {window} are out of range")
     i32 = _torch.int32
-    tp, lp = _ptr(table, "table", i32, (R, width), dev), _ptr(lens, "lens", i32, (R,), dev)
-    op = _ptr(o, "o", kind, (R, Hq, D), dev)
+    if not (table.dtype is i32 and lens.dtype is i32 and o.dtype is kind and table.shape[0] == R and lens.shape == (R,)
+            and o.shape == (R, Hq, D) and table.get_device() == lens.get_device() == o.get_device() == dev
+            and table.is_contiguous() and lens.is_contiguous() and o.is_contiguous()):
+        _ptr(table, "table", i32, (R, width), dev)
+        _ptr(lens, "lens", i32, (R,), dev)
+        _ptr(o, "o", kind, (R, Hq, D), dev)
     lsep = None if lse is None else _ptr(lse, "lse", _torch.float32, (R, Hq), dev)
-    n = _attend_work(_codes[k_cache.dtype], pages, H, page, D, R, Hq, width)
+    n = _attend_work(code, pages, H, page, D, R, Hq, width)
     held = _workspace(n, _torch.uint8, dev, stream) if n else None
-    _call("kv_attend", dev, c, q.data_ptr(), q_row if R > 1 else 0, q_head if Hq > 1 else 0, _codes[kind], R, Hq, tp, width,
-          lp, D ** -0.5 if scale is None else scale, window if window < _MAX else 0, op, lsep,
-          held.data_ptr() if n else None, n, _stream_of(dev, stream))
+    _call("kv_attend", dev, c, q.data_ptr(), q_row if R > 1 else 0, q_head if Hq > 1 else 0, _codes[kind], R, Hq,
+          table.data_ptr(), width, lens.data_ptr(), D ** -0.5 if scale is None else scale, window if window < _MAX else 0,
+          o.data_ptr(), lsep, held.data_ptr() if n else None, n, _stream_of(dev, stream))
 
 
 def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, residual=None, residual_out=None,
@@ -299,19 +325,31 @@ def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, resi
     shape = N, D = x.shape
     if N > _MAX or D > _MAX:
         raise ValueError(f"x: {tuple(shape)} is too large")
-    xp, x_row = _rows(x, "x", kind, shape, dev, D)
-    rp = rop = None
-    r_row = ro_row = D
-    if residual is not None:
-        rp, r_row = _rows(residual, "residual", kind, shape, dev, D)
-        if residual_out is None:
-            rop, ro_row = rp, r_row
-        else:
-            rop, ro_row = _rows(residual_out, "residual_out", kind, shape, dev, D)
-    elif residual_out is not None:
-        raise ValueError("residual_out: there is no residual")
     groups = -(-D // group) if group > 0 else 1
-    cp, c_row = _rows(codes, "codes", _torch.float8_e4m3fn, shape, dev, D)
-    _call("norm_quant", dev, xp, x_row, rp, r_row, rop, ro_row,
-          None if weight is None else _ptr(weight, "weight", kind, (D,), dev), code, N, D, eps, group, cp, c_row,
-          _ptr(scales, "scales", _torch.float32, (N, groups), dev), _stream_of(dev, stream))
+    f8, f32 = _torch.float8_e4m3fn, _torch.float32
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out: there is no residual")
+        r, out = x, x                     # (checked with x, not passed)
+    else:
+        r, out = residual, residual if residual_out is None else residual_out
+    w = x if weight is None else weight
+    if (r.dtype is kind and out.dtype is kind and w.dtype is kind and codes.dtype is f8 and scales.dtype is f32
+            and r.shape == shape and out.shape == shape and codes.shape == shape and scales.shape == (N, groups)
+            and (w is x or w.shape == (D,))
+            and r.get_device() == out.get_device() == w.get_device() == codes.get_device() == scales.get_device() == dev
+            and x.is_contiguous() and r.is_contiguous() and out.is_contiguous() and w.is_contiguous()
+            and codes.is_contiguous() and scales.is_contiguous()):
+        x_row = r_row = ro_row = c_row = D
+    else:
+        x_row = _rows(x, "x", kind, shape, dev, D)[1]
+        r_row = _rows(r, "residual", kind, shape, dev, D)[1]
+        ro_row = _rows(out, "residual_out", kind, shape, dev, D)[1]
+        c_row = _rows(codes, "codes", f8, shape, dev, D)[1]
+        if w is not x:
+            _ptr(w, "weight", kind, (D,), dev)
+        _ptr(scales, "scales", f32, (N, groups), dev)
+    have = residual is not None
+    _call("norm_quant", dev, x.data_ptr(), x_row, r.data_ptr() if have else None, r_row, out.data_ptr() if have else None,
+          ro_row, None if weight is None else w.data_ptr(), code, N, D, eps, group, codes.data_ptr(), c_row,
+          scales.data_ptr(), _stream_of(dev, stream))

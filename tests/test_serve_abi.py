@@ -114,8 +114,8 @@ def test_attend_workspace(lib):
     """Two segments of 16 rows of D sums, their maximum and weight sum for each workgroup,
     and a first unit for each request and the end."""
     n = ctypes.c_size_t()
-    for R, Hq, H, width, D, groups in ((1, 32, 8, 8192, 128, 768), (256, 32, 4, 512, 128, 768), (3, 40, 2, 9, 64, 3 * 2 * 2 * 2),
-                                       (65536, 1, 1, 100, 64, 1024), (2, 8, 8, 4096, 256, 256)):
+    for R, Hq, H, width, D, groups in ((1, 32, 8, 8192, 128, 512), (256, 32, 4, 512, 128, 512), (3, 40, 2, 9, 64, 3 * 2 * 2 * 2),
+                                       (65536, 1, 1, 100, 64, 768), (2, 8, 8, 4096, 256, 256)):
         assert lib.kv_attend_work(cache(H=H, D=D), R, Hq, width, n) == OK
         blocks = H * -(-(Hq // H) // 16)
         groups = min(groups, R * blocks * -(-width * 16 // 128))
@@ -135,7 +135,9 @@ def test_append_refusals(lib):
 
 
 def test_plan_and_release_refusals(lib):
-    assert lib.kv_plan_work(64, 64) == 0 and lib.kv_plan_work(64, 1 << 20) == 64 and lib.kv_plan_work(5000, 64) == 5000
+    for in_place in (0, 1):
+        assert lib.kv_plan_work(64, 64, in_place) == 0 and lib.kv_plan_work(5000, 64, in_place) == 5000
+    assert lib.kv_plan_work(64, 1 << 20, 1) == 64 and lib.kv_plan_work(64, 1 << 20, 0) == 0
 
     def plan(lens=A, more=A, R=4, table=A, width=8, free=A, free_size=9, n_free=A, page=16, slots=A, n_slots=4, starts=A,
              lens_out=A, n_free_out=A, status=A, work=None):
