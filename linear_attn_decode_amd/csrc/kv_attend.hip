@@ -110,10 +110,15 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     }
 }
 
-// Wavefronts a SIMD holds, which is workgroups a compute unit holds: what the registers of a
-// tile in flight leave room for (256 columns of 16 bits take more than half of them)
+// Wavefronts a SIMD holds, which is workgroups a compute unit holds. 16 KB of tile in flight a
+// wavefront saturate HBM with one each (64 ragged requests of 128 columns: 74.4 us with one,
+// 76.3 with two, 93 with three, which spills); smaller tiles want more of them (64 columns:
+// 21.9 us with three, 22.8 with two, 27.8 with one; e4m3 at 128 columns: 153 us with two, 177
+// with one, whose conversions nothing overlaps).
 constexpr int waves_per_simd(int kv, int qt, int D) {
-    return D == 64 ? 3 : D == 128 ? 2 : kv == WB_E4M3 && qt == WB_BF16 ? 2 : 1;
+    if (D == 64) return 3;
+    if (kv == WB_E4M3) return D == 128 || qt == WB_BF16 ? 2 : 1;
+    return 1;
 }
 
 // A place in a run: turn `turn` of request r for block of heads hb
