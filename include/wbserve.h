@@ -93,7 +93,8 @@ int kv_release_pages(const uint8_t* ended, int32_t* lens, int R, const int32_t* 
  * scale = max|x| / 448 (2^-126 at least) and code = e4m3(x / scale), to nearest with ties to
  * the even code; a vector of zeros has scale 0, one that holds a NaN or an infinity reads
  * back as NaN. Slots
- * given twice in one call end up with one of the two tokens. Rows 16-byte aligned. */
+ * given twice in one call end up with one of the two tokens. Rows 16-byte aligned; N * H
+ * below 2^31. */
 int kv_append(const wb_kv_cache* c, const void* k, const void* v, int64_t k_row, int64_t v_row, int src,
               const int64_t* slots, int N, void* stream);
 

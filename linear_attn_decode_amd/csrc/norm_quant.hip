@@ -5,7 +5,10 @@
 // and every output written once; HBM bounds it (a single row: the launch). The 128 columns
 // of a group are 16 neighbouring lanes of one chunk, so a group's maximum is four DPP steps.
 // Rows of up to 512 columns take 16, 32 or 64 lanes, several rows a wavefront; wider ones a
-// workgroup of as many wavefronts as their chunks need. Strides and alignment are free: the
+// workgroup of as many wavefronts as their chunks need, two chunks a lane (8191 rows of 5000
+// bfloat16 columns with a residual: 60.1 us, 4.79 TB/s, the rate of a copy; 66.5 us with one
+// chunk, 63.0 with three, 72.1 with four; 56.8 us with stores past the caches, which cost the
+// kernel that reads them next 7 us). Strides and alignment are free: the
 // 16-byte accesses need only the element's alignment on this hardware, and the chunk that
 // holds a row's ragged end goes by single elements.
 #include "serve_device.hpp"

@@ -121,7 +121,7 @@ int kv_append(const wb_kv_cache* c, const void* k, const void* v, int64_t k_row,
     if (src == WB_E4M3) return WB_EUNSUPPORTED;
     if (N == 0) return WB_OK;
     if (!k || !v || !slots) return WB_EINVAL;
-    if (int64_t(N) * c->H * (c->D / 8) > (int64_t(1) << 38)) return WB_EUNSUPPORTED;      // (grid size)
+    if (int64_t(N) * c->H > 0x7FFFFFFF) return WB_EUNSUPPORTED;
     const int64_t row = int64_t(c->H) * c->D;
     if (N > 1 && (k_row < row || v_row < row)) return WB_EINVAL;
     const int size = element_size(src);

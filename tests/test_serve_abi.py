@@ -130,7 +130,7 @@ def test_append_refusals(lib):
     for kw, code in [(dict(N=-1), EINVAL), (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(slots=None), EINVAL),
                      (dict(src=9), EINVAL), (dict(src=serve.F16), EUNSUPPORTED), (dict(src=serve.E4M3), EUNSUPPORTED),
                      (dict(c=e, src=serve.E4M3), EUNSUPPORTED), (dict(k_row=511), EINVAL), (dict(v_row=0), EINVAL),
-                     (dict(k_row=516), EALIGN), (dict(v=A + 4), EALIGN), (dict(slots=A + 4), EALIGN)]:
+                     (dict(k_row=516), EALIGN), (dict(N=1 << 30), EUNSUPPORTED), (dict(v=A + 4), EALIGN), (dict(slots=A + 4), EALIGN)]:
         assert call(**kw) == code, kw
 
 
