@@ -112,7 +112,7 @@ int kv_append(const wb_kv_cache* c, const void* k, const void* v, int64_t k_row,
  * q [R][Hq][D] of type q_dtype (the cache's, or WB_BF16 / WB_F16 for an 8-bit cache), strides
  * q_row and q_head in elements, multiples of 8; o [R][Hq][D] contiguous, of q's type; table
  * int32 [R][width]; lens int32 [R]. `work` has kv_attend_work() bytes (NULL if 0), 16-byte
- * aligned, and belongs to the call until it has run. 1 <= R <= 65536, Hq a multiple of
+ * aligned, whatever they hold, and belongs to the call until it has run. 1 <= R <= 65536, Hq a multiple of
  * H and at most 4096, width * page at most 2^30. */
 int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head, int q_dtype, int R, int Hq,
               const int32_t* table, int width, const int32_t* lens, float scale, int window, void* o, float* lse,

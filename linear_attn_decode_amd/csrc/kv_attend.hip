@@ -26,8 +26,9 @@
 // from the lengths on the device, so that ragged batches and single long requests fill the
 // card alike and captured graphs keep working as lengths grow. A run may cover several
 // segments (all turns, or the rest, or the first of a request's block). Segments that are
-// whole are finished by their workgroup; the others, at most two a workgroup, leave their
-// sums in the caller's workspace for a second, small launch.
+// whole are finished by their workgroup; the others, at most two a workgroup, leave their sums
+// in the caller's workspace, where the workgroup that stores a segment's last part, or a
+// second launch, joins them in the order of the cache: results do not depend on timing.
 #include "serve_device.hpp"
 
 namespace wb {
@@ -67,6 +68,7 @@ struct Run {
     int64_t total, from, to;        // all units; this workgroup's
     int64_t start;                  // first unit of request r
     int r;                          // the request of unit `from`
+    int n;                          // workgroups with work
 };
 
 __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
@@ -87,7 +89,7 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     const int64_t upto = wave_scan(mine);
     Run s;
     s.total = lane64(upto, 63) * A.head_blocks;
-    const int n = int(s.total < gridDim.x ? s.total : int64_t(gridDim.x));
+    const int n = s.n = int(s.total < gridDim.x ? s.total : int64_t(gridDim.x));
     s.r = 0;
     s.from = s.to = s.start = 0;
     if (int(blockIdx.x) >= n) return s;
@@ -205,7 +207,86 @@ __device__ __forceinline__ void finish(const AttendArgs& A, f32x4 v, float l, fl
     if (A.lse && col == 0) A.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
 }
 
-template <int KV, int QT, int D>
+// The parts that units [from, to) of one request and block were computed in: `count` (1: they
+// were finished by their workgroup) in the slots at(c) of the workspace.
+struct Parts {
+    int64_t first;
+    int w0, count;
+    __device__ __forceinline__ Parts(int64_t total, int64_t n, int64_t from, int64_t to) {
+        w0 = int(run_of(total, from, n));
+        count = int(run_of(total, to - 1, n)) - w0 + 1;
+        first = 2 * int64_t(w0) + (run_start(total, w0, n) != from);
+    }
+    __device__ __forceinline__ size_t at(int c) const { return size_t(c ? 2 * (int64_t(w0) + c) : first); }
+};
+__device__ __forceinline__ Parts parts_of(const AttendArgs& A, int r, int hb) {
+    const int64_t total = A.spans[A.R], start = A.spans[r], end = r + 1 < A.R ? A.spans[r + 1] : total;
+    const int64_t turns = quotient64(end - start, A.head_blocks);
+    return Parts(total, total < A.groups ? total : A.groups, start + hb * turns, start + (hb + 1) * turns);
+}
+
+// Parts that are joined HERE, in the launch that stores them, are stored and loaded at the
+// card's scope, past the caches that its compute dies do not share: a wavefront whose stores
+// have completed then needs no write-back of its die's cache before others may read them, nor
+// they an invalidation of theirs. (With fences, which do both for the whole cache, the batch of
+// 64 ragged requests takes 180 us, not 73.)
+template <bool HERE>
+__device__ __forceinline__ void put_part(float* p, f32x2 v) {
+    if constexpr (HERE)
+        __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    else
+        *reinterpret_cast<f32x2*>(p) = v;
+}
+template <bool HERE>
+__device__ __forceinline__ f32x2 get_part(const float* p) {
+    if constexpr (!HERE) return *reinterpret_cast<const f32x2*>(p);
+    return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                                       __HIP_MEMORY_SCOPE_AGENT));
+}
+__device__ __forceinline__ void stores_complete() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Whether this is the last of `count` workgroups to come here. The counter needs no clearing:
+// it holds the call's tag above its 12 bits of count, whoever finds another tag there puts
+// the call's with a count of 0 (one exchange; it fails only where another workgroup's has
+// succeeded), and the last one takes the tag out again, so that a replay of a captured call,
+// which has the same tag, starts over. Nothing waits here.
+constexpr int kCountBits = 12;
+__device__ __forceinline__ bool last_to_arrive(uint64_t* c, uint64_t tag, int count) {
+    uint64_t v = __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (v >> kCountBits != tag)
+        __hip_atomic_compare_exchange_strong(c, &v, tag << kCountBits, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+    v = __hip_atomic_fetch_add(c, uint64_t(1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = int(v & ((1u << kCountBits) - 1)) + 1 == count;
+    if (last) __hip_atomic_store(c, uint64_t(0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return last;
+}
+
+// 4 columns of head h of a joined row, in one pass with a running maximum: a part's sums are
+// requested with its maximum
+template <int QT, int D, bool HERE>
+__device__ __forceinline__ void join_columns(const AttendArgs& A, const Parts& parts, int h, int col, size_t row) {
+    float m = -INFINITY, l = 0.f;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int c = 0; c < parts.count; ++c) {
+        const size_t at = parts.at(c) * 16 + h;
+        const f32x2 ml = get_part<HERE>(A.part_ml + 2 * at), v0 = get_part<HERE>(A.part_o + at * D + col),
+                    v1 = get_part<HERE>(A.part_o + at * D + col + 2);
+        const float mc = ml[0], lc = ml[1];
+        const f32x4 vc = {v0[0], v0[1], v1[0], v1[1]};
+        const float top = fmaxf(m, mc), ref = top == -INFINITY ? 0.f : top;
+        const float f = __builtin_amdgcn_exp2f(m - ref), fc = __builtin_amdgcn_exp2f(mc - ref);
+        l = l * f + lc * fc;
+        v = v * f + vc * fc;
+        m = top;
+    }
+    finish<QT>(A, v, l, m, row, D, col);
+}
+
+// JOINS: the workgroup that comes last joins a split segment (else a second launch does)
+template <int KV, int QT, int D, bool JOINS>
 __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_kernel(const AttendArgs A) {
     using T = Attend<KV, QT, D>;
     using M = typename T::M;
@@ -213,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
     __shared__ float sums[kWaves][16][LD];
     __shared__ float stat_m[kWaves][16], stat_l[kWaves][16];
     __shared__ int bad_page[kWaves];
+    __shared__ int is_last;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int head = lane & 15, g = lane >> 4;
@@ -220,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
     const int page_mask = (1 << A.page_log2) - 1;
     const float mul = A.scale * kLog2e;
     const Run run = find_run(A);
-    if (A.spans && blockIdx.x == 0 && tid == 0) A.spans[A.R] = run.total;
+    if (!JOINS && A.spans && blockIdx.x == 0 && tid == 0) A.spans[A.R] = run.total;
     if (run.from == run.to) return;
 
     // The run as a sequence of turns. Three places of it are in work at a time: the turn that
@@ -353,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
             const int n = cur.n, base = cur.from + cur.turn * kTurn + wave * kTile;
             const int seen = A.window && n > A.window ? n - A.window : 0;     // first token that counts
             const bool new_block = next.hb != cur.hb || next.r != cur.r;
-            if (A.spans && cur.hb == 0 && cur.turn == 0 && tid == 0) A.spans[cur.r] = run.from + k;
+            if (!JOINS && A.spans && cur.hb == 0 && cur.turn == 0 && tid == 0) A.spans[cur.r] = run.from + k;
 
             // scores: s[t][i] of token base + 8 g + 4 t + i
             f32x4 s[2];
@@ -518,10 +600,24 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
             finish<QT>(A, v, ll, mm, size_t(r) * A.Hq + head0 + h, D, d);
         } else {
             const size_t at = size_t(slot) * 16 + h;
-            *reinterpret_cast<f32x4*>(A.part_o + at * D + d) = v;
-            if (d == 0) {
-                A.part_ml[2 * at] = mm;
-                A.part_ml[2 * at + 1] = ll;
+            put_part<JOINS>(A.part_o + at * D + d, f32x2{v[0], v[1]});
+            put_part<JOINS>(A.part_o + at * D + d + 2, f32x2{v[2], v[3]});
+            if (d == 0) put_part<JOINS>(A.part_ml + 2 * at, f32x2{mm, ll});
+        }
+    }
+
+    if (JOINS && !alone) {
+        // the workgroup that stores the last part of a segment joins it
+        stores_complete();
+        __syncthreads();
+        const int64_t unit0 = run.from + k - cur.turn;
+        const Parts parts(run.total, run.n, unit0, unit0 + cur.turns);
+        if (tid == 0) is_last = last_to_arrive(A.arrivals + parts.w0, A.tag, parts.count);
+        __syncthreads();
+        if (is_last) {
+            for (int e = tid; e < heads * (D / 4); e += kThreads) {
+                const int h = e / (D / 4), d = e - h * (D / 4);
+                join_columns<QT, D, true>(A, parts, h, 4 * d, size_t(r) * A.Hq + head0 + h);
             }
         }
     }
@@ -538,22 +634,6 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
     }
 }
 
-// The unfinished segments of a request's block of heads: `count` (1: it was finished) in the
-// slots at(c) of the workspace.
-struct Parts {
-    int64_t first;
-    int w0, count;
-    __device__ __forceinline__ Parts(const AttendArgs& A, int r, int hb) {
-        const int64_t total = A.spans[A.R], start = A.spans[r], end = r + 1 < A.R ? A.spans[r + 1] : total;
-        const int64_t turns = quotient64(end - start, A.head_blocks), a = start + hb * turns;
-        const int64_t n = total < A.groups ? total : A.groups;
-        w0 = int(run_of(total, a, n));
-        count = int(run_of(total, a + turns - 1, n)) - w0 + 1;
-        first = 2 * int64_t(w0) + (run_start(total, w0, n) != a);
-    }
-    __device__ __forceinline__ size_t at(int c) const { return size_t(c ? 2 * (int64_t(w0) + c) : first); }
-};
-
 // Joins the segments of a request. Few requests (which may have hundreds each): a workgroup
 // per (request, query head, 64 columns), 16 lanes across the columns and 16 along the
 // segments, whose factors are worked out once in LDS.
@@ -568,7 +648,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_long_kernel(const AttendArg
     const int tid = threadIdx.x;
     const int r = blockIdx.x, h = blockIdx.y;
     const int kvh = h / A.G, in_kv = h - kvh * A.G;
-    const Parts parts(A, r, kvh * (A.head_blocks / A.c.H) + in_kv / 16);
+    const Parts parts = parts_of(A, r, kvh * (A.head_blocks / A.c.H) + in_kv / 16);
     const int count = parts.count, in_block = in_kv & 15;
     if (count == 1) return;
 
@@ -615,35 +695,24 @@ __global__ void __launch_bounds__(kJoinThreads) join_long_kernel(const AttendArg
 template <int QT, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) {
     const int r = blockIdx.x / A.head_blocks, hb = blockIdx.x - r * A.head_blocks;
-    const Parts parts(A, r, hb);
-    const int count = parts.count;
-    if (count == 1) return;
+    const Parts parts = parts_of(A, r, hb);
+    if (parts.count == 1) return;
     const int blocks_of_kv = A.head_blocks / A.c.H;
     const int kvh = hb / blocks_of_kv, qb = hb - kvh * blocks_of_kv;
     const int heads = min(16, A.G - 16 * qb);
     for (int e = threadIdx.x; e < heads * (D / 4); e += kJoinThreads) {
         const int h = e / (D / 4), d = e - h * (D / 4);
-        // in one pass with a running maximum: a segment's sums are requested with its maximum
-        float m = -INFINITY, l = 0.f;
-        f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int c = 0; c < count; ++c) {
-            const size_t at = parts.at(c) * 16 + h;
-            const float mc = A.part_ml[2 * at], lc = A.part_ml[2 * at + 1];
-            const f32x4 vc = *reinterpret_cast<const f32x4*>(A.part_o + at * D + 4 * d);
-            const float top = fmaxf(m, mc), ref = top == -INFINITY ? 0.f : top;
-            const float f = __builtin_amdgcn_exp2f(m - ref), fc = __builtin_amdgcn_exp2f(mc - ref);
-            l = l * f + lc * fc;
-            v = v * f + vc * fc;
-            m = top;
-        }
-        finish<QT>(A, v, l, m, size_t(r) * A.Hq + kvh * A.G + 16 * qb + h, D, 4 * d);
+        join_columns<QT, D, false>(A, parts, h, 4 * d, size_t(r) * A.Hq + kvh * A.G + 16 * qb + h);
     }
 }
 
 template <int KV, int QT, int D>
 hipError_t attend_d(const AttendArgs& a, hipStream_t s) {
-    attend_kernel<KV, QT, D><<<a.groups, kThreads, 0, s>>>(a);
+    if (a.arrivals) {
+        attend_kernel<KV, QT, D, true><<<a.groups, kThreads, 0, s>>>(a);
+        return hipGetLastError();
+    }
+    attend_kernel<KV, QT, D, false><<<a.groups, kThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.spans) return e;
     if (int64_t(a.R) * a.Hq * (D / kJoinCols) <= kLongWorkgroups)
@@ -663,6 +732,14 @@ hipError_t attend_t(const AttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
+// A request's block may get all workgroups but one for each other block, and the one that comes
+// last joins their parts; above kPartsJoined of them (few key-value heads, small tiles) that
+// costs more than a second launch of many workgroups. 32 query and 8 key-value heads of 128
+// columns, joined by the last workgroup / by a second launch: 1 request of 237 tokens 9.3 / 11.7
+// us, 8 to 512 tokens 9.9 / 12.2, 32 to 1024 18.1 / 22.6, 64 to 4096 74.0 / 74.5, 1 of 8000 (32
+// parts) 14.0 / 13.4; 4 key-value heads of 256 columns, 1 of 8000 (64 parts): 53 / 16.
+constexpr int kPartsJoined = 32;
+
 // As many workgroups as the card's 256 compute units hold at once, and no more than all
 // requests at full width have units.
 AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width, int q_dtype) {
@@ -673,12 +750,15 @@ AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width, int q_dty
     const int64_t turns = (int64_t(width) * c.page + kTurn - 1) / kTurn;
     const int64_t most = int64_t(R) * turns * p.head_blocks;
     p.groups = int(most < 256 * per_cu ? most : 256 * per_cu);
-    p.part_o_bytes = p.part_ml_bytes = p.spans_bytes = 0;
+    p.part_o_bytes = p.part_ml_bytes = p.spans_bytes = p.arrivals_bytes = 0;
+    p.joins_itself = false;
     if (turns > 1) {
         const size_t rows = size_t(p.groups) * 2 * 16;
         p.part_o_bytes = rows * c.D * 4;
         p.part_ml_bytes = rows * 8;
         p.spans_bytes = (size_t(R) + 1) * 8;
+        p.arrivals_bytes = size_t(p.groups) * 8;
+        p.joins_itself = p.groups <= kPartsJoined * p.head_blocks;
     }
     return p;
 }

@@ -58,7 +58,10 @@ struct AttendArgs {
     float* lse = nullptr;
     float* part_o = nullptr;      // [groups][2][16][D] sums of unfinished segments
     float* part_ml = nullptr;     // [groups][2][16][2] their maximum and weight sum
-    int64_t* spans = nullptr;     // [R + 1] first unit of each request, all units
+    int64_t* spans = nullptr;     // [R + 1] first unit of each request, all units (for a second launch)
+    uint64_t* arrivals = nullptr; // [groups] workgroups that stored a part of the segment that begins in
+                                  // a workgroup's run and goes on behind it (or null: a second launch joins)
+    uint64_t tag = 0;             // of this call, 52 bits, not 0
     float scale = 0.f;
     int R = 0, Hq = 0, width = 0, window = 0, q_dtype = 0, page_log2 = 0;
     int G = 1;                    // query heads of a key-value head
@@ -67,7 +70,8 @@ struct AttendArgs {
 };
 struct AttendPlan {
     int head_blocks, groups;
-    size_t part_o_bytes, part_ml_bytes, spans_bytes;     // all 0: no request can take two turns
+    size_t part_o_bytes, part_ml_bytes, spans_bytes, arrivals_bytes;     // all 0: no request can take two turns
+    bool joins_itself;                                   // the workgroups join what they split
 };
 AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width, int q_dtype);
 hipError_t launch_attend(const AttendArgs& a, hipStream_t stream);

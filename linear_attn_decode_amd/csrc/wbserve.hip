@@ -1,5 +1,10 @@
 // Host side of the serving operators' C ABI (include/wbserve.h): argument checks and
 // dispatch. No device memory is allocated and nothing is kept between calls.
+#include <time.h>
+#include <unistd.h>
+
+#include <atomic>
+
 #include "serve_kernels.hpp"
 
 namespace {
@@ -46,7 +51,27 @@ int check_attend(const wb_kv_cache* c, int R, int Hq, int width) {
     return Hq > kMaxQueryHeads ? WB_EUNSUPPORTED : WB_OK;
 }
 
-size_t work_bytes_of(const wb::AttendPlan& p) { return p.part_o_bytes + p.part_ml_bytes + p.spans_bytes; }
+size_t work_bytes_of(const wb::AttendPlan& p) {
+    return p.part_o_bytes + p.part_ml_bytes + p.spans_bytes + p.arrivals_bytes;
+}
+
+// A call's tag, 52 bits: successive numbers from a start of the process's own, scrambled
+// (SplitMix64's finaliser; Steele, Lea, Flood, OOPSLA 2014), so that whatever the workspace
+// held before is the call's own tag with probability 2^-52.
+uint64_t next_tag() {
+    static std::atomic<uint64_t> next{[] {
+        timespec t{};
+        clock_gettime(CLOCK_REALTIME, &t);
+        return uint64_t(t.tv_sec) * 1000000007u + uint64_t(t.tv_nsec) + (uint64_t(getpid()) << 40);
+    }()};
+    for (;;) {
+        uint64_t z = next.fetch_add(1, std::memory_order_relaxed) * 0x9E3779B97F4A7C15ull;
+        z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+        z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+        z = (z ^ (z >> 31)) >> 12;
+        if (z) return z;
+    }
+}
 
 }  // namespace
 
@@ -180,7 +205,13 @@ int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head
         uint8_t* w = static_cast<uint8_t*>(work);
         a.part_o = reinterpret_cast<float*>(w);
         a.part_ml = reinterpret_cast<float*>(w + p.part_o_bytes);
-        a.spans = reinterpret_cast<int64_t*>(w + p.part_o_bytes + p.part_ml_bytes);
+        w += p.part_o_bytes + p.part_ml_bytes;
+        if (p.joins_itself) {
+            a.arrivals = reinterpret_cast<uint64_t*>(w + p.spans_bytes);
+            a.tag = next_tag();
+        } else {
+            a.spans = reinterpret_cast<int64_t*>(w);
+        }
     }
     a.scale = scale;
     a.R = R;

@@ -678,6 +678,42 @@ def test_calls_on_two_streams_do_not_disturb_each_other():
             assert torch.equal(o, want)
 
 
+@pytest.mark.parametrize("D,H", [(128, 4), (64, 2), (256, 4)])
+def test_attend_workspace_may_hold_anything(D, H):
+    """The same call with workspaces of zeros, ones, noise and what earlier calls (also of other
+    sizes) left there: equal results."""
+    import linear_attn_decode_amd as wb
+    from linear_attn_decode_amd import serve as S
+    g = torch.Generator().manual_seed(9)
+    page, width, R = 16, 60, 7
+    k, v = (rand(g, R * width, H, page, D, dtype="bf16").cuda() for _ in range(2))
+    table = torch.randperm(R * width, generator=g).int().view(R, width).cuda()
+    q = rand(g, R, 4 * H, D, dtype="bf16").cuda()
+    all_lens = [[960, 5, 0, 700, 31, 128, 400], [1, 2, 3, 4, 5, 6, 7], [960] * 7]
+    want = []
+    for lens in all_lens:
+        o = torch.empty_like(q)
+        wb.kv_attend(q, k, v, table, torch.tensor(lens, dtype=torch.int32).cuda(), o)
+        want.append(o)
+    torch.cuda.synchronize()
+    c, dev, shape, code = S._cache(k, v, None, None)
+    n = S._attend_work(code, *shape, R, 4 * H, width)
+    assert n > 0
+    work = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for fill in (0, 255, None, "left", "left"):
+        if fill is None:
+            work.copy_(torch.randint(0, 256, (n,), generator=g, dtype=torch.uint8))
+        elif fill != "left":
+            work.fill_(fill)
+        for lens, o_want in zip(all_lens, want):
+            o = torch.zeros_like(q)
+            ln = torch.tensor(lens, dtype=torch.int32).cuda()
+            S._call("kv_attend", dev, c, q.data_ptr(), 4 * H * D, D, code, R, 4 * H, table.data_ptr(), width, ln.data_ptr(),
+                    D ** -0.5, 0, o.data_ptr(), None, work.data_ptr(), n, S._stream_of(dev, None))
+            torch.cuda.synchronize()
+            assert torch.equal(o, o_want), (fill, lens)
+
+
 def test_binding_refusals():
     import linear_attn_decode_amd as wb
     cu = lambda *a, **kw: torch.zeros(*a, device="cuda", **kw)

@@ -112,14 +112,14 @@ def test_attend_runs_and_segments(groups, seed):
 
 def test_attend_workspace(lib):
     """Two segments of 16 rows of D sums, their maximum and weight sum for each workgroup,
-    and a first unit for each request and the end."""
+    a first unit for each request and the end, a counter for each workgroup."""
     n = ctypes.c_size_t()
     for R, Hq, H, width, D, groups in ((1, 32, 8, 8192, 128, 256), (256, 32, 4, 512, 128, 256), (3, 40, 2, 9, 64, 3 * 2 * 2 * 2),
                                        (65536, 1, 1, 100, 64, 768), (2, 8, 8, 4096, 256, 256)):
         assert lib.kv_attend_work(cache(H=H, D=D), R, Hq, width, n) == OK
         blocks = H * -(-(Hq // H) // 16)
         groups = min(groups, R * blocks * -(-width * 16 // 128))
-        assert n.value == groups * 2 * 16 * (4 * D + 8) + 8 * (R + 1)
+        assert n.value == groups * 2 * 16 * (4 * D + 8) + 8 * (R + 1) + 8 * groups
 
 
 def test_append_refusals(lib):
