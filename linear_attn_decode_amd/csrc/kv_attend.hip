@@ -291,9 +291,12 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
     using T = Attend<KV, QT, D>;
     using M = typename T::M;
     constexpr int KQ = T::KQ, VB = T::VB, VN = T::VN, LD = T::LD;
-    __shared__ float sums[kWaves][16][LD];
-    __shared__ float stat_m[kWaves][16], stat_l[kWaves][16];
-    __shared__ int bad_page[kWaves];
+    // Two sets of a segment's sums where they fit, taken in turn: a wavefront may store the next
+    // segment's while others read this one's, and one barrier a segment is enough.
+    constexpr int kSets = D == 256 && waves_per_simd(KV, QT, D) == 2 ? 1 : 2;
+    __shared__ float sums_[kSets][kWaves][16][LD];
+    __shared__ float stat_m_[kSets][kWaves][16], stat_l_[kSets][kWaves][16];
+    __shared__ int bad_page_[kSets][kWaves];
     __shared__ int is_last;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -429,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
     };
     clear();
     bool first_segment = true;
+    int set = 0;
     int t0 = cur.turn;                                          // of the segment
 
     for (int64_t k = 0; k < units; ++k) {
@@ -547,24 +551,24 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
 
             const bool last_turn = cur.turn + 1 == cur.turns;
             if (last_turn || k + 1 == units) {
-    // end of a segment: join the wavefronts, everything relative to the workgroup's maximum
+    // end of a segment: join the wavefronts
     const bool alone = t0 == 0 && last_turn;
     const int slot = 2 * int(blockIdx.x) + !first_segment;      // of its sums, if it is not whole
     const int r = cur.r, kvh = cur.kvh, qb = cur.hb - kvh * blocks_of_kv;
     const int heads = min(16, A.G - 16 * qb), head0 = kvh * A.G + 16 * qb;
     l = add_xor32_f32(add_xor16_f32(l));
-    if (!first_segment) __syncthreads();                        // (the last segment's have been read)
+    if (kSets == 1 && !first_segment) __syncthreads();          // (the last segment's have been read)
+    auto& sums = sums_[set];
+    auto& stat_m = stat_m_[set];
+    auto& stat_l = stat_l_[set];
+    auto& bad_page = bad_page_[set];
+    set = kSets - 1 - set;
     if (g == 0) {
         stat_m[wave][head] = m;
         stat_l[wave][head] = l;
     }
     const int any_bad = __any(bad_here);
     if (lane == 0) bad_page[wave] = any_bad;
-    __syncthreads();
-    float M_ = stat_m[0][head];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) M_ = fmaxf(M_, stat_m[w][head]);
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - M_);
     if (head < heads) {
 #pragma unroll
         for (int vn = 0; vn < VN; ++vn)
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
                 for (int c = 0; c < VB; c += 4) {
                     f32x4 v;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = acc[vn * VB + c + e][i] * f;
+                    for (int e = 0; e < 4; ++e) v[e] = acc[vn * VB + c + e][i];
                     *reinterpret_cast<f32x4*>(&sums[wave][head][vn * 16 * VB + (4 * g + i) * VB + c]) = v;
                 }
     }
@@ -592,8 +596,9 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            v += *reinterpret_cast<const f32x4*>(&sums[w][h][d]);
-            ll += stat_l[w][h] * __builtin_amdgcn_exp2f(stat_m[w][h] - ref);
+            const float f = __builtin_amdgcn_exp2f(stat_m[w][h] - ref);
+            v += *reinterpret_cast<const f32x4*>(&sums[w][h][d]) * f;
+            ll += stat_l[w][h] * f;
         }
         if (poison) ll = __builtin_nanf("");
         if (alone) {
