@@ -92,9 +92,8 @@ int kv_release_pages(const uint8_t* ended, int32_t* lens, int R, const int32_t* 
  * WB_F32 (rounded to nearest), for an 8-bit cache also WB_BF16 or WB_F16: then
  * scale = max|x| / 448 (2^-126 at least) and code = e4m3(x / scale), to nearest with ties to
  * the even code; a vector of zeros has scale 0, one that holds a NaN or an infinity reads
- * back as NaN. Slots
- * given twice in one call end up with one of the two tokens. Rows 16-byte aligned; N * H
- * below 2^31. */
+ * back as NaN. A slot is given at most once in a call (kv_plan_pages gives none twice): one
+ * that is given twice holds a mixture of its tokens. Rows 16-byte aligned; N * H below 2^31. */
 int kv_append(const wb_kv_cache* c, const void* k, const void* v, int64_t k_row, int64_t v_row, int src,
               const int64_t* slots, int N, void* stream);
 
@@ -106,14 +105,15 @@ int kv_append(const wb_kv_cache* c, const void* k, const void* v, int64_t k_row,
  * Scores, maxima and sums are float32, the weights e^{s_t - max} enter the product with v as
  * two 16-bit limbs, o is rounded once. A request without tokens, or whose scores are all
  * -infinity, has o = 0 and lse = -infinity. Stored values outside the range are not used,
- * whatever they hold; a NaN or an infinity inside it gives values that are not finite. A
+ * whatever they hold; a NaN inside it gives NaN, an infinity what the formula gives or NaN. A
  * request with a length outside [0, width * page], or a page id outside [0, pages) in the
- * range it reads, has o = lse = NaN.
+ * range it reads, has o = lse = NaN. Results do not depend on timing: equal calls give equal
+ * bits.
  * q [R][Hq][D] of type q_dtype (the cache's, or WB_BF16 / WB_F16 for an 8-bit cache), strides
  * q_row and q_head in elements, multiples of 8; o [R][Hq][D] contiguous, of q's type; table
  * int32 [R][width]; lens int32 [R]. `work` has kv_attend_work() bytes (NULL if 0), 16-byte
- * aligned, whatever they hold, and belongs to the call until it has run. 1 <= R <= 65536, Hq a multiple of
- * H and at most 4096, width * page at most 2^30. */
+ * aligned, whatever they hold, and belongs to the call until it has run. No output overlaps
+ * an input. 1 <= R <= 65536, Hq a multiple of H and at most 4096, width * page at most 2^30. */
 int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head, int q_dtype, int R, int Hq,
               const int32_t* table, int width, const int32_t* lens, float scale, int window, void* o, float* lse,
               void* work, size_t work_bytes, void* stream);

@@ -78,7 +78,8 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
 
 // This workgroup's run (from == to: none), by every wavefront for itself: lane l sums the
 // turns of requests [l R / 64, (l + 1) R / 64), one scan finds the lane whose requests hold
-// the run's first unit, another the request among them.
+// the run's first unit, another the request among them. (Lengths that change under a call give
+// wrong results, but every index stays inside: places are clamped.)
 __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     const int lane = threadIdx.x & 63;
     const int most = A.width << A.page_log2, per = (A.R + 63) / 64;
@@ -98,7 +99,9 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     const int64_t at = quotient64(s.from, A.head_blocks);          // in turns of all requests before
     const int who = __ffsll((unsigned long long)__ballot(upto > at)) - 1;
     int64_t before = lane64(upto, who) - lane64(mine, who);
-    for (int base = who * per;; base += 64) {           // (a lane of it passes `at`)
+    s.r = min((who + 1) * per, A.R) - 1;
+    s.start = before * A.head_blocks;
+    for (int base = who * per; base < (who + 1) * per; base += 64) {
         const int turns = base + lane < (who + 1) * per ? turns_at(base + lane) : 0;
         const int64_t sum = before + wave_scan(turns);
         const uint64_t past = __ballot(sum > at);
@@ -106,10 +109,11 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
             const int l = __ffsll((unsigned long long)past) - 1;
             s.r = base + l;
             s.start = (lane64(sum, l) - __builtin_amdgcn_readlane(turns, l)) * A.head_blocks;
-            return s;
+            break;
         }
         before = lane64(sum, 63);
     }
+    return s;
 }
 
 // Wavefronts a SIMD holds, which is workgroups a compute unit holds. 16 KB of tile in flight a
@@ -213,8 +217,8 @@ struct Parts {
     int64_t first;
     int w0, count;
     __device__ __forceinline__ Parts(int64_t total, int64_t n, int64_t from, int64_t to) {
-        w0 = int(run_of(total, from, n));
-        count = int(run_of(total, to - 1, n)) - w0 + 1;
+        w0 = int(run_of(total, max(from, int64_t(0)), n));
+        count = int(run_of(total, min(to, total) - 1, n)) - w0 + 1;
         first = 2 * int64_t(w0) + (run_start(total, w0, n) != from);
     }
     __device__ __forceinline__ size_t at(int c) const { return size_t(c ? 2 * (int64_t(w0) + c) : first); }
@@ -338,9 +342,10 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
     };
     const int64_t units = run.to - run.from;
     enter(cur, run.r);
-    cur.hb = int(quotient64(run.from - run.start, cur.turns));
+    const int64_t in_r = max(run.from - run.start, int64_t(0));
+    cur.hb = int(min(quotient64(in_r, cur.turns), int64_t(A.head_blocks) - 1));
     cur.kvh = cur.hb / blocks_of_kv;
-    cur.turn = int(run.from - run.start - int64_t(cur.hb) * cur.turns);
+    cur.turn = int(min(in_r - int64_t(cur.hb) * cur.turns, int64_t(cur.turns) - 1));
     Place next = cur;
     if (units > 1) advance(next);
     Place after = next;

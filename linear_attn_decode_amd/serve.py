@@ -248,7 +248,7 @@ def release_pages(ended, lens, table, free, n_free, page: int, status, stream=No
 def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=None):
     """Writes keys and values of new tokens, ``k``, ``v`` [N, H, D] (rows may be strided), at
     ``slots`` (int64 [N]) of the cache; tokens with a slot outside the cache (-1: padding)
-    are not stored. They are of the cache's type or float32, for a float8_e4m3fn cache also
+    are not stored, and no slot is given twice. They are of the cache's type or float32, for a float8_e4m3fn cache also
     bfloat16 or float16: each vector is then stored as max|x| / 448 and the nearest codes."""
     c, dev, shape, _ = _cache(k_cache, v_cache, k_scale, v_scale)
     kind = k.dtype

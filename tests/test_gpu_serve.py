@@ -154,6 +154,18 @@ def test_attend_many_requests():
     run_attend("bf16", "bf16", 64, 1, 2, [int(n) for n in rng.integers(0, 400, 700)], 32, seed=5)
 
 
+@pytest.mark.parametrize("kv,D,H,G,R,longest,window", [("bf16", 128, 3, 2, 300, 200, 0), ("f16", 64, 2, 1, 1030, 70, 0),
+                                                       ("e4m3", 128, 5, 4, 130, 600, 0), ("e4m3", 256, 2, 2, 65, 300, 100),
+                                                       ("bf16", 256, 4, 8, 64, 500, 0), ("bf16", 64, 1, 1, 4100, 40, 0)])
+def test_attend_batches_past_the_lane_count(kv, D, H, G, R, longest, window):
+    """More requests than lanes, idle ones among them, one long one behind many short ones."""
+    rng = np.random.default_rng(R)
+    lens = [int(n) for n in rng.integers(0, longest, R)]
+    lens[R // 3: R // 3 + 5] = [0] * 5
+    lens[-1] = 4 * longest
+    run_attend(kv, "bf16" if kv == "e4m3" else kv, D, H, G, lens, 16, window=window, seed=R)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
 def test_attend_scales(scale):
     run_attend("bf16", "bf16", 128, 1, 4, [1, 50, 400], 16, scale=scale, seed=6)
@@ -676,6 +688,39 @@ def test_calls_on_two_streams_do_not_disturb_each_other():
         torch.cuda.synchronize()
         for q, k, v, table, lens, o, want, s in runs:
             assert torch.equal(o, want)
+
+
+def test_two_captured_calls_replay_side_by_side():
+    """Two graphs of the same call on other inputs, replayed on two streams at once: each has a
+    workspace of its own, and every replay the eager call's bits."""
+    import linear_attn_decode_amd as wb
+    g = torch.Generator().manual_seed(31)
+    page, H, D, width, R = 16, 8, 128, 64, 6
+    k, v = (rand(g, R * width, H, page, D, dtype="bf16").cuda() for _ in range(2))
+    table = torch.randperm(R * width, generator=g).int().view(R, width).cuda()
+    runs = []
+    for i in range(2):
+        q = rand(g, R, 4 * H, D, dtype="bf16").cuda()
+        lens = torch.tensor([1000 - 300 * i, 5, 700, 1024, 0, 333 + i], dtype=torch.int32).cuda()
+        want, o = torch.empty_like(q), torch.zeros_like(q)
+        wb.kv_attend(q, k, v, table, lens, want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                wb.kv_attend(q, k, v, table, lens, o)
+        runs.append((graph, o, want, torch.cuda.Stream(), q, lens))
+    for _ in range(10):
+        for _, o, *_ in runs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for graph, o, want, s, *_ in runs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, o, want, *_ in runs:
+            assert torch.equal(o, want)
+        wb.kv_attend(runs[0][4], k, v, table, runs[0][5], torch.empty_like(runs[0][1]))      # eager work between
 
 
 @pytest.mark.parametrize("D,H", [(128, 4), (64, 2), (256, 4)])
