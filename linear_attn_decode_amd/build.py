@@ -1,7 +1,7 @@
 """Build the HIP library ``libwbstate.so`` in-tree for gfx950.
 
-Every source under ``csrc/`` is compiled by hipcc (objects under ``_build/``), then
-linked into ``linear_attn_decode_amd/libwbstate.so``. Packed FP32 instructions are
+Every source under ``csrc/`` (the write-back path) and ``csrc_serve/`` (the serving
+operators) is compiled by hipcc (objects under ``_build/``), then linked into ``linear_attn_decode_amd/libwbstate.so``. Packed FP32 instructions are
 disabled for all device code (``-packed-fp32-ops``).
 """
 from __future__ import annotations
@@ -16,6 +16,7 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_SERVE = os.path.join(PKG, "csrc_serve")
 OUT = os.path.join(PKG, "libwbstate.so")
 BUILD = os.path.join(ROOT, "_build")
 ARCH = os.environ.get("WB_OFFLOAD_ARCH", "gfx950")
@@ -23,7 +24,7 @@ ARCH = os.environ.get("WB_OFFLOAD_ARCH", "gfx950")
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+    "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", CSRC_SERVE,
     "-Wno-unused-command-line-argument",
 ]
 
@@ -46,7 +47,7 @@ def _compile(src: str) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
+    sources = sorted(glob.glob(os.path.join(CSRC, "*.hip")) + glob.glob(os.path.join(CSRC_SERVE, "*.hip")))
     jobs = min(len(sources), int(os.environ.get("MAX_JOBS", "8")))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
         objs = list(ex.map(_compile, sources))
