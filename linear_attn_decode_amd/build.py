@@ -1,8 +1,9 @@
 """Build the HIP library ``libwbstate.so`` in-tree for gfx950.
 
 Every source under ``csrc/`` (the write-back path) and ``csrc_serve/`` (the serving
-operators) is compiled by hipcc (objects under ``_build/``), then linked into ``linear_attn_decode_amd/libwbstate.so``. Packed FP32 instructions are
-disabled for all device code (``-packed-fp32-ops``).
+operators) is compiled by hipcc (objects under ``_build/``), then linked into
+``linear_attn_decode_amd/libwbstate.so``. Packed FP32 instructions are disabled for all
+device code (``-packed-fp32-ops``).
 """
 from __future__ import annotations
 
