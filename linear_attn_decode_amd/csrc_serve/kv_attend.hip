@@ -267,26 +267,31 @@ __device__ __forceinline__ bool last_to_arrive(uint64_t* c, uint64_t tag, int co
     return last;
 }
 
-// 4 columns of head h of a joined row, in one pass with a running maximum: a part's sums are
-// requested with its maximum
-template <int QT, int D, bool HERE>
-__device__ __forceinline__ void join_columns(const AttendArgs& A, const Parts& parts, int h, int col, size_t row) {
-    float m = -INFINITY, l = 0.f;
+// 4 columns of head h of a row joined from parts c0, c0 + 2^step_log2, ...: their sum, weight sum and
+// maximum, in one pass with a running maximum (a part's sums are requested with its maximum)
+struct Joined {
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int c = 0; c < parts.count; ++c) {
-        const size_t at = parts.at(c) * 16 + h;
-        const f32x2 ml = get_part<HERE>(A.part_ml + 2 * at), v0 = get_part<HERE>(A.part_o + at * D + col),
-                    v1 = get_part<HERE>(A.part_o + at * D + col + 2);
-        const float mc = ml[0], lc = ml[1];
-        const f32x4 vc = {v0[0], v0[1], v1[0], v1[1]};
+    float m = -INFINITY, l = 0.f;
+    __device__ __forceinline__ void add(f32x4 vc, float mc, float lc) {
         const float top = fmaxf(m, mc), ref = top == -INFINITY ? 0.f : top;
         const float f = __builtin_amdgcn_exp2f(m - ref), fc = __builtin_amdgcn_exp2f(mc - ref);
         l = l * f + lc * fc;
         v = v * f + vc * fc;
         m = top;
     }
-    finish<QT>(A, v, l, m, row, D, col);
+};
+template <int D, bool HERE>
+__device__ __forceinline__ Joined join_columns(const AttendArgs& A, const Parts& parts, int h, int col, int c0,
+                                               int step_log2) {
+    Joined j;
+#pragma unroll 8
+    for (int i = 0; i < (parts.count - c0 + (1 << step_log2) - 1) >> step_log2; ++i) {
+        const size_t at = parts.at(c0 + (i << step_log2)) * 16 + h;
+        const f32x2 ml = get_part<HERE>(A.part_ml + 2 * at), v0 = get_part<HERE>(A.part_o + at * D + col),
+                    v1 = get_part<HERE>(A.part_o + at * D + col + 2);
+        j.add(f32x4{v0[0], v0[1], v1[0], v1[1]}, ml[0], ml[1]);
+    }
+    return j;
 }
 
 // JOINS: the workgroup that comes last joins a split segment (else a second launch does)
@@ -625,9 +630,37 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
         if (tid == 0) is_last = last_to_arrive(A.arrivals + parts.w0, A.tag, parts.count);
         __syncthreads();
         if (is_last) {
-            for (int e = tid; e < heads * (D / 4); e += kThreads) {
-                const int h = e / (D / 4), d = e - h * (D / 4);
-                join_columns<QT, D, true>(A, parts, h, 4 * d, size_t(r) * A.Hq + head0 + h);
+            // a lane per 4 columns, and where lanes are left every `ways`-th part
+            const int items = heads * (D / 4);
+            int ways_log2 = 0;
+            while ((items << (ways_log2 + 1)) <= kThreads && (2 << ways_log2) <= parts.count) ++ways_log2;
+            const int ways = 1 << ways_log2;
+            const int way = ways > 1 ? tid / items : 0;
+            auto row_of = [&](int h) { return size_t(r) * A.Hq + head0 + h; };
+            if (ways == 1) {
+                for (int e = tid; e < items; e += kThreads) {
+                    const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
+                    const Joined j = join_columns<D, true>(A, parts, h, d, 0, 0);
+                    finish<QT>(A, j.v, j.l, j.m, row_of(h), D, d);
+                }
+            } else {
+                const int e = tid - way * items, h = e / (D / 4), d = 4 * (e - h * (D / 4));
+                Joined j;
+                // (the sums have been read: their place holds each way's, 8 floats a lane)
+                f32x4* place = reinterpret_cast<f32x4*>(&sums[0][0][0]);
+                if (way < ways) {
+                    j = join_columns<D, true>(A, parts, h, d, way, ways_log2);
+                    place[2 * tid] = j.v;
+                    place[2 * tid + 1] = f32x4{j.m, j.l, 0.f, 0.f};
+                }
+                __syncthreads();
+                if (way == 0) {
+                    for (int w = 1; w < ways; ++w) {
+                        const f32x4 ml = place[2 * (w * items + e) + 1];
+                        j.add(place[2 * (w * items + e)], ml[0], ml[1]);
+                    }
+                    finish<QT>(A, j.v, j.l, j.m, row_of(h), D, d);
+                }
             }
         }
     }
@@ -712,7 +745,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttendArgs A) 
     const int heads = min(16, A.G - 16 * qb);
     for (int e = threadIdx.x; e < heads * (D / 4); e += kJoinThreads) {
         const int h = e / (D / 4), d = e - h * (D / 4);
-        join_columns<QT, D, false>(A, parts, h, 4 * d, size_t(r) * A.Hq + kvh * A.G + 16 * qb + h);
+        const Joined j = join_columns<D, false>(A, parts, h, 4 * d, 0, 0);
+        finish<QT>(A, j.v, j.l, j.m, size_t(r) * A.Hq + kvh * A.G + 16 * qb + h, D, 4 * d);
     }
 }
 
@@ -742,12 +776,13 @@ hipError_t attend_t(const AttendArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// A request's block may get all workgroups but one for each other block, and the one that comes
-// last joins their parts; above kPartsJoined of them (few key-value heads, small tiles) that
-// costs more than a second launch of many workgroups. 32 query and 8 key-value heads of 128
-// columns, joined by the last workgroup / by a second launch: 1 request of 237 tokens 9.3 / 11.7
-// us, 8 to 512 tokens 9.9 / 12.2, 32 to 1024 18.1 / 22.6, 64 to 4096 74.0 / 74.5, 1 of 8000 (32
-// parts) 14.0 / 13.4; 4 key-value heads of 256 columns, 1 of 8000 (64 parts): 53 / 16.
+// A request's block may get nearly all of its share of the workgroups (their number over that
+// of blocks), and the one that comes last joins their parts: above kPartsJoined of them for
+// each lane that costs more than a second launch of many workgroups. 32 query and 8 key-value
+// heads of 128 columns, joined by the last workgroup / by a second launch: 1 request of 237
+// tokens 9.2 / 11.7 us, 1 of 8000 (16 parts a lane) 13.3 / 13.4, 8 to 512 tokens 9.7 / 12.2, 32
+// to 1024 18.0 / 22.6, 64 to 4096 73.5 / 74.5; 20 heads of 64 columns, 24 windows of 1024: 20.7
+// / 21.9; 4 key-value heads of 256 columns, 1 request of 8000 (128 parts a lane): 53 / 16.
 constexpr int kPartsJoined = 32;
 
 // As many workgroups as the card's 256 compute units hold at once, and no more than all
@@ -768,7 +803,8 @@ AttendPlan attend_plan(const wb_kv_cache& c, int R, int Hq, int width, int q_dty
         p.part_ml_bytes = rows * 8;
         p.spans_bytes = (size_t(R) + 1) * 8;
         p.arrivals_bytes = size_t(p.groups) * 8;
-        p.joins_itself = p.groups <= kPartsJoined * p.head_blocks;
+        const int heads = G < 16 ? G : 16;
+        p.joins_itself = int64_t(p.groups) * heads * (c.D / 4) <= int64_t(kPartsJoined) * kThreads * p.head_blocks;
     }
     return p;
 }
