@@ -48,11 +48,6 @@ __device__ __forceinline__ int turns_of(int n, int window, int most) {
     return (n - first_token(n, window) + kTurn - 1) / kTurn;
 }
 
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v)))) |
-                   uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32);
-}
-
 // a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division is some 150
 // dependent instructions)
 __device__ __forceinline__ int64_t quotient64(int64_t a, int64_t b) {
@@ -69,6 +64,7 @@ struct Run {
     int64_t start;                  // first unit of request r
     int r;                          // the request of unit `from`
     int n;                          // workgroups with work
+    int lens_at, lens;              // the lane's length of requests lens_at ..+63, r's among them
 };
 
 __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
@@ -83,15 +79,21 @@ __device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
 __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     const int lane = threadIdx.x & 63;
     const int most = A.width << A.page_log2, per = (A.R + 63) / 64;
-    auto turns_at = [&](int r) { return r < A.R ? turns_of(A.lens[r], A.window, most) : 0; };
-    int64_t mine = 0;
+    auto len_at = [&](int r) { return r < A.R ? A.lens[r] : 0; };
+    auto turns_at = [&](int r, int len) { return r < A.R ? turns_of(len, A.window, most) : 0; };
+    const int len0 = len_at(lane);                       // (up to 64 requests: all there is to load)
+    int64_t mine = turns_at(lane, len0);
+    if (per > 1) {
+        mine = 0;
 #pragma unroll 4
-    for (int i = 0; i < per; ++i) mine += turns_at(lane * per + i);
+        for (int i = 0; i < per; ++i) mine += turns_at(lane * per + i, len_at(lane * per + i));
+    }
     const int64_t upto = wave_scan(mine);
     Run s;
     s.total = lane64(upto, 63) * A.head_blocks;
     const int n = s.n = int(s.total < gridDim.x ? s.total : int64_t(gridDim.x));
-    s.r = 0;
+    s.r = s.lens_at = 0;
+    s.lens = len0;
     s.from = s.to = s.start = 0;
     if (int(blockIdx.x) >= n) return s;
     s.from = run_start(s.total, blockIdx.x, n);
@@ -99,10 +101,15 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
     const int64_t at = quotient64(s.from, A.head_blocks);          // in turns of all requests before
     const int who = __ffsll((unsigned long long)__ballot(upto > at)) - 1;
     int64_t before = lane64(upto, who) - lane64(mine, who);
+    if (per == 1) {
+        s.r = who;
+        s.start = before * A.head_blocks;
+        return s;
+    }
     s.r = min((who + 1) * per, A.R) - 1;
     s.start = before * A.head_blocks;
     for (int base = who * per; base < (who + 1) * per; base += 64) {
-        const int turns = base + lane < (who + 1) * per ? turns_at(base + lane) : 0;
+        const int turns = base + lane < (who + 1) * per ? turns_at(base + lane, len_at(base + lane)) : 0;
         const int64_t sum = before + wave_scan(turns);
         const uint64_t past = __ballot(sum > at);
         if (past) {
@@ -113,6 +120,8 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
         }
         before = lane64(sum, 63);
     }
+    s.lens_at = s.r & ~63;
+    s.lens = len_at(s.lens_at + lane);
     return s;
 }
 
@@ -139,7 +148,6 @@ template <int T>
 struct Mat;
 template <>
 struct Mat<WB_BF16> {
-    typedef bf16x8 V8;
     static __device__ __forceinline__ f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                        0, 0);
@@ -147,7 +155,6 @@ struct Mat<WB_BF16> {
 };
 template <>
 struct Mat<WB_F16> {
-    typedef f16x8 V8;
     static __device__ __forceinline__ f32x4 mul(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                       0);
@@ -321,8 +328,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
     // is computed, the next one, whose keys and values are requested, and the one after it,
     // whose page ids are. Requests' ends make no difference to the sequence: at the start of
     // a request or block the loads have been in flight as long as inside one.
-    int lens_at = run.r & ~63;
-    int lens64 = lens_at + lane < A.R ? A.lens[lens_at + lane] : 0;
+    int lens_at = run.lens_at, lens64 = run.lens;
     Place cur;
     auto enter = [&](Place& p, int r) {
         if (r - lens_at >= 64) {
