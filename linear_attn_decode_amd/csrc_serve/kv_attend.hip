@@ -426,17 +426,20 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
         }
     };
 
+    // (page ids first: the first keys wait for them)
+    int pk = page_at(cur, koff), pv = page_at(cur, voff);
+    const int pk_next = page_at(next, koff), pv_next = page_at(next, voff);
     u32x4 qh[KQ], ql[KQ];
     T::load_q(A, cur.r, cur.kvh, cur.hb - cur.kvh * blocks_of_kv, qh, ql);
     size_t row_v;
     {
-        const int pk = page_at(cur, koff), pv = page_at(cur, voff);
         const size_t row_k = row_in(cur, pk, koff);
         row_v = row_in(cur, pv, voff);
         load_keys(row_k, row_v);
         load_values(row_v);
     }
-    int pk = page_at(next, koff), pv = page_at(next, voff);
+    pk = pk_next;
+    pv = pv_next;
 
     f32x4 acc[VN * VB];
     float m, l;
@@ -684,59 +687,28 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
 }
 
 // Joins the segments of a request. Few requests (which may have hundreds each): a workgroup
-// per (request, query head, 64 columns), 16 lanes across the columns and 16 along the
-// segments, whose factors are worked out once in LDS.
-constexpr int kJoinThreads = 256, kJoinCols = 64, kJoinStep = 1024;
+// per (request, query head, 64 columns), 16 lanes across the columns and 16 along the segments.
+constexpr int kJoinThreads = 256, kJoinCols = 64;
 constexpr int kLongWorkgroups = 2048;
 template <int QT, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_long_kernel(const AttendArgs A) {
-    constexpr int NT = kJoinThreads, L = kJoinCols / 4, N = NT / L;
-    __shared__ float factor[kJoinStep];
-    __shared__ f32x4 part[N][L];
-    __shared__ float red_m[NT / 64], red_l[NT / 64];
-    const int tid = threadIdx.x;
+    constexpr int L = kJoinCols / 4, N = kJoinThreads / L;
+    static_assert(N == 16, "ways along the segments");
+    __shared__ f32x4 sums[N][L];
+    __shared__ f32x2 stats[N][L];
     const int r = blockIdx.x, h = blockIdx.y;
     const int kvh = h / A.G, in_kv = h - kvh * A.G;
     const Parts parts = parts_of(A, r, kvh * (A.head_blocks / A.c.H) + in_kv / 16);
-    const int count = parts.count, in_block = in_kv & 15;
-    if (count == 1) return;
-
-    float m = -INFINITY;
-    for (int c = tid; c < count; c += NT) m = fmaxf(m, A.part_ml[2 * (parts.at(c) * 16 + in_block)]);
-    m = max_xor32(max_xor16(m));
-#pragma unroll
-    for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-    if ((tid & 63) == 0) red_m[tid >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red_m[0], red_m[1]), fmaxf(red_m[2], red_m[3]));
-    const float ref = m == -INFINITY ? 0.f : m;
-
-    const int d = tid % L, w = tid / L;
-    const float* col = A.part_o + blockIdx.z * kJoinCols + 4 * d;
-    f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    for (int base = 0; base < count; base += kJoinStep) {
-        const int upto = min(kJoinStep, count - base);
-        __syncthreads();
-        for (int c = tid; c < upto; c += NT) {
-            const size_t at = parts.at(base + c) * 16 + in_block;
-            const float f = __builtin_amdgcn_exp2f(A.part_ml[2 * at] - ref);
-            factor[c] = f;
-            l += A.part_ml[2 * at + 1] * f;
-        }
-        __syncthreads();
-#pragma unroll 8
-        for (int c = w; c < upto; c += N) v += *reinterpret_cast<const f32x4*>(col + (parts.at(base + c) * 16 + in_block) * D) * factor[c];
-    }
-    l = __uint_as_float(lanes_reduce<OpAdd, 64>(__float_as_uint(l)));
-    if ((tid & 63) == 0) red_l[tid >> 6] = l;
-    part[w][d] = v;
+    if (parts.count == 1) return;
+    const int d = threadIdx.x % L, w = threadIdx.x / L, col = blockIdx.z * kJoinCols + 4 * d;
+    Joined j = join_columns<D, false>(A, parts, in_kv & 15, col, w, 4);
+    sums[w][d] = j.v;
+    stats[w][d] = f32x2{j.m, j.l};
     __syncthreads();
     if (w) return;
 #pragma unroll
-    for (int i = 1; i < N; ++i) v += part[i][d];
-    l = (red_l[0] + red_l[1]) + (red_l[2] + red_l[3]);
-    finish<QT>(A, v, l, m, size_t(r) * A.Hq + h, D, blockIdx.z * kJoinCols + 4 * d);
+    for (int i = 1; i < N; ++i) j.add(sums[i][d], stats[i][d][0], stats[i][d][1]);
+    finish<QT>(A, j.v, j.l, j.m, size_t(r) * A.Hq + h, D, col);
 }
 
 // Many requests (of few segments each, most of them whole, with nothing to join): a workgroup
