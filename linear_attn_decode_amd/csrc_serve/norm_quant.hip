@@ -4,49 +4,74 @@
 // between the sum of squares, the groups' maxima and the codes, so every input is read once
 // and every output written once; HBM bounds it (a single row: the launch). The 128 columns
 // of a group are 16 neighbouring lanes of one chunk, so a group's maximum is four DPP steps.
-// Rows of up to 512 columns take 16, 32 or 64 lanes, several rows a wavefront; wider ones a
+// Rows of up to 512 columns take 8, 16, 32 or 64 lanes, several rows a wavefront; wider ones a
 // workgroup of as many wavefronts as their chunks need, two chunks a lane (8191 rows of 5000
 // bfloat16 columns with a residual: 60.1 us, 4.79 TB/s, the rate of a copy; 66.5 us with one
 // chunk, 63.0 with three, 72.1 with four; 56.8 us with stores past the caches, which cost the
 // kernel that reads them next 7 us). Strides and alignment are free: the
 // 16-byte accesses need only the element's alignment on this hardware, and the chunk that
-// holds a row's ragged end goes by single elements.
+// holds a row's ragged end goes by 4, 2 and 1 columns (bfloat16 with a residual: 400000 rows of
+// 100 columns 80.9 us, 109 by single elements; 2352941 rows of 17 179 us, and 305 by single
+// elements with 16 lanes a row; 312500 rows of 128 51.4 us).
 #include "serve_device.hpp"
 
 namespace wb {
 namespace {
 
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
+typedef f32x2 f32x2_a4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
+typedef uint32_t u32_a1 __attribute__((aligned(1)));
+typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
+// 8 columns from `at`, or the n < 8 that are left of the row (then 0): 4, 2 and 1 of them by the
+// bits of n, three accesses where single elements would be up to seven
 template <int T>
 __device__ __forceinline__ void load_chunk(const void* p, int64_t at, int n, float x[8]) {
     if constexpr (T == WB_F32) {
         const float* s = static_cast<const float*>(p) + at;
+        f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
         if (n >= 8) {
-            const f32x4 a = *reinterpret_cast<const f32x4_a4*>(s), b = *reinterpret_cast<const f32x4_a4*>(s + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = a[i];
-                x[4 + i] = b[i];
-            }
+            a = *reinterpret_cast<const f32x4_a4*>(s);
+            b = *reinterpret_cast<const f32x4_a4*>(s + 4);
         } else {
+            f32x2 pair = {0.f, 0.f};
+            float one = 0.f;
+            if (n & 4) a = *reinterpret_cast<const f32x4_a4*>(s);
+            if (n & 2) pair = *reinterpret_cast<const f32x2_a4*>(s + (n & 4));
+            if (n & 1) one = s[n & 6];
+            f32x4 rest = {0.f, 0.f, 0.f, 0.f};               // what follows the four
+            if (n & 2) rest = f32x4{pair[0], pair[1], one, 0.f};
+            else rest[0] = one;
+            if (n & 4) b = rest;
+            else a = rest;
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = i < n ? s[i] : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            x[i] = a[i];
+            x[4 + i] = b[i];
         }
     } else {
         const uint16_t* s = static_cast<const uint16_t*>(p) + at;
+        u32x4 w = {0, 0, 0, 0};
         if (n >= 8) {
-            const u32x4 w = *reinterpret_cast<const u32x4_a2*>(s);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = Elem<T>::get(uint16_t(w[i]));
-                x[2 * i + 1] = Elem<T>::get(uint16_t(w[i] >> 16));
-            }
+            w = *reinterpret_cast<const u32x4_a2*>(s);
         } else {
+            u32x2 four = {0, 0};
+            uint32_t pair = 0, one = 0;
+            if (n & 4) four = *reinterpret_cast<const u32x2_a2*>(s);
+            if (n & 2) pair = *reinterpret_cast<const u32_a2*>(s + (n & 4));
+            if (n & 1) one = s[n & 6];
+            const uint32_t r0 = n & 2 ? pair : one, r1 = n & 2 ? one : 0;
+            w = n & 4 ? u32x4{four[0], four[1], r0, r1} : u32x4{r0, r1, 0, 0};
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = i < n ? Elem<T>::get(s[i]) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = Elem<T>::get(uint16_t(w[i]));
+            x[2 * i + 1] = Elem<T>::get(uint16_t(w[i] >> 16));
         }
     }
 }
@@ -55,30 +80,44 @@ template <int T>
 __device__ __forceinline__ void store_chunk(void* p, int64_t at, int n, const float x[8]) {
     if constexpr (T == WB_F32) {
         float* s = static_cast<float*>(p) + at;
+        const f32x4 a = {x[0], x[1], x[2], x[3]}, b = {x[4], x[5], x[6], x[7]};
         if (n >= 8) {
-            *reinterpret_cast<f32x4_a4*>(s) = f32x4{x[0], x[1], x[2], x[3]};
-            *reinterpret_cast<f32x4_a4*>(s + 4) = f32x4{x[4], x[5], x[6], x[7]};
+            *reinterpret_cast<f32x4_a4*>(s) = a;
+            *reinterpret_cast<f32x4_a4*>(s + 4) = b;
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) s[i] = x[i];
+            const f32x4 rest = n & 4 ? b : a;
+            if (n & 4) *reinterpret_cast<f32x4_a4*>(s) = a;
+            if (n & 2) *reinterpret_cast<f32x2_a4*>(s + (n & 4)) = f32x2{rest[0], rest[1]};
+            if (n & 1) s[n & 6] = n & 2 ? rest[2] : rest[0];
         }
     } else {
         uint16_t* s = static_cast<uint16_t*>(p) + at;
-        if (n >= 8) {
-            u32x4 w;
+        u32x4 w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = uint32_t(Elem<T>::put(x[2 * i])) | uint32_t(Elem<T>::put(x[2 * i + 1])) << 16;
+        for (int i = 0; i < 4; ++i) w[i] = uint32_t(Elem<T>::put(x[2 * i])) | uint32_t(Elem<T>::put(x[2 * i + 1])) << 16;
+        if (n >= 8) {
             *reinterpret_cast<u32x4_a2*>(s) = w;
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < n) s[i] = Elem<T>::put(x[i]);
+            const uint32_t r0 = n & 4 ? w[2] : w[0], r1 = n & 4 ? w[3] : w[1];
+            if (n & 4) *reinterpret_cast<u32x2_a2*>(s) = u32x2{w[0], w[1]};
+            if (n & 2) *reinterpret_cast<u32_a2*>(s + (n & 4)) = r0;
+            if (n & 1) s[n & 6] = uint16_t(n & 2 ? r1 : r0);
         }
     }
 }
 
-// LR: lanes of a row (16, 32, 64), or 0 for the whole workgroup. V: chunks of a lane.
+__device__ __forceinline__ void store_codes(uint8_t* s, int n, u32x2 w) {
+    if (n >= 8) {
+        *reinterpret_cast<u32x2_a1*>(s) = w;
+    } else {
+        const uint32_t rest = n & 4 ? w[1] : w[0];
+        if (n & 4) *reinterpret_cast<u32_a1*>(s) = w[0];
+        if (n & 2) *reinterpret_cast<u16_a1*>(s + (n & 4)) = uint16_t(rest);
+        if (n & 1) s[n & 6] = uint8_t(n & 2 ? rest >> 16 : rest);
+    }
+}
+
+// LR: lanes of a row (8, 16, 32, 64), or 0 for the whole workgroup. V: chunks of a lane.
 template <int T, int LR, int V>
 __global__ void __launch_bounds__(LR ? 256 : 1024) norm_kernel(const NormArgs A) {
     __shared__ uint32_t red[16];
@@ -159,7 +198,7 @@ __global__ void __launch_bounds__(LR ? 256 : 1024) norm_kernel(const NormArgs A)
         for (int c = 0; c < V; ++c) top[c] = all;
     } else {
 #pragma unroll
-        for (int c = 0; c < V; ++c) top[c] = lanes_reduce<OpMax, 16>(top[c]);
+        for (int c = 0; c < V; ++c) top[c] = lanes_reduce<OpMax, LR == 8 ? 8 : 16>(top[c]);
     }
     const int groups = A.group ? (D + 127) / 128 : 1;
 #pragma unroll
@@ -174,14 +213,7 @@ __global__ void __launch_bounds__(LR ? 256 : 1024) norm_kernel(const NormArgs A)
         u32x2 w;
         w[0] = e4m3_pack4(q[0], q[1], q[2], q[3]);
         w[1] = e4m3_pack4(q[4], q[5], q[6], q[7]);
-        uint8_t* out = A.codes + n * A.c_row + j;
-        if (left >= 8) {
-            *reinterpret_cast<u32x2_a1*>(out) = w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left) out[i] = uint8_t(w[i >> 2] >> (8 * (i & 3)));
-        }
+        store_codes(A.codes + n * A.c_row + j, left, w);
         if (A.group ? (lane & 15) == 0 : c == 0 && lane == 0) A.scales[n * groups + (A.group ? j >> 7 : 0)] = scale;
     }
 }
@@ -191,7 +223,8 @@ hipError_t norm_t(const NormArgs& a, hipStream_t s) {
     const int chunks = (a.D + 7) / 8;
     auto rows = [&](int per) { return unsigned((a.N + per - 1) / per); };
     auto threads = [&](int v) { return unsigned(((chunks + v - 1) / v + 63) / 64 * 64); };
-    if (chunks <= 16) norm_kernel<T, 16, 1><<<rows(16), 256, 0, s>>>(a);
+    if (chunks <= 8) norm_kernel<T, 8, 1><<<rows(32), 256, 0, s>>>(a);
+    else if (chunks <= 16) norm_kernel<T, 16, 1><<<rows(16), 256, 0, s>>>(a);
     else if (chunks <= 32) norm_kernel<T, 32, 1><<<rows(8), 256, 0, s>>>(a);
     else if (chunks <= 64) norm_kernel<T, 64, 1><<<rows(4), 256, 0, s>>>(a);
     else if (chunks <= 2048) norm_kernel<T, 0, 2><<<a.N, threads(2), 0, s>>>(a);

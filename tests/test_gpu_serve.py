@@ -474,6 +474,15 @@ def test_norm_strides_and_alignment(D, slack, shift):
     run_norm(6, D, "f32", True, 0, slack=slack, shift=shift, in_place=True)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("base", [0, 56, 120, 248, 1040])
+def test_norm_row_ends(dt, base):
+    """Every length of a row's last chunk, at each number of lanes a row takes."""
+    for tail in range(1, 8):
+        run_norm(37, base + tail, dt, True, 128, slack=3, shift=1, seed=tail)
+        run_norm(37, base + tail, dt, False, 0, seed=tail)
+
+
 @pytest.mark.parametrize("N", [1, 2, 63, 64, 1023, 5000])
 def test_norm_rows(N):
     run_norm(N, 128, "f32", False, 0, seed=N)
