@@ -494,6 +494,30 @@ def test_norm_widest_rows():
     run_norm(2, 65535, "f32", False, 0)
 
 
+@pytest.mark.parametrize("log2w", [-140, -126, -122, -119, -118, -100, 0, 100, 124])
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_scales_at_the_ends_of_the_range(log2w, group):
+    """Weights that put a scale at its least value, beside it, and a row's values near the
+    largest float32. (Products below the normal numbers are off by 2^-150 each: 2^-22 of a
+    scale, two of them.)"""
+    import linear_attn_decode_amd as wb
+    N, D = 64, 200
+    g = torch.Generator().manual_seed(200 + log2w)
+    x = rand(g, N, D) * torch.exp(2 * torch.randn((N, 1), generator=g))
+    w = torch.ldexp(1 + 0.3 * torch.rand(D, generator=g), torch.tensor(log2w))
+    codes = torch.empty((N, D), dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty((N, -(-D // group) if group else 1), device="cuda")
+    wb.norm_quant(x.cuda(), w.cuda(), codes, scales, eps=1e-6, group=group)
+    torch.cuda.synchronize()
+    _, y, want = O.norm(x.double().numpy(), None, w.double().numpy(), 1e-6, group)
+    rel = (D / 256 + 64 + 24) * U
+    sc = scales.double().cpu().numpy()
+    assert (np.abs(sc - want) <= (rel + 2 * U) * want).all()
+    q = np.clip(y / np.repeat(sc, group or D, axis=1)[:, :D], -448, 448)
+    err = np.abs(codes.double().cpu().numpy() - q)
+    assert (err <= O.e4m3_half_step(q) + 2 * rel * np.abs(q) + 2.0 ** -21).all()
+
+
 def test_norm_zero_and_non_finite_rows():
     import linear_attn_decode_amd as wb
     x = torch.ones((4, 512), device="cuda")
