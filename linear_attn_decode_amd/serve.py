@@ -192,6 +192,8 @@ def plan_pages(lens, more, table, free, n_free, page: int, slots, starts, status
     and then nothing is placed and every slot is -1."""
     if _torch is None:
         _load()
+    if not -_MAX <= page <= _MAX:         # (ctypes would pass its lower 32 bits)
+        raise ValueError(f"page: {page} is out of range")
     dev = _device(lens, "lens")
     i32 = _torch.int32
     if table.dim() != 2 or free.dim() != 1 or slots.dim() != 1:
@@ -232,6 +234,8 @@ def release_pages(ended, lens, table, free, n_free, page: int, status, stream=No
     (int32 [1]) as for ``plan_pages`` (4: more pages than ``free`` holds)."""
     if _torch is None:
         _load()
+    if not -_MAX <= page <= _MAX:
+        raise ValueError(f"page: {page} is out of range")
     dev = _device(lens, "lens")
     i32 = _torch.int32
     if table.dim() != 2 or free.dim() != 1:
@@ -317,6 +321,8 @@ def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, resi
     float32; rows may be strided."""
     if _torch is None:
         _load()
+    if not -_MAX <= group <= _MAX:        # (the library would take its lower 32 bits, and write their number of scales)
+        raise ValueError(f"group: {group} is out of range")
     dev = _device(x, "x")
     kind = x.dtype
     code = _codes.get(kind, E4M3)
