@@ -102,13 +102,14 @@ int kv_append(const wb_kv_cache* c, const void* k, const void* v, int64_t k_row,
  * h / (Hq / H),
  *   s_t = scale * q[r][h] . k_t,  o[r][h] = sum_t e^{s_t} v_t / sum_t e^{s_t},
  *   lse[r][h] = log sum_t e^{s_t} (float32 [R][Hq], or NULL).
- * Scores, maxima and sums are float32, the weights e^{s_t - max} enter the product with v as
- * two 16-bit limbs, o is rounded once. A request without tokens, or whose scores are all
- * -infinity, has o = 0 and lse = -infinity. Stored values outside the range are not used,
- * whatever they hold; a NaN inside it gives NaN, an infinity what the formula gives or NaN. A
- * request with a length outside [0, width * page], or a page id outside [0, pages) in the
- * range it reads, has o = lse = NaN. Results do not depend on timing: equal calls give equal
- * bits.
+ * Scores, maxima and sums are float32, the weights e^{s_t - max} (times the value's scale, for
+ * an 8-bit cache) enter the product with v as two 16-bit limbs, within 2^-17 of each weight (and
+ * for a float16 cache 2^-40 of the largest), o is rounded once. A request without tokens, or
+ * whose scores are all -infinity, has o = 0 and lse = -infinity. Stored values outside the range
+ * are not used, whatever they hold; a NaN inside it gives NaN, an infinity what the formula
+ * gives or NaN. A request with a length outside [0, width * page], or a page id outside
+ * [0, pages) in the range it reads, has o = lse = NaN. Results do not depend on timing: equal
+ * calls give equal bits.
  * q [R][Hq][D] of type q_dtype (the cache's, or WB_BF16 / WB_F16 for an 8-bit cache), strides
  * q_row and q_head in elements, multiples of 8; o [R][Hq][D] contiguous, of q's type; table
  * int32 [R][width]; lens int32 [R]. `work` has kv_attend_work() bytes (NULL if 0), 16-byte

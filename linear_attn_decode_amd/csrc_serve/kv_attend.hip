@@ -20,6 +20,9 @@
 //     over all c each lane ends with contiguous columns of its head.
 //   * The weights enter as two 16-bit limbs, p = hi + lo: the second product costs matrix
 //     time that is idle anyway and keeps their rounding (2^-9 in bfloat16) out of the result.
+//     Float16 limbs hold 2^15 p, which is at most 2^15: their smallest step, 2^-24, is then
+//     2^-39 of the largest weight. (Limbs of p itself lose a weight of e^-17.4 altogether, which
+//     is all there is of a row whose one heavy token has a value near 0.)
 // Work is split along the cache. Its units are turns of 128 tokens (a tile for each of a
 // workgroup's 4 wavefronts) of one request for one block of heads, in the order (request,
 // block, turn); as many workgroups as the card holds at once take equal runs of them, found
@@ -178,6 +181,7 @@ struct Attend {
     static constexpr int VB = D == 64 ? 4 : 8;        // value columns of a lane's block
     static constexpr int VN = D / (16 * VB);          // blocks of a lane (2 for D = 256)
     static constexpr int LD = D + 4;                  // LDS stride of a head's sums
+    static constexpr float kLimbs = MT == WB_F16 ? 0x1p15f : 1.f;     // what the weights' limbs are multiplied by
     using M = Mat<MT>;
 
     // q's operands: lane l holds head l % 16, the 8 values that meet the keys' 8 of each product
@@ -536,6 +540,8 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
                     a *= vs[j >> 1][(2 * j) & 3];
                     b *= vs[j >> 1][(2 * j + 1) & 3];
                 }
+                a *= T::kLimbs;
+                b *= T::kLimbs;
                 const uint16_t ah = Elem<T::MT>::put(a), bh = Elem<T::MT>::put(b);
                 ph[j] = uint32_t(ah) | uint32_t(bh) << 16;
                 pl[j] = uint32_t(Elem<T::MT>::put(a - Elem<T::MT>::get(ah))) |
@@ -619,6 +625,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(KV, QT, D)) attend_ke
             v += *reinterpret_cast<const f32x4*>(&sums[w][h][d]) * f;
             ll += stat_l[w][h] * f;
         }
+        v *= 1.f / T::kLimbs;
         if (poison) ll = __builtin_nanf("");
         if (alone) {
             finish<QT>(A, v, ll, mm, size_t(r) * A.Hq + head0 + h, D, d);

@@ -1,0 +1,99 @@
+"""The serving operators (include/wbserve.h) where their numbers and sizes come near the ends
+of their ranges, against their float64 definitions (oracle/serving.py).
+
+Tolerances, from the arithmetic (u = 2^-24, half a float32 step), are written at each test.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import serving as O
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+U = 2.0 ** -24
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+# ---------------------------------------------------------------------------- attention
+def sink_bound(ro, W, n, D, gap, kv, v_max):
+    """Scores are within e_s = (D + 4) u A + 2^-22 A (A: the largest, `gap`), a weight and the
+    sum that divides it off by that each, sums over tokens by (96 + n / 32) u twice; a weight's
+    limbs leave 2^-17 of it, float16 ones also half of the smallest float16 step at 2^15 times
+    the weight, 2^-40 a token; the output is rounded once, by half a step, which is not below
+    2^-25 in float16."""
+    A = max(1.0, abs(gap))
+    e_s = (D + 4) * U * A + 2.0 ** -22 * A
+    half = torch.finfo(TYPES[kv]).eps / 2 * np.abs(ro)
+    tol = W * (2 * e_s + 2.0 ** -17 + 2 * (96 + n / 32) * U)
+    if kv == "f16":
+        half, tol = np.maximum(half, 2.0 ** -25), tol + n * 2.0 ** -40 * v_max
+    return half + tol
+
+
+@pytest.mark.parametrize("gap", [9.0, 12.0, 15.0, 16.5, 17.0, 17.5, 18.0])
+@pytest.mark.parametrize("kv,D,R,n,at", [("f16", 256, 800, 2048, 0), ("f16", 64, 1, 20000, 0), ("f16", 128, 1, 20000, 9000),
+                                         ("f16", 128, 3, 131072, 1), ("bf16", 128, 1, 20000, 0)])
+def test_attend_one_token_far_above_all_others(kv, D, R, n, at, gap):
+    """A token of value 0 that takes nearly all the weight, `gap` above n - 1 equal ones that
+    make up the row: whole requests of one workgroup (800 of 16 turns on 256 workgroups) and
+    split ones. The requests share their pages."""
+    import linear_attn_decode_amd as wb
+    print(f"[case] sink kv={kv} D={D} R={R} n={n} at={at} gap={gap}", flush=True)
+    page = 64
+    pages = -(-n // page)
+    k = torch.zeros((pages, 1, page, D), dtype=TYPES[kv], device="cuda")
+    v = torch.full_like(k, 64.0)
+    k[at // page, 0, at % page, 0] = gap
+    v[at // page, 0, at % page] = 0
+    q = torch.zeros((R, 2, D), dtype=TYPES[kv], device="cuda")
+    q[:, 0, 0], q[:, 1, 0] = 1.0, 0.5                                    # (the second head: half the gap)
+    table = torch.arange(pages, dtype=torch.int32).repeat(R, 1).cuda()
+    o, lse = torch.empty_like(q), torch.empty((R, 2), device="cuda")
+    wb.kv_attend(q, k, v, table, torch.full((R,), n, dtype=torch.int32).cuda(), o, scale=1.0, lse=lse)
+    torch.cuda.synchronize()
+    for h, g in ((0, gap), (1, gap / 2)):
+        rest = (n - 1) * math.exp(-g)
+        ro = 64.0 * rest / (1 + rest)
+        got = o[:, h].double().cpu().numpy()
+        assert (np.abs(got - ro) <= sink_bound(ro, ro, n, D, g, kv, 64.0)).all(), (h, ro, got.min(), got.max())
+        want = g + math.log1p(rest)
+        e_s = (D + 4) * U * g + 2.0 ** -22 * g
+        assert (np.abs(lse[:, h].double().cpu().numpy() - want) <= e_s + (96 + n / 32) * U + 2 * U * want).all()
+
+
+@pytest.mark.parametrize("n", [1, 300, 5000])
+def test_attend_largest_float16_values(n):
+    """Equal weights over the largest values: the sums of 2^15 times the weights stay float32
+    numbers, and the mean is the value (off by (96 + n / 32) u, far below half a float16 step)."""
+    import linear_attn_decode_amd as wb
+    page, D = 64, 128
+    pages = -(-n // page)
+    k = torch.zeros((pages, 1, page, D), dtype=torch.float16, device="cuda")
+    v = torch.full_like(k, 65504.0)
+    v[..., 1::2] = -65504.0
+    q = torch.ones((1, 4, D), dtype=torch.float16, device="cuda")
+    o = torch.empty_like(q)
+    wb.kv_attend(q, k, v, torch.arange(pages, dtype=torch.int32)[None].cuda(), torch.tensor([n], dtype=torch.int32).cuda(), o)
+    torch.cuda.synchronize()
+    assert (o[..., ::2] == 65504).all() and (o[..., 1::2] == -65504).all()
+
+
+def test_attend_weights_of_random_scores_far_apart():
+    """Float16 keys whose scores spread over some 30 nats, against the definition, without an
+    allowance for lost weights but 2^-40 a token."""
+    import linear_attn_decode_amd as wb
+    page, D, H, G, n = 16, 64, 2, 4, 6000
+    g = torch.Generator().manual_seed(41)
+    pages = n // page
+    k, v = (torch.randn((pages, H, page, D), generator=g).half().cuda() for _ in range(2))
+    q = (4 * torch.randn((1, H * G, D), generator=g)).half().cuda()
+    o = torch.empty_like(q)
+    wb.kv_attend(q, k, v, torch.arange(pages, dtype=torch.int32)[None].cuda(), torch.tensor([n], dtype=torch.int32).cuda(), o)
+    torch.cuda.synchronize()
+    k64, v64 = (x.double().cpu().numpy().transpose(0, 2, 1, 3).reshape(n, H, D) for x in (k, v))
+    ro, _, W, size = O.attend(q[0].double().cpu().numpy(), k64, v64, D ** -0.5)
+    err = np.abs(o[0].double().cpu().numpy() - ro)
+    tol = sink_bound(ro, W, n, D, float(size.max()), "f16", np.abs(v64).max())
+    assert (err <= tol).all(), float((err / tol).max())
