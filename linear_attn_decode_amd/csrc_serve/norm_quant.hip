@@ -194,7 +194,9 @@ __global__ void __launch_bounds__(LR ? 256 : 1024) norm_kernel(const NormArgs A)
         for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[c][i], h[c][i], sum);
     }
     sum = __uint_as_float(row_reduce(OpAdd{}, __float_as_uint(sum)));
-    const float rstd = 1.f / sqrtf(sum / float(D) + A.eps);
+    // (a row of zeros without eps: any factor keeps its zeros, 0 * infinity would not)
+    const float ms = sum / float(D) + A.eps;
+    const float rstd = ms == 0.f ? 1.f : 1.f / sqrtf(ms);
     // rstd = pow2 * frac, frac in [1, 2): the row's z = h * pow2 * w is rounded once, y = z * frac,
     // and y / scale = z * 448 / max |z| has none of rstd's roundings
     const float pow2 = rstd != rstd ? rstd : __uint_as_float(__float_as_uint(rstd) & 0x7F800000u);

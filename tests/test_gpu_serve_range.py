@@ -97,3 +97,31 @@ def test_attend_weights_of_random_scores_far_apart():
     err = np.abs(o[0].double().cpu().numpy() - ro)
     tol = sink_bound(ro, W, n, D, float(size.max()), "f16", np.abs(v64).max())
     assert (err <= tol).all(), float((err / tol).max())
+
+
+# ---------------------------------------------------------------------------- norm
+# every kernel: 8, 16, 32 and 64 lanes a row, a workgroup with 2, 4 and 8 chunks a lane
+NORM_WIDTHS = [1, 50, 100, 200, 500, 1000, 5000, 20000, 40000]
+
+
+@pytest.mark.parametrize("D", NORM_WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_norm_rows_of_zeros_without_eps(D, dt):
+    """A group of zeros has scale 0 and codes 0, with eps = 0 too, beside rows that are not zero."""
+    import linear_attn_decode_amd as wb
+    print(f"[case] norm zeros D={D} {dt}", flush=True)
+    x = torch.ones((5, D), dtype=TYPES[dt], device="cuda")
+    x[0] = x[3] = 0
+    w = torch.full((D,), -2.0, dtype=TYPES[dt], device="cuda")
+    r = torch.zeros_like(x)
+    for group in (0, 128):
+        codes = torch.empty((5, D), dtype=torch.float8_e4m3fn, device="cuda")
+        scales = torch.empty((5, -(-D // group) if group else 1), device="cuda")
+        for kw in ({}, {"residual": r, "residual_out": torch.empty_like(x)}):
+            codes.view(torch.uint8).fill_(77)
+            scales.fill_(math.nan)
+            wb.norm_quant(x, w, codes, scales, eps=0.0, group=group, **kw)
+            torch.cuda.synchronize()
+            c = codes.float()
+            assert (c[[0, 3]] == 0).all() and (scales[[0, 3]] == 0).all()
+            assert (c[[1, 2, 4]] == -448).all() and (scales[[1, 2, 4]] - 2 / 448).abs().max() <= 2 / 448 * 8 * U
