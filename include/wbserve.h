@@ -127,7 +127,8 @@ int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes
  *   y = h / sqrt(mean(h^2) + eps) * weight (weight NULL: 1),
  *   scale_g = max_{j in group g} |y_j| / 448 (2^-126 at least), code_j = e4m3(y_j / scale_g),
  * groups of `group` columns (128; the last may be shorter) or the whole row (group 0). The
- * norm takes h before it is rounded. x, residual, residual_out, weight are of type `dtype`
+ * norm takes h before it is rounded, of any finite size (where its squares leave float32's
+ * range, it takes h and eps scaled). x, residual, residual_out, weight are of type `dtype`
  * (WB_BF16, WB_F16, WB_F32); x_row, r_row, ro_row, c_row are row strides in elements; scales
  * float32 [N][ceil(D / group)]. A group of zeros has scale 0 and codes 0; a group that holds
  * a NaN or an infinity, or whose row holds a NaN, has NaN codes. residual_out may be

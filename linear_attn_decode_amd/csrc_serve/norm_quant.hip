@@ -194,8 +194,34 @@ __global__ void __launch_bounds__(LR ? 256 : 1024) norm_kernel(const NormArgs A)
         for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[c][i], h[c][i], sum);
     }
     sum = __uint_as_float(row_reduce(OpAdd{}, __float_as_uint(sum)));
+    float ms = sum / float(D) + A.eps;
+    // Where the squares leave float32's range (|h| of 1.8e19 and more, or so small that they lose
+    // bits against eps): h 2^-e and eps 2^-2e in their place, which gives the same y, with 2^e next
+    // above the larger of max |h| and the root of eps. The row's lanes all go this way or none.
+    if (!(ms >= 0x1p-100f && ms < INFINITY)) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int c = 0; c < V; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) most = OpMax::of(most, magnitude(h[c][i]));
+        most = row_reduce(OpMax{}, most);
+        if (most < 0x7F800000u) {                        // (an infinity or a NaN stays as it is)
+            const int eh = most ? __builtin_amdgcn_frexp_expf(__uint_as_float(most)) : -1000;
+            const int ee = A.eps > 0.f ? (__builtin_amdgcn_frexp_expf(A.eps) + 1) >> 1 : -1000;
+            const int e = most || A.eps > 0.f ? max(eh, ee) : 0;
+            sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < V; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[c][i] = __builtin_amdgcn_ldexpf(h[c][i], -e);
+                    sum = __builtin_fmaf(h[c][i], h[c][i], sum);
+                }
+            sum = __uint_as_float(row_reduce(OpAdd{}, __float_as_uint(sum)));
+            ms = sum / float(D) + __builtin_amdgcn_ldexpf(A.eps, -2 * e);
+        }
+    }
     // (a row of zeros without eps: any factor keeps its zeros, 0 * infinity would not)
-    const float ms = sum / float(D) + A.eps;
     const float rstd = ms == 0.f ? 1.f : 1.f / sqrtf(ms);
     // rstd = pow2 * frac, frac in [1, 2): the row's z = h * pow2 * w is rounded once, y = z * frac,
     // and y / scale = z * 448 / max |z| has none of rstd's roundings

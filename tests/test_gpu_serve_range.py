@@ -125,3 +125,55 @@ def test_norm_rows_of_zeros_without_eps(D, dt):
             c = codes.float()
             assert (c[[0, 3]] == 0).all() and (scales[[0, 3]] == 0).all()
             assert (c[[1, 2, 4]] == -448).all() and (scales[[1, 2, 4]] - 2 / 448).abs().max() <= 2 / 448 * 8 * U
+
+
+def check_norm(x, w, eps, group, residual=None):
+    """A row's squares are all positive: their sum is off by a step a value of a lane (64 at
+    most), a step of lanes (6) and a wavefront (16), and y takes half of that and 24 more
+    roundings; y and products below the normal numbers are off by 2^-150 each, 2^-23 of the least
+    scale, three of them; a code by half a step, in doubt by those."""
+    import linear_attn_decode_amd as wb
+    N, D = x.shape
+    assert w is None or float(w.abs().max()) <= 1.9
+    codes = torch.empty((N, D), dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty((N, -(-D // group) if group else 1), device="cuda")
+    out = None if residual is None else torch.empty_like(x)
+    wb.norm_quant(x, w, codes, scales, eps=eps, group=group, residual=residual, residual_out=out)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        h, y, want = O.norm(x.double().cpu().numpy(), None if residual is None else residual.double().cpu().numpy(),
+                            None if w is None else w.double().cpu().numpy(), float(np.float32(eps)), group)
+    zeros = (h == 0).all(1)                                              # (0 / 0 without eps: by the interface, 0)
+    y[zeros], want[zeros] = 0, 0
+    if residual is not None:
+        t = torch.finfo(x.dtype).eps
+        assert (np.abs(out.double().cpu().numpy() - h) <= (t / 2 + 2 * U) * np.abs(h)).all()
+    rel = (86 + 24) * U
+    sc = scales.double().cpu().numpy()
+    # (1 / rms is 2^k in [1, 2) times: h 2^k of 2^-150 and less is 0 in float32, with weights up to
+    # 1.9 here a y of up to 2^-148.07, and a group of such values one of zeros)
+    top = np.stack([np.abs(y[:, i:i + (group or D)]).max(1) for i in range(0, D, group or D)], 1)
+    nothing = (sc == 0) & (top <= 2.0 ** -148)
+    assert (nothing | (np.abs(sc - want) <= (rel + 2 * U) * want)).all(), (sc[:, 0], want[:, 0])
+    q = np.clip(y / np.repeat(np.where(sc > 0, sc, 1.0), group or D, axis=1)[:, :D], -448, 448)
+    err = np.abs(codes.double().cpu().numpy() - q)
+    assert (err <= O.e4m3_half_step(q) + 2 * rel * np.abs(q) + 3 * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 1e-30, 1e-6, 1e30])
+@pytest.mark.parametrize("D", NORM_WIDTHS)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_norm_rows_whose_squares_leave_the_range(dt, D, eps):
+    """Rows near the largest and the smallest numbers, whose squares are infinite or 0 in
+    float32, each beside an ordinary one, and rows that hold both ends."""
+    print(f"[case] norm range {dt} D={D} eps={eps}", flush=True)
+    g = torch.Generator().manual_seed(D)
+    size = [1.0, 2.0 ** 124, 2.0 ** 64, 2.0 ** 63, 1.0, 2.0 ** -48, 2.0 ** -60, 2.0 ** -64, 2.0 ** -75, 2.0 ** -110, 2.0 ** -126,
+            2.0 ** -146 if dt == "f32" else 2.0 ** -130, 1.0]
+    x = (torch.randn((len(size), D), generator=g).clamp(-4, 4).double() * torch.tensor(size, dtype=torch.float64)[:, None]).to(TYPES[dt])
+    x[4, ::3] = 2.0 ** 100
+    x[12, ::3] = 2.0 ** -80
+    w = (1 + 0.3 * torch.rand(D, generator=g)).to(TYPES[dt])
+    check_norm(x.cuda(), w.cuda(), eps, 128)
+    check_norm(x.cuda(), None, eps, 0)
+    check_norm(x.cuda(), w.cuda(), eps, 0, residual=torch.zeros_like(x).cuda())
