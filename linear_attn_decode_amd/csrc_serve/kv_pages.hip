@@ -388,7 +388,7 @@ hipError_t launch_release(const ReleaseArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_append(const AppendArgs& a, hipStream_t s) {
+static hipError_t append(const AppendArgs& a, hipStream_t s) {
     if (a.c.dtype == WB_E4M3) {
         if (a.src == WB_BF16) return append_d<WB_E4M3, WB_BF16>(a, s);
         if (a.src == WB_F16) return append_d<WB_E4M3, WB_F16>(a, s);
@@ -396,6 +396,20 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s) {
     }
     if (a.c.dtype == WB_BF16) return a.src == WB_F32 ? append_d<WB_BF16, WB_F32>(a, s) : append_d<WB_BF16, WB_BF16>(a, s);
     return a.src == WB_F32 ? append_d<WB_F16, WB_F32>(a, s) : append_d<WB_F16, WB_F16>(a, s);
+}
+
+hipError_t launch_append(const AppendArgs& a, hipStream_t s) {
+    const int64_t size = a.src == WB_F32 ? 4 : 2, most = kLaunchItems / (int64_t(a.c.H) * (a.c.D / 8));
+    for (int64_t i0 = 0; i0 < a.N; i0 += most) {
+        AppendArgs b = a;
+        b.N = int(a.N - i0 < most ? a.N - i0 : most);
+        b.k = static_cast<const uint8_t*>(a.k) + i0 * a.k_row * size;
+        b.v = static_cast<const uint8_t*>(a.v) + i0 * a.v_row * size;
+        b.slots = a.slots + i0;
+        const hipError_t e = append(b, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace wb

@@ -290,10 +290,21 @@ hipError_t norm_t(const NormArgs& a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-    if (a.N == 0) return hipSuccess;
-    if (a.dtype == WB_BF16) return norm_t<WB_BF16>(a, s);
-    if (a.dtype == WB_F16) return norm_t<WB_F16>(a, s);
-    return norm_t<WB_F32>(a, s);
+    const int64_t size = a.dtype == WB_F32 ? 4 : 2, groups = a.group ? (a.D + a.group - 1) / a.group : 1;
+    const int64_t most = kLaunchItems / 1024 * (a.D <= 512 ? 16 : 1);      // (64 lanes a row, or a workgroup)
+    auto shifted = [](const void* p, int64_t bytes) { return p ? static_cast<const uint8_t*>(p) + bytes : nullptr; };
+    for (int64_t n0 = 0; n0 < a.N; n0 += most) {
+        NormArgs b = a;
+        b.N = int(a.N - n0 < most ? a.N - n0 : most);
+        b.x = shifted(a.x, n0 * a.x_row * size);
+        b.residual = shifted(a.residual, n0 * a.r_row * size);
+        b.residual_out = const_cast<uint8_t*>(shifted(a.residual_out, n0 * a.ro_row * size));
+        b.codes = a.codes + n0 * a.c_row;
+        b.scales = a.scales + n0 * groups;
+        const hipError_t e = a.dtype == WB_BF16 ? norm_t<WB_BF16>(b, s) : a.dtype == WB_F16 ? norm_t<WB_F16>(b, s) : norm_t<WB_F32>(b, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace wb

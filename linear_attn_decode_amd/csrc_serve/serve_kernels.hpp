@@ -8,6 +8,10 @@
 
 namespace wb {
 
+// Work-items of one launch of the kernels that take some for each row or vector, at most: a grid's
+// dimension holds fewer than 2^32. More rows go in several launches.
+constexpr int64_t kLaunchItems = int64_t(1) << 31;
+
 struct PlanArgs {
     const int32_t* lens = nullptr;
     const int32_t* more = nullptr;

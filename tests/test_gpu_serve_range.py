@@ -177,3 +177,58 @@ def test_norm_rows_whose_squares_leave_the_range(dt, D, eps):
     check_norm(x.cuda(), w.cuda(), eps, 128)
     check_norm(x.cuda(), None, eps, 0)
     check_norm(x.cuda(), w.cuda(), eps, 0, residual=torch.zeros_like(x).cuda())
+
+
+# ---------------------------------------------------------------------------- sizes
+@pytest.fixture
+def large():
+    """Memory for tests of many rows, given back behind them."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("needs 130 GB of free GPU memory")
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("N,D", [(2 ** 29 + 5, 1), (2 ** 28 + 1, 65), (2 ** 26 + 3, 513)])
+def test_norm_of_more_rows_than_a_grid_dimension_holds(large, N, D):
+    """8, 16 and 64 lanes a row, 2^32 of them and more: rows of zeros, but for some."""
+    import linear_attn_decode_amd as wb
+    print(f"[case] norm N={N} D={D}", flush=True)
+    x = torch.zeros((N, D), dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, 2 ** 25 - 1, 2 ** 25, N // 2, N - 2, N - 1]
+    for i, r in enumerate(at):
+        x[r] = i + 1
+    codes = torch.empty((N, D), dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.full((N, 1), math.nan, device="cuda")
+    wb.norm_quant(x, None, codes, scales, eps=0.0)
+    torch.cuda.synchronize()
+    assert int((scales == 0).sum()) == N - len(at)
+    for r in at:
+        # (y is 1 but for the roundings of the sum, the root and the products: 110 u, as above)
+        assert abs(float(scales[r]) * 448 - 1) <= 112 * U and (codes[r].float() == 448).all()
+    for r in {2, 3, 2 ** 25 + 1, N - 3} - set(at):
+        assert (codes[r].float() == 0).all()
+
+
+def test_append_of_more_vectors_than_a_grid_dimension_holds(large):
+    """2^27 vectors of 32 lanes and more, all but some of them padding. (Keys and values are the
+    same memory here: they are only read.)"""
+    import linear_attn_decode_amd as wb
+    N, H, D, page = 2 ** 21 + 9, 64, 256, 8
+    print(f"[case] append N={N} H={H} D={D}", flush=True)
+    k = torch.empty((N, H, D), dtype=torch.bfloat16, device="cuda")
+    slots = torch.full((N,), -1, dtype=torch.int64, device="cuda")
+    at = [0, 5, 2 ** 20, 2 ** 21 - 1, 2 ** 21, N - 1]
+    g = torch.Generator().manual_seed(51)
+    new = torch.randn((len(at), H, D), generator=g).bfloat16().cuda()
+    for i, r in enumerate(at):
+        k[r] = new[i]
+        slots[r] = 2 * i + 1
+    kc, vc = (torch.full((2, H, page, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    wb.kv_append(k, k, kc, vc, slots)
+    torch.cuda.synchronize()
+    want = torch.full((2 * page, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    want[torch.arange(len(at)).cuda() * 2 + 1] = new
+    want = want.view(2, page, H, D).transpose(1, 2)
+    assert torch.equal(kc, want) and torch.equal(vc, want)
