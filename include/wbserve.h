@@ -7,10 +7,11 @@
  * Conventions are those of wbstate.h: status codes WB_*, caller-owned device memory (the
  * library never allocates), arguments validated on the host before anything is enqueued,
  * asynchronous execution on `stream` (a hipStream_t of the current device, which must be
- * the device of every pointer). No call synchronises the host, keeps state between calls
- * or uses memory that was not passed to it, so calls on different streams are independent
- * and every call can be captured into a graph; what a captured call reads (lengths, page
- * tables, free pages) may change between replays.
+ * the device of every pointer). No call synchronises the host, keeps anything of its inputs
+ * or outputs for the next or uses device memory that was not passed to it, so calls on
+ * different streams are independent and every call can be captured into a graph; what a
+ * captured call reads (lengths, page tables, free pages) may change between replays. (The
+ * process counts the calls of kv_attend: a call marks its workspace with its number.)
  *
  * Stored keys and values: one array each, [pages][H][page][D], D contiguous: the tokens
  * of a page are contiguous for each key-value head. Token t of request r is token
@@ -59,8 +60,8 @@ typedef struct wb_kv_cache {
  *   *status = 0.
  * lens_out may be lens and n_free_out may be n_free. Other table entries and the free
  * array are not written. lens, more, lens_out: int32 [R]; table: int32 [R][width];
- * free: int32 [free_size]; starts: int32 [R + 1]; slots: int64 [n_slots]; n_free,
- * n_free_out, status: int32 [1]; work: int32 [R], needed when kv_plan_work() says so.
+ * free: int32 [free_size]; starts: int32 [R + 1]; slots: int64 [n_slots], 16-byte aligned;
+ * n_free, n_free_out, status: int32 [1]; work: int32 [R], needed when kv_plan_work() says so.
  * All or nothing: a plan that cannot be carried out sets *status to the first of
  *   1  a negative length, a negative count of new tokens, or *n_free outside [0, free_size]
  *   2  a request would need more than `width` pages
@@ -111,10 +112,10 @@ int kv_append(const wb_kv_cache* c, const void* k, const void* v, int64_t k_row,
  * [0, pages) in the range it reads, has o = lse = NaN. Results do not depend on timing: equal
  * calls give equal bits.
  * q [R][Hq][D] of type q_dtype (the cache's, or WB_BF16 / WB_F16 for an 8-bit cache), strides
- * q_row and q_head in elements, multiples of 8; o [R][Hq][D] contiguous, of q's type; table
- * int32 [R][width]; lens int32 [R]. `work` has kv_attend_work() bytes (NULL if 0), 16-byte
- * aligned, whatever they hold, and belongs to the call until it has run. No output overlaps
- * an input. 1 <= R <= 65536, Hq a multiple of H and at most 4096, width * page at most 2^30. */
+ * q_row and q_head in elements, multiples of 8; o [R][Hq][D] contiguous, of q's type; q and o
+ * 16-byte aligned; table int32 [R][width]; lens int32 [R]. `work` has kv_attend_work() bytes
+ * (NULL if 0), 16-byte aligned, whatever they hold, and belongs to the call until it has run.
+ * No output overlaps an input. 1 <= R <= 65536, Hq a multiple of H and at most 4096, width * page at most 2^30. */
 int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head, int q_dtype, int R, int Hq,
               const int32_t* table, int width, const int32_t* lens, float scale, int window, void* o, float* lse,
               void* work, size_t work_bytes, void* stream);

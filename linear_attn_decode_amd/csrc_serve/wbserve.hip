@@ -1,5 +1,5 @@
 // Host side of the serving operators' C ABI (include/wbserve.h): argument checks and
-// dispatch. No device memory is allocated and nothing is kept between calls.
+// dispatch. No device memory is allocated, and nothing of a call is kept for the next.
 #include <time.h>
 #include <unistd.h>
 

@@ -183,8 +183,8 @@ def plan_pages(lens, more, table, free, n_free, page: int, slots, starts, status
                stream=None):
     """Places ``more[r]`` new tokens behind the ``lens[r]`` stored ones of each request:
     pages are popped off the stack ``free[:n_free]`` (topmost first, request by request)
-    into ``table`` (int32 [R, width]), ``slots`` (int64 [n]) gets each new token's slot in
-    request order and -1 behind the last, ``starts`` (int32 [R + 1]) each request's first
+    into ``table`` (int32 [R, width]), ``slots`` (int64 [n], 16-byte aligned) gets each new
+    token's slot in request order and -1 behind the last, ``starts`` (int32 [R + 1]) each request's first
     new token. ``lens_out`` and ``n_free_out`` get the new lengths and number of free pages
     (default: in place). int32 [R]: lens, more; int32 [1]: n_free, status. All or nothing:
     ``status`` becomes 0, or 1 (a negative count, ``n_free`` out of range), 2 (more pages
@@ -250,8 +250,8 @@ def release_pages(ended, lens, table, free, n_free, page: int, status, stream=No
 
 
 def kv_append(k, v, k_cache, v_cache, slots, k_scale=None, v_scale=None, stream=None):
-    """Writes keys and values of new tokens, ``k``, ``v`` [N, H, D] (rows may be strided), at
-    ``slots`` (int64 [N]) of the cache; tokens with a slot outside the cache (-1: padding)
+    """Writes keys and values of new tokens, ``k``, ``v`` [N, H, D] (rows may be strided, all
+    16-byte aligned), at ``slots`` (int64 [N]) of the cache; tokens with a slot outside the cache (-1: padding)
     are not stored, and no slot is given twice. They are of the cache's type or float32, for a float8_e4m3fn cache also
     bfloat16 or float16: each vector is then stored as max|x| / 448 and the nearest codes."""
     c, dev, shape, _ = _cache(k_cache, v_cache, k_scale, v_scale)
@@ -279,7 +279,8 @@ def kv_attend(q, k_cache, v_cache, table, lens, o, scale=None, window: int = 0, 
     """Attention of one new token per request over its stored tokens (the last ``window``
     of them; 0: all): ``o`` [R, Hq, D] = softmax(scale q k^T) v, ``lse`` (float32 [R, Hq],
     optional) the log-sum-exp of its scores. ``q`` [R, Hq, D] is of the cache's type
-    (bfloat16 or float16 for a float8_e4m3fn cache), requests and heads may be strided;
+    (bfloat16 or float16 for a float8_e4m3fn cache), requests and heads may be strided (by
+    multiples of 8; ``q`` and ``o`` are 16-byte aligned);
     query head h reads key-value head h // (Hq // H). ``table`` int32 [R, width], ``lens``
     int32 [R]: the stored tokens of each request, the new one's among them. ``scale``
     defaults to 1 / sqrt(D). A request without tokens has o = 0 and lse = -inf; one whose
