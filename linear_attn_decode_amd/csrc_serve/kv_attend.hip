@@ -129,10 +129,12 @@ __device__ __forceinline__ Run find_run(const AttendArgs& A) {
 }
 
 // Wavefronts a SIMD holds, which is workgroups a compute unit holds. 16 KB of tile in flight a
-// wavefront saturate HBM with one each (64 ragged requests of 128 columns: 74.4 us with one,
-// 76.3 with two, 93 with three, which spills); smaller tiles want more of them (64 columns:
-// 21.9 us with three, 22.8 with two, 27.8 with one; e4m3 at 128 columns: 153 us with two, 177
-// with one, whose conversions nothing overlaps).
+// wavefront saturate HBM with one each (64 ragged requests of 128 bfloat16 columns: 73.1 us with
+// one, 75.6 with two, 85.0 with three); smaller tiles and conversions want more of them. 64
+// columns with three, two and one: 256 ragged e4m3 requests to 4096 tokens 91.5, 96.2 and 142 us,
+// 100 float16 windows of 1024 tokens 61.0, 61.8 and 77.2, 64 ragged bfloat16 requests 43.8, 42.9
+// and 47.1. e4m3 with two and one: 128 columns 153.4 and 176.5 us, 256 columns 91.5 and 95.5 with
+// a bfloat16 query, but 118.2 and 106.3 with the two limbs of a float16 one.
 constexpr int waves_per_simd(int kv, int qt, int D) {
     if (D == 64) return 3;
     if (kv == WB_E4M3) return D == 128 || qt == WB_BF16 ? 2 : 1;
@@ -244,7 +246,7 @@ __device__ __forceinline__ Parts parts_of(const AttendArgs& A, int r, int hb) {
 // card's scope, past the caches that its compute dies do not share: a wavefront whose stores
 // have completed then needs no write-back of its die's cache before others may read them, nor
 // they an invalidation of theirs. (With fences, which do both for the whole cache, the batch of
-// 64 ragged requests takes 180 us, not 73.)
+// 64 ragged requests takes 162 us, not 73.)
 template <bool HERE>
 __device__ __forceinline__ void put_part(float* p, f32x2 v) {
     if constexpr (HERE)
@@ -765,9 +767,10 @@ hipError_t attend_t(const AttendArgs& a, hipStream_t s) {
 // of blocks), and the one that comes last joins their parts: above kPartsJoined of them for
 // each lane that costs more than a second launch of many workgroups. 32 query and 8 key-value
 // heads of 128 columns, joined by the last workgroup / by a second launch: 1 request of 237
-// tokens 9.2 / 11.7 us, 1 of 8000 (16 parts a lane) 13.3 / 13.4, 8 to 512 tokens 9.7 / 12.2, 32
-// to 1024 18.0 / 22.6, 64 to 4096 73.5 / 74.5; 20 heads of 64 columns, 24 windows of 1024: 20.7
-// / 21.9; 4 key-value heads of 256 columns, 1 request of 8000 (128 parts a lane): 53 / 16.
+// tokens 9.3 / 12.0 us, 1 of 8000 (16 parts a lane) 15.1 / 15.4, 8 to 512 tokens 9.3 / 12.1, 32
+// to 1024 17.7 / 21.6, 64 to 4096 73.0 / 74.8; 20 heads of 64 columns, 24 windows of 1024: 20.1
+// / 21.6; 1 request of 8000 with 32 query and 4 key-value heads of 256 columns 55.3 / 18.6, with
+// 64 query heads (128 parts a lane) 88.2 / 19.7.
 constexpr int kPartsJoined = 32;
 
 // As many workgroups as the card's 256 compute units hold at once, and no more than all

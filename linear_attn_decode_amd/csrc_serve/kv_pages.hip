@@ -14,8 +14,8 @@ namespace {
 //     and writes its share of the slots; the first also writes the rest.
 //   * Otherwise one workgroup takes the sums, which may be in place, and a second launch of many
 //     workgroups writes the slots, with the pages before each request in `work`.
-// Measured for 256 requests and 700 419 new tokens: 7.6 us in the second form, 13 us in the
-// third (5.9 and 6.9 us of kernels and a gap).
+// Measured for 256 requests and 700 419 new tokens, in a graph: 7.3 us in the second form, 13.1
+// us in the third (kernels of 4.9 and 9.7 us in a trace, 8.2 of the second form).
 constexpr int kPlanRows = 1024;        // requests whose sums are kept in LDS
 constexpr int64_t kPlanSlots = 4096;
 constexpr int kFillPerThread = 8, kFillThreads = 256;
@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kReleaseThreads) release_kernel(const ReleaseA
 // rows are read in order. Bound by HBM: every input value is read once and every stored byte
 // written once, past the caches (what a decode step reads back of it is one token a request);
 // the vector's maximum is taken by lane exchanges inside its D / 8 lanes. 65536 tokens of 8
-// heads of 128 columns into an e4m3 cache: 77.8 us, 5.23 TB/s (80.4 us with ordinary stores,
-// 92 us with keys and values in workgroups of their own; a copy of 4 GiB runs at 4.73 TB/s).
+// heads of 128 columns into an e4m3 cache: 77.6 us, 5.25 TB/s (80.8 us with ordinary stores,
+// 92.4 us with keys and values in workgroups of their own; a copy of 4 GiB runs at 4.7 TB/s).
 template <int SRC>
 __device__ __forceinline__ void load8(const void* p, int64_t at, float x[8]) {
     if constexpr (SRC == WB_F32) {

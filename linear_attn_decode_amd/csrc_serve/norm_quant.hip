@@ -6,13 +6,13 @@
 // of a group are 16 neighbouring lanes of one chunk, so a group's maximum is four DPP steps.
 // Rows of up to 512 columns take 8, 16, 32 or 64 lanes, several rows a wavefront; wider ones a
 // workgroup of as many wavefronts as their chunks need, two chunks a lane (8191 rows of 5000
-// bfloat16 columns with a residual: 60.1 us, 4.79 TB/s, the rate of a copy; 66.5 us with one
-// chunk, 63.0 with three, 72.1 with four; 56.8 us with stores past the caches, which cost the
-// kernel that reads them next 7 us). Strides and alignment are free: the
+// bfloat16 columns with a residual: 60.2 us, 4.78 TB/s, the rate of a copy; 68 us with one
+// chunk, 65 with three, 73 with four; 2 us less with stores past the caches, but 8192 rows of
+// 4096 and the two kernels that read their outputs next then take 78.9 us together, not 74.4). Strides and alignment are free: the
 // 16-byte accesses need only the element's alignment on this hardware, and the chunk that
 // holds a row's ragged end goes by 4, 2 and 1 columns (bfloat16 with a residual: 400000 rows of
-// 100 columns 80.9 us, 109 by single elements; 2352941 rows of 17 179 us, and 305 by single
-// elements with 16 lanes a row; 312500 rows of 128 51.4 us).
+// 100 columns 78.5 us, 109 by single elements; 2352941 rows of 17 174 us, and 305 by single
+// elements with 16 lanes a row; 312500 rows of 128 53.1 us).
 #include "serve_device.hpp"
 
 namespace wb {
