@@ -343,7 +343,7 @@ def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, resi
     w = x if weight is None else weight
     if (r.dtype is kind and out.dtype is kind and w.dtype is kind and codes.dtype is f8 and scales.dtype is f32
             and r.shape == shape and out.shape == shape and codes.shape == shape and scales.shape == (N, groups)
-            and (w is x or w.shape == (D,))
+            and (weight is None or w.shape == (D,))
             and r.get_device() == out.get_device() == w.get_device() == codes.get_device() == scales.get_device() == dev
             and x.is_contiguous() and r.is_contiguous() and out.is_contiguous() and w.is_contiguous()
             and codes.is_contiguous() and scales.is_contiguous()):
@@ -353,7 +353,7 @@ def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, resi
         r_row = _rows(r, "residual", kind, shape, dev, D)[1]
         ro_row = _rows(out, "residual_out", kind, shape, dev, D)[1]
         c_row = _rows(codes, "codes", f8, shape, dev, D)[1]
-        if w is not x:
+        if weight is not None:
             _ptr(w, "weight", kind, (D,), dev)
         _ptr(scales, "scales", f32, (N, groups), dev)
     have = residual is not None

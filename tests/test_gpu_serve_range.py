@@ -179,6 +179,16 @@ def test_norm_rows_whose_squares_leave_the_range(dt, D, eps):
     check_norm(x.cuda(), w.cuda(), eps, 0, residual=torch.zeros_like(x).cuda())
 
 
+def test_norm_weight_that_is_the_rows_is_refused():
+    """A weight is [D], also where the rows themselves are given for one."""
+    import linear_attn_decode_amd as wb
+    wide = torch.ones((2, 16), device="cuda")
+    for x in (wide, wide[:, :8], wide[:1]):
+        codes, scales = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty((x.shape[0], 1), device="cuda")
+        with pytest.raises(ValueError, match="weight"):
+            wb.norm_quant(x, x, codes, scales)
+
+
 # ---------------------------------------------------------------------------- sizes
 @pytest.fixture
 def large():
