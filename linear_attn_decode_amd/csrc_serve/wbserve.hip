@@ -192,6 +192,7 @@ int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head
         if (work_bytes < need) return WB_ESIZE;
         if (!aligned(work, 16)) return WB_EALIGN;
     }
+    if (o == q) return WB_EINVAL;      // (a split request's query is read where another part has finished)
     wb::AttendArgs a;
     a.c = *c;
     a.q = q;

@@ -189,7 +189,7 @@ def plan_pages(lens, more, table, free, n_free, page: int, slots, starts, status
     (default: in place). int32 [R]: lens, more; int32 [1]: n_free, status. All or nothing:
     ``status`` becomes 0, or 1 (a negative count, ``n_free`` out of range), 2 (more pages
     than ``table`` is wide), 3 (more new tokens than ``slots``), 4 (not enough free pages),
-    and then nothing is placed and every slot is -1."""
+    and then nothing is placed and every slot is -1. Other outputs overlap no input."""
     if _torch is None:
         _load()
     if not -_MAX <= page <= _MAX:         # (ctypes would pass its lower 32 bits)
@@ -284,7 +284,7 @@ def kv_attend(q, k_cache, v_cache, table, lens, o, scale=None, window: int = 0, 
     query head h reads key-value head h // (Hq // H). ``table`` int32 [R, width], ``lens``
     int32 [R]: the stored tokens of each request, the new one's among them. ``scale``
     defaults to 1 / sqrt(D). A request without tokens has o = 0 and lse = -inf; one whose
-    length or page ids are out of range has NaN."""
+    length or page ids are out of range has NaN. ``o`` is not ``q``: outputs overlap no input."""
     c, dev, shape, code = _cache(k_cache, v_cache, k_scale, v_scale)
     kind = q.dtype
     if q.dim() != 3 or table.dim() != 2 or kind not in _codes:
@@ -319,7 +319,7 @@ def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, resi
     ``scales`` (float32 [N, groups]) gets max|y| / 448 of each 128 columns (``group`` 128)
     or of each row (``group`` 0) and ``codes`` (float8_e4m3fn [N, D]) y / scale. ``x``,
     ``residual``, ``weight`` ([D], or None for 1) are of one type: bfloat16, float16 or
-    float32; rows may be strided."""
+    float32; rows may be strided. Other outputs overlap no input."""
     if _torch is None:
         _load()
     if not -_MAX <= group <= _MAX:        # (the library would take its lower 32 bits, and write their number of scales)

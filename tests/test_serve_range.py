@@ -4,6 +4,7 @@ import ctypes
 import pytest
 
 import linear_attn_decode_amd as wb
+from linear_attn_decode_amd import serve
 
 torch = pytest.importorskip("torch")
 
@@ -25,3 +26,13 @@ def test_pages_past_32_bits_are_refused(page):
         wb.plan_pages(n, n, table, n, one, page, torch.zeros(1, dtype=torch.int64), torch.zeros(2, dtype=torch.int32), one)
     with pytest.raises(ValueError, match="page: .* is out of range"):
         wb.release_pages(n, n, table, n, one, page, one)
+
+
+def test_attention_into_its_own_query_is_refused():
+    """Parts of a split request would read the query where another workgroup has stored the row.
+    (The address is never used: the call is refused behind every other check.)"""
+    h = ctypes.CDLL(wb.LIB_PATH)
+    h.kv_attend.restype, h.kv_attend.argtypes = wb.SERVE_SIGNATURES["kv_attend"]
+    A = 0x100000
+    c = wb.KVCacheDesc(A, A, None, None, 10, 16, 4, 128, serve.BF16)
+    assert h.kv_attend(c, A, 1024, 128, serve.BF16, 2, 8, A, 8, A, 1.0, 0, A, None, None, 0, None) == -1
