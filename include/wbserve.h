@@ -1,8 +1,8 @@
 /*
  * wbserve.h -- C ABI of the serving operators around the recurrent-state layers of a
  * hybrid language model (MI355X, gfx950): the paged key-value cache of its
- * full-attention layers (page planning, cache writes, attention of one new token) and
- * the root-mean-square norm whose output is stored in 8 bits.
+ * full-attention layers (page planning, cache writes, attention of one new token and of
+ * chunks of them) and the root-mean-square norm whose output is stored in 8 bits.
  *
  * Conventions are those of wbstate.h: status codes WB_*, caller-owned device memory (the
  * library never allocates), arguments validated on the host before anything is enqueued,
@@ -122,6 +122,37 @@ int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head
 
 /* Bytes of workspace of kv_attend. Host only. */
 int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes);
+
+/* Attention of chunks of new tokens over the requests' stored tokens, the new ones among them
+ * (kv_append has stored them): whole prompts, parts of prompts, drafted tokens and single tokens
+ * in one call. Request r's m = starts[r + 1] - starts[r] new tokens are rows starts[r] ..
+ * starts[r + 1] - 1 of q and o and the last m of its n = lens[r] stored ones (starts and lens as
+ * kv_plan_pages gives them): row starts[r] + i has position p = n - m + i, and head h, which reads
+ * key-value head h / (Hq / H), sees t in [max(0, p + 1 - window), p] (window 0: [0, p]):
+ *   s_t = scale * q[row][h] . k_t,  o[row][h] = sum_t e^{s_t} v_t / sum_t e^{s_t},
+ *   lse[row][h] = log sum_t e^{s_t} (float32 [N][Hq], or NULL).
+ * Scores, maxima and sums are float32. The weights e^{s_t - ref} (ref within 4 / log2(e) of the
+ * running maximum; times the value's scale, for an 8-bit cache) enter the product with v rounded
+ * to 16 bits of the cache's type (within 2^-8 of each weight in bfloat16, 2^-11 and 2^-36 of the
+ * largest in float16), for a float16 q over an 8-bit cache as two bfloat16 limbs (2^-16); o is
+ * rounded once. A row whose scores are all -infinity has o = 0 and lse = -infinity. Stored values
+ * that a row does not see leave no trace in it, whatever they hold; a NaN that it sees gives NaN,
+ * an infinity what the formula gives or NaN. A request with a length outside [m, width * page] has
+ * o = lse = NaN, and so has a row that sees a token of a page id outside [0, pages) (other rows of
+ * its request may). A request whose starts decrease or leave [0, N] has no rows; rows of no
+ * request are left as they were. Equal calls give equal bits.
+ * q [N][Hq][D] of type q_dtype (the cache's, or WB_BF16 / WB_F16 for an 8-bit cache), strides
+ * q_row and q_head in elements, multiples of 8; o [N][Hq][D] contiguous, of q's type; q and o
+ * 16-byte aligned; table int32 [R][width]; lens int32 [R]; starts int32 [R + 1]. `work` has
+ * kv_attend_chunk_work() bytes (NULL if 0), 16-byte aligned, whatever they hold, and belongs to
+ * the call until it has run. No output overlaps an input. N >= 0, N * Hq below 2^31; R, Hq and
+ * width as for kv_attend. */
+int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head, int q_dtype, int N, int R, int Hq,
+                    const int32_t* table, int width, const int32_t* lens, const int32_t* starts, float scale, int window,
+                    void* o, float* lse, void* work, size_t work_bytes, void* stream);
+
+/* Bytes of workspace of kv_attend_chunk. Host only. */
+int kv_attend_chunk_work(const wb_kv_cache* c, int N, int R, int Hq, int width, size_t* bytes);
 
 /* Root-mean-square norm with an 8-bit output: for each of N rows of D columns
  *   h = x + residual (float32; residual NULL: h = x), residual_out = h rounded to residual's type,

@@ -51,6 +51,13 @@ int check_attend(const wb_kv_cache* c, int R, int Hq, int width) {
     return Hq > kMaxQueryHeads ? WB_EUNSUPPORTED : WB_OK;
 }
 
+int check_chunk(const wb_kv_cache* c, int N, int R, int Hq, int width) {
+    const int v = check_attend(c, R, Hq, width);
+    if (v) return v;
+    if (N < 0) return WB_EINVAL;
+    return int64_t(N) * Hq > 0x7FFFFFFF ? WB_EUNSUPPORTED : WB_OK;
+}
+
 size_t work_bytes_of(const wb::AttendPlan& p) {
     return p.part_o_bytes + p.part_ml_bytes + p.spans_bytes + p.arrivals_bytes;
 }
@@ -225,6 +232,70 @@ int kv_attend(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head
     a.head_blocks = p.head_blocks;
     a.groups = p.groups;
     return hip_status(wb::launch_attend(a, static_cast<hipStream_t>(stream)));
+}
+
+int kv_attend_chunk_work(const wb_kv_cache* c, int N, int R, int Hq, int width, size_t* bytes) {
+    if (!bytes) return WB_EINVAL;
+    const int v = check_chunk(c, N, R, Hq, width);
+    if (v) return v;
+    const wb::ChunkPlan p = wb::chunk_plan(*c, N, R, Hq, width);
+    *bytes = p.part_o_bytes + p.part_ml_bytes;
+    return WB_OK;
+}
+
+int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t q_head, int q_dtype, int N, int R, int Hq,
+                    const int32_t* table, int width, const int32_t* lens, const int32_t* starts, float scale, int window,
+                    void* o, float* lse, void* work, size_t work_bytes, void* stream) {
+    const int v = check_chunk(c, N, R, Hq, width);
+    if (v) return v;
+    if (window < 0) return WB_EINVAL;
+    if (q_dtype != WB_BF16 && q_dtype != WB_F16) return WB_EINVAL;
+    if (c->dtype != WB_E4M3 && q_dtype != c->dtype) return WB_EUNSUPPORTED;
+    if (N == 0) return WB_OK;
+    if (!q || !table || !lens || !starts || !o) return WB_EINVAL;
+    if (!aligned(q, 16) || !aligned(o, 16) || q_row % 8 || q_head % 8 || !aligned(table, 4) || !aligned(lens, 4) ||
+        !aligned(starts, 4) || !aligned(lse, 4))
+        return WB_EALIGN;
+    const wb::ChunkPlan p = wb::chunk_plan(*c, N, R, Hq, width);
+    const size_t need = p.part_o_bytes + p.part_ml_bytes;
+    if (need) {
+        if (!work) return WB_EINVAL;
+        if (work_bytes < need) return WB_ESIZE;
+        if (!aligned(work, 16)) return WB_EALIGN;
+    }
+    if (o == q) return WB_EINVAL;      // (a block's queries are read where another part has finished)
+    wb::ChunkArgs a;
+    a.c = *c;
+    a.q = q;
+    a.q_row = q_row;
+    a.q_head = q_head;
+    a.table = table;
+    a.lens = lens;
+    a.starts = starts;
+    a.o = o;
+    a.lse = lse;
+    if (need) {
+        a.part_o = static_cast<float*>(work);
+        a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + p.part_o_bytes);
+    }
+    a.scale = scale;
+    a.N = N;
+    a.R = R;
+    a.Hq = Hq;
+    a.width = width;
+    a.window = window;
+    a.q_dtype = q_dtype;
+    a.page_log2 = page_log2(c->page);
+    a.G = Hq / c->H;
+    a.rows = p.rows;
+    a.heads = p.heads;
+    a.tokens = p.tokens;
+    a.head_blocks = p.head_blocks;
+    a.part_tiles = p.part_tiles;
+    a.target = p.target;
+    a.slots = p.slots;
+    a.groups = p.groups;
+    return hip_status(wb::launch_chunk(a, static_cast<hipStream_t>(stream)));
 }
 
 int norm_quant(const void* x, int64_t x_row, const void* residual, int64_t r_row, void* residual_out, int64_t ro_row,

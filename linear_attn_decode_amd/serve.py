@@ -39,6 +39,8 @@ SERVE_SIGNATURES = {
     "kv_append": (_I, [_C, _P, _P, _I64, _I64, _I, _P, _I, _P]),
     "kv_attend": (_I, [_C, _P, _I64, _I64, _I, _I, _I, _P, _I, _P, _F, _I, _P, _P, _P, _SZ, _P]),
     "kv_attend_work": (_I, [_C, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "kv_attend_chunk": (_I, [_C, _P, _I64, _I64, _I, _I, _I, _I, _P, _I, _P, _P, _F, _I, _P, _P, _P, _SZ, _P]),
+    "kv_attend_chunk_work": (_I, [_C, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "norm_quant": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I, _I, _I, _F, _I, _P, _I64, _P, _P]),
 }
 
@@ -179,6 +181,16 @@ def _attend_work(code, pages, H, page, D, R, Hq, width):
     return need.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _chunk_work(code, pages, H, page, D, N, R, Hq, width):
+    """Workspace bytes of kv_attend_chunk, which follow from the sizes alone."""
+    fake, need = 16, _SZ()
+    scale = fake if code == E4M3 else 0
+    _check(_fn["kv_attend_chunk_work"](_desc.pack(fake, fake, scale, scale, pages, page, H, D, code), N, R, Hq, width,
+                                       ctypes.byref(need)), "kv_attend_chunk")
+    return need.value
+
+
 def plan_pages(lens, more, table, free, n_free, page: int, slots, starts, status, lens_out=None, n_free_out=None,
                stream=None):
     """Places ``more[r]`` new tokens behind the ``lens[r]`` stored ones of each request:
@@ -310,6 +322,46 @@ def kv_attend(q, k_cache, v_cache, table, lens, o, scale=None, window: int = 0, 
     _call("kv_attend", dev, c, q.data_ptr(), q_row if R > 1 else 0, q_head if Hq > 1 else 0, _codes[kind], R, Hq,
           table.data_ptr(), width, lens.data_ptr(), D ** -0.5 if scale is None else scale, window if window < _MAX else 0,
           o.data_ptr(), lsep, held.data_ptr() if n else None, n, _stream_of(dev, stream))
+
+
+def kv_attend_chunk(q, k_cache, v_cache, table, lens, starts, o, scale=None, window: int = 0, lse=None, k_scale=None,
+                    v_scale=None, stream=None):
+    """Attention of chunks of new tokens (prompts, parts of them, drafted tokens, single tokens) over
+    the stored ones, which they are the last of: rows ``starts[r]`` .. ``starts[r + 1] - 1`` of ``q``
+    [N, Hq, D] are request r's, and each sees the stored tokens up to its own (the last ``window`` of
+    them; 0: all). ``o`` [N, Hq, D] = softmax(scale q k^T) v, ``lse`` (float32 [N, Hq], optional) the
+    log-sum-exp of the scores. ``starts`` (int32 [R + 1]) and ``lens`` (int32 [R]) are what ``plan_pages``
+    gives; the new tokens have been stored by ``kv_append``. Types, strides and alignment of ``q``,
+    ``table`` and the cache, and ``scale``, as for ``kv_attend``. Rows of no request are left as they were;
+    a request whose length is out of range, or rows that see a page id out of range, have NaN.
+    Outputs overlap no input."""
+    c, dev, shape, code = _cache(k_cache, v_cache, k_scale, v_scale)
+    kind = q.dtype
+    if q.dim() != 3 or table.dim() != 2 or kind not in _codes:
+        raise ValueError(f"q, table: expected [N, Hq, D] and [R, width], got {kind} {tuple(q.shape)}, {tuple(table.shape)}")
+    N, Hq, D = q.shape
+    pages, H, page, d = shape
+    q_row, q_head, q_col = q.stride()
+    if q.get_device() != dev or D != d or q_col != 1:
+        _refuse(q, "q", f"[N, Hq, {d}] with contiguous heads", dev)
+    R, width = table.shape
+    if N > _MAX or Hq > _MAX or R > _MAX or width > _MAX or not 0 <= window:
+        raise ValueError(f"q, table, window: {tuple(q.shape)}, {tuple(table.shape)}, {window} are out of range")
+    i32 = _torch.int32
+    if not (table.dtype is i32 and lens.dtype is i32 and starts.dtype is i32 and o.dtype is kind and lens.shape == (R,)
+            and starts.shape == (R + 1,) and o.shape == (N, Hq, D)
+            and table.get_device() == lens.get_device() == starts.get_device() == o.get_device() == dev
+            and table.is_contiguous() and lens.is_contiguous() and starts.is_contiguous() and o.is_contiguous()):
+        _ptr(table, "table", i32, (R, width), dev)
+        _ptr(lens, "lens", i32, (R,), dev)
+        _ptr(starts, "starts", i32, (R + 1,), dev)
+        _ptr(o, "o", kind, (N, Hq, D), dev)
+    lsep = None if lse is None else _ptr(lse, "lse", _torch.float32, (N, Hq), dev)
+    n = _chunk_work(code, pages, H, page, D, N, R, Hq, width)
+    held = _workspace(n, _torch.uint8, dev, stream) if n else None
+    _call("kv_attend_chunk", dev, c, q.data_ptr(), q_row if N > 1 else 0, q_head if Hq > 1 else 0, _codes[kind], N, R, Hq,
+          table.data_ptr(), width, lens.data_ptr(), starts.data_ptr(), D ** -0.5 if scale is None else scale,
+          window if window < _MAX else 0, o.data_ptr(), lsep, held.data_ptr() if n else None, n, _stream_of(dev, stream))
 
 
 def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, residual=None, residual_out=None,

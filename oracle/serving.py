@@ -103,6 +103,30 @@ def attend(q, k, v, scale, window=0):
     return o, lse, w, size
 
 
+def attend_chunk(q, k, v, scale, window=0):
+    """One request's chunk: q [m, Hq, D] its last m tokens, k and v [n, H, D] its stored ones. Returns
+    (o [m, Hq, D], lse [m, Hq], mean |v| under the weights [m, Hq, D], sum |scale q k| at most [m, Hq]),
+    all of what each token sees."""
+    m, Hq, D = q.shape
+    n, H, _ = k.shape
+    o, w = np.zeros((m, Hq, D)), np.zeros((m, Hq, D))
+    lse, size = np.full((m, Hq), -np.inf), np.zeros((m, Hq))
+    at, t = np.arange(n - m, n)[:, None], np.arange(n)[None, :]
+    hidden = t > at if not window else (t > at) | (t <= at - window)
+    for h in range(Hq):
+        kh, vh = k[:, h // (Hq // H)], v[:, h // (Hq // H)]
+        s = np.where(hidden, -np.inf, scale * (q[:, h] @ kh.T))
+        size[:, h] = np.where(hidden, 0, abs(scale) * (np.abs(q[:, h]) @ np.abs(kh).T)).max(1, initial=0)
+        top = s.max(1, initial=-np.inf)
+        e = np.exp(s - np.where(np.isneginf(top), 0, top)[:, None])
+        total = e.sum(1)
+        some = total > 0
+        by = np.where(some, total, 1)[:, None]
+        o[:, h], w[:, h] = e @ vh / by, e @ np.abs(vh) / by
+        lse[some, h] = top[some] + np.log(total[some])
+    return o, lse, w, size
+
+
 def norm(x, residual, weight, eps, group):
     """(h, y, scales): h the row that is stored, y its norm, a scale for each group."""
     h = x if residual is None else x + residual
