@@ -1,8 +1,9 @@
 /*
  * wbserve.h -- C ABI of the serving operators around the recurrent-state layers of a
  * hybrid language model (MI355X, gfx950): the paged key-value cache of its
- * full-attention layers (page planning, cache writes, attention of one new token and of
- * chunks of them) and the root-mean-square norm whose output is stored in 8 bits.
+ * full-attention layers (norms and rotary positions of queries and keys, page planning,
+ * cache writes, attention of one new token and of chunks of them), the root-mean-square
+ * norm whose output is stored in 8 bits, and log probabilities of tokens.
  *
  * Conventions are those of wbstate.h: status codes WB_*, caller-owned device memory (the
  * library never allocates), arguments validated on the host before anything is enqueued,
@@ -11,7 +12,7 @@
  * or outputs for the next or uses device memory that was not passed to it, so calls on
  * different streams are independent and every call can be captured into a graph; what a
  * captured call reads (lengths, page tables, free pages) may change between replays. (The
- * process counts the calls of kv_attend: a call marks its workspace with its number.)
+ * process counts the calls of kv_attend and token_logprobs: a call marks its workspace with its number.)
  *
  * Stored keys and values: one array each, [pages][H][page][D], D contiguous: the tokens
  * of a page are contiguous for each key-value head. Token t of request r is token
@@ -153,6 +154,48 @@ int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t 
 
 /* Bytes of workspace of kv_attend_chunk. Host only. */
 int kv_attend_chunk_work(const wb_kv_cache* c, int N, int R, int Hq, int width, size_t* bytes);
+
+/* Heads of N tokens, read at x and written at out (which may be x, with the same strides): head h of
+ * token i begins at element i * row + h * head and is contiguous; out_row and out_head likewise.
+ * weight: of the norm (D values of the same type), or NULL: no norm. */
+typedef struct wb_heads {
+    const void* x;
+    void* out;
+    const void* weight;
+    int64_t row, head, out_row, out_head;
+    int32_t H, reserved;
+} wb_heads;
+
+/* Norms and rotary positions of queries and keys: for each head of q and (if not NULL) k
+ *   y = x / sqrt(mean(x^2) + eps) * weight  (weight NULL: y = x),
+ * and pairs (a, b) of its first `rot` columns, (y_i, y_{i + rot / 2}) or, interleaved,
+ * (y_{2 i}, y_{2 i + 1}), become
+ *   (a cos t - b sin t, a sin t + b cos t) * magnitude,  t = position * freqs[i]  (radians),
+ * the others stay y. freqs: float64 [rot / 2], any: positions scaled for long contexts are other
+ * frequencies and a magnitude. Angles are taken in 64 bits (positions up to 2^31 to 2^-20 of a radian), the
+ * rest is float32, outputs are rounded once. Rows of any finite size have their norm (where squares
+ * leave float32's range, it is taken of the scaled row); a row of zeros stays zeros. positions: int32 [N],
+ * or int64 with positions64; both may be NULL if rot is 0 (norms alone). Types WB_BF16, WB_F16, WB_F32;
+ * 1 <= D <= 1024, rot even, 0 <= rot <= D. Outputs overlap nothing but their own input. */
+int qk_rotate(const wb_heads* q, const wb_heads* k, int dtype, int N, int D, const void* positions, int positions64,
+              const double* freqs, int rot, int interleaved, float magnitude, float eps, void* stream);
+
+/* Log probabilities of given tokens: for each of N rows x of V logits (type `dtype`, `row` elements apart)
+ *   lse = log sum_j e^{scale x_j},  logprob = scale x_token - lse,  p_j = e^{scale x_j - lse},
+ *   entropy = -sum_j p_j log p_j  (NULL: not wanted),
+ *   top_ids, top_logprobs [N][K]: the K largest logits' columns and their log probabilities, larger logits
+ *   first, equal ones by their column; NaN counts as -infinity in this order (K 0: not wanted).
+ * Sums are float32. A token outside [0, V) (padding) has logprob NaN; logits of -infinity have p = 0; a
+ * row that holds a NaN or +infinity, or nothing but -infinity, has NaN in place of its log probabilities and
+ * entropy. tokens: int32 [N], or int64 with tokens64. logprob, entropy: float32 [N]; top_ids int32,
+ * top_logprobs float32. 1 <= V <= 2^24, K <= 64 and V, 2^-100 <= scale <= 2^100 (1 / temperature), N >= 0.
+ * `work` as for kv_attend, of token_logprobs_work() bytes. Equal calls give equal bits. No output overlaps an input. */
+int token_logprobs(const void* logits, int64_t row, int dtype, int N, int V, const void* tokens, int tokens64, float scale,
+                   float* logprob, float* entropy, int K, int32_t* top_ids, float* top_logprobs, void* work,
+                   size_t work_bytes, void* stream);
+
+/* Bytes of workspace of token_logprobs. Host only. */
+int token_logprobs_work(int N, int V, int K, size_t* bytes);
 
 /* Root-mean-square norm with an 8-bit output: for each of N rows of D columns
  *   h = x + residual (float32; residual NULL: h = x), residual_out = h rounded to residual's type,

@@ -282,5 +282,5 @@ def damp_select(samples, s, k_hi=16, block=32, tau=0.01, stream=None):
     return perm, cost
 
 
-from .serve import (SERVE_SIGNATURES, KVCacheDesc, kv_append, kv_attend, kv_attend_chunk, norm_quant,  # noqa: E402,F401
-                    plan_pages, release_pages)
+from .serve import (SERVE_SIGNATURES, HeadsDesc, KVCacheDesc, kv_append, kv_attend, kv_attend_chunk,  # noqa: E402,F401
+                    norm_quant, plan_pages, qk_rotate, release_pages, rotary_frequencies, token_logprobs)

@@ -51,12 +51,6 @@ __device__ __forceinline__ int turns_of(int n, int window, int most) {
     return (n - first_token(n, window) + kTurn - 1) / kTurn;
 }
 
-// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division is some 150
-// dependent instructions)
-__device__ __forceinline__ int64_t quotient64(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
-    return a / b;
-}
 // Run of workgroup w of n: units [total w / n, total (w + 1) / n)
 __device__ __forceinline__ int64_t run_start(int64_t total, int64_t w, int64_t n) { return quotient64(total * w, n); }
 // The workgroup whose run holds unit u
@@ -69,11 +63,6 @@ struct Run {
     int n;                          // workgroups with work
     int lens_at, lens;              // the lane's length of requests lens_at ..+63, r's among them
 };
-
-__device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
-    return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v), lane))) |
-                   uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32);
-}
 
 // This workgroup's run (from == to: none), by every wavefront for itself: lane l sums the
 // turns of requests [l R / 64, (l + 1) R / 64), one scan finds the lane whose requests hold
@@ -261,25 +250,6 @@ __device__ __forceinline__ f32x2 get_part(const float* p) {
     return __builtin_bit_cast(f32x2, __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
                                                        __HIP_MEMORY_SCOPE_AGENT));
 }
-__device__ __forceinline__ void stores_complete() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-// Whether this is the last of `count` workgroups to come here. The counter needs no clearing:
-// it holds the call's tag above its 12 bits of count, whoever finds another tag there puts
-// the call's with a count of 0 (one exchange; it fails only where another workgroup's has
-// succeeded), and the last one takes the tag out again, so that a replay of a captured call,
-// which has the same tag, starts over. Nothing waits here.
-constexpr int kCountBits = 12;
-__device__ __forceinline__ bool last_to_arrive(uint64_t* c, uint64_t tag, int count) {
-    uint64_t v = __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (v >> kCountBits != tag)
-        __hip_atomic_compare_exchange_strong(c, &v, tag << kCountBits, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT);
-    v = __hip_atomic_fetch_add(c, uint64_t(1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const bool last = int(v & ((1u << kCountBits) - 1)) + 1 == count;
-    if (last) __hip_atomic_store(c, uint64_t(0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return last;
-}
-
 // 4 columns of head h of a row joined from parts c0, c0 + 2^step_log2, ...: their sum, weight sum and
 // maximum, in one pass with a running maximum (a part's sums are requested with its maximum)
 struct Joined {

@@ -17,15 +17,6 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves, kTile = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------------------- where a workgroup works
-__device__ __forceinline__ int64_t quotient64(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
-    return a / b;
-}
-__device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
-    return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v), lane))) |
-                   uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32);
-}
-
 // A request: its new tokens (rows first ..+m of q), stored tokens n; span: key tiles of a
 // block of its rows at most. A bad length has n = 0 and one tile of which nothing is read.
 struct Request {

@@ -1,0 +1,336 @@
+// Log probabilities of given tokens, entropy and the most probable tokens (wbserve.h).
+//
+//   lse = log sum_j e^{x_j},  logprob = x_token - lse,  entropy = lse - sum_j p_j x_j
+//
+// Reading the logits once bounds it (HBM). A workgroup takes a row, or, where rows are few, a
+// segment of one; a lane takes vectors of 8 columns and keeps a running maximum m, s = sum e^{x - m}
+// and t = sum e^{x - m} (x - m), so that the entropy is log s - t / s without cancellation.
+// The top K need no second pass over the row: the stream leaves the maximum of every chunk of 512
+// columns in LDS. K chunks by (maximum, then position) hold all of the top K, for any column of
+// another chunk is behind the maxima of K that are larger, or as large and before it. Of those K
+// chunks' vectors, K are found likewise, and of those 8 K columns the top K: whatever the row
+// holds, K * 512 columns at most are read again.
+#include "serve_device.hpp"
+
+namespace wb {
+namespace {
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kChunk = 512;                       // columns a wavefront takes at a time, 8 a lane
+constexpr int kMaxTop = 64;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Order of values as whole numbers: larger ones first, -0 as 0, NaN as -infinity
+__device__ __forceinline__ uint32_t order_of(float x) {
+    x = x != x ? -INFINITY : x + 0.f;
+    const uint32_t b = __float_as_uint(x);
+    return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+    return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+// Larger values before smaller, equal ones by position. 0 stands for nothing.
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t at) { return uint64_t(order_of(x)) << 32 | (0xFFFFFFFFu - at); }
+__device__ __forceinline__ uint32_t at_of(uint64_t key) { return 0xFFFFFFFFu - uint32_t(key); }
+
+// Vector v of a row: columns 8 v - off ..+7, of which some of the first and the last may be outside
+// [0, V): -infinity, which adds nothing and is never taken.
+template <int T>
+struct Row {
+    const void* p;
+    int V, off;
+    __device__ __forceinline__ float one(int64_t i) const {
+        if constexpr (T == WB_F32) return static_cast<const float*>(p)[i];
+        else return Elem<T>::get(static_cast<const uint16_t*>(p)[i]);
+    }
+    __device__ __forceinline__ void load(int v, float (&x)[8]) const {
+        const int64_t c = int64_t(v) * 8 - off;
+        if (c >= 0 && c + 8 <= V) {
+            if constexpr (T == WB_F32) {
+                const f32x4* s = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + c);
+                const f32x4 a = s[0], b = s[1];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = a[e];
+                    x[4 + e] = b[e];
+                }
+            } else {
+                const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = Elem<T>::get(uint16_t(w[e]));
+                    x[2 * e + 1] = Elem<T>::get(uint16_t(w[e] >> 16));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] = -INFINITY;
+                if (c + e >= 0 && c + e < V) x[e] = one(c + e);
+            }
+        }
+    }
+};
+
+// s = sum e^{c (x - m)}, t = sum e^{c (x - m)} c (x - m) in powers of two
+struct Sums {
+    float m = -INFINITY, s = 0.f, t = 0.f;
+    __device__ __forceinline__ void move(float to, float c) {            // to >= m
+        // (2^-256 is 0: nothing is left of sums so far below, which the product must not turn into NaN)
+        const float by = m == to ? 0.f : fmaxf((m - to) * c, -256.f), f = __builtin_amdgcn_exp2f(by);
+        t = (t + s * by) * f;
+        s *= f;
+        m = to;
+    }
+    __device__ __forceinline__ void add(const Sums& o, float c) {
+        const float top = fmaxf(m, o.m);
+        Sums q = o;
+        move(top, c);
+        q.move(top, c);
+        s += q.s;
+        t += q.t;
+    }
+};
+
+// The first K of n keys in order, out[0 .. K) (0 where there are fewer), by all threads of the
+// workgroup; `keys` has room for the next power of two past n and is left in any order.
+__device__ __forceinline__ void first_keys(uint64_t* keys, int n, int K, uint64_t* out) {
+    const int tid = threadIdx.x;
+    if (n <= kThreads) {
+        // each key's place is the number of larger ones
+        for (int i = tid; i < K; i += kThreads)
+            if (i >= n) out[i] = 0;
+        if (tid < n) {
+            const uint64_t mine = keys[tid];
+            int place = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) place += keys[j] > mine;
+            if (place < K) out[place] = mine;
+        }
+        __syncthreads();
+        return;
+    }
+    int size = 2 * kThreads;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kThreads) keys[i] = 0;
+    __syncthreads();
+    for (int run = 2; run <= size; run *= 2)
+        for (int step = run / 2; step; step /= 2) {
+            for (int i = tid; i < size / 2; i += kThreads) {
+                const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
+                const uint64_t a = keys[lo], b = keys[hi];
+                if ((a < b) == ((lo & run) == 0)) {
+                    keys[lo] = b;
+                    keys[hi] = a;
+                }
+            }
+            __syncthreads();
+        }
+    for (int i = tid; i < K; i += kThreads) out[i] = keys[i];
+    __syncthreads();
+}
+
+template <int T, bool TOP>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A) {
+    // chunks' maxima, then vectors' (64 of each of the top K chunks), then columns
+    constexpr int kKeys = TOP ? kMaxTop * 64 : 1;
+    __shared__ uint64_t keys[kKeys];
+    __shared__ uint64_t first[TOP ? kMaxTop : 1];
+    __shared__ float sums[kWaves][3];
+    __shared__ int count, is_last;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t row = A.first + blockIdx.x / A.segments;
+    const int segment = blockIdx.x % A.segments;
+    const int size = T == WB_F32 ? 4 : 2;
+    Row<T> x;
+    x.p = static_cast<const uint8_t*>(A.logits) + row * A.row * size;
+    x.V = A.V;
+    x.off = int((reinterpret_cast<uintptr_t>(x.p) & 15) / size);
+    const float c = A.scale * kLog2e;
+    const int vectors = (A.V + x.off + 7) / 8, chunks = (vectors + 63) / 64;
+    const int c0 = int(int64_t(chunks) * segment / A.segments), c1 = int(int64_t(chunks) * (segment + 1) / A.segments);
+
+    Sums own;
+#pragma unroll 2
+    for (int k = c0 + wave; k < c1; k += kWaves) {
+        const int v = 64 * k + lane;
+        float y[8];
+        if (v < vectors) {
+            x.load(v, y);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = -INFINITY;
+        }
+        float top = y[0];
+#pragma unroll
+        for (int e = 1; e < 8; ++e) top = fmaxf(top, y[e]);
+        top = fmaxf(top, -INFINITY);                               // (NaN throughout)
+        if (top > own.m) own.move(top, c);
+        const float ref = own.m == -INFINITY ? 0.f : own.m;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = (y[e] - ref) * c, p = __builtin_amdgcn_exp2f(d);
+            own.s += p;
+            own.t = __builtin_fmaf(p, fmaxf(d, -256.f), own.t);     // (0 times -infinity is not 0)
+        }
+        if constexpr (TOP) {
+            const uint32_t best = lanes_reduce<OpMax, 64>(order_of(top));
+            if (lane == 0) keys[k - c0] = uint64_t(best) << 32 | (0xFFFFFFFFu - uint32_t(k));
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        Sums o;
+        o.m = __shfl_xor(own.m, d);
+        o.s = __shfl_xor(own.s, d);
+        o.t = __shfl_xor(own.t, d);
+        own.add(o, c);
+    }
+    if (lane == 0) {
+        sums[wave][0] = own.m;
+        sums[wave][1] = own.s;
+        sums[wave][2] = own.t;
+    }
+    if (tid == 0) count = 0;
+    __syncthreads();
+    own = Sums{sums[0][0], sums[0][1], sums[0][2]};
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) own.add(Sums{sums[w][0], sums[w][1], sums[w][2]}, c);
+
+    if constexpr (TOP) {
+        const int K = A.K;
+        first_keys(keys, c1 - c0, K, first);
+        const int held = min(K, c1 - c0);
+        const uint32_t least = c1 - c0 >= K ? uint32_t(first[K - 1] >> 32) : 0;      // no column below it is taken
+        // vectors of those chunks
+        for (int i = wave; i < held; i += kWaves) {
+            const int v = 64 * int(at_of(first[i])) + lane;
+            if (v < vectors) {
+                float y[8];
+                x.load(v, y);
+                float top = y[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, y[e]);
+                const uint32_t o = order_of(fmaxf(top, -INFINITY));
+                if (o >= least) keys[atomicAdd(&count, 1)] = uint64_t(o) << 32 | (0xFFFFFFFFu - uint32_t(v));
+            }
+        }
+        __syncthreads();
+        const int n_vectors = count;
+        first_keys(keys, n_vectors, K, first);
+        // columns of those vectors
+        if (tid == 0) count = 0;
+        const uint32_t least_v = n_vectors >= K ? uint32_t(first[K - 1] >> 32) : 0;
+        uint64_t mine = 0;
+        if (tid < 8 * min(K, n_vectors)) {
+            const int64_t at = int64_t(at_of(first[tid >> 3])) * 8 - x.off + (tid & 7);
+            if (at >= 0 && at < A.V) {
+                const float value = x.one(at);
+                if (order_of(value) >= least_v) mine = key_of(value, uint32_t(at));
+            }
+        }
+        __syncthreads();
+        if (mine) keys[atomicAdd(&count, 1)] = mine;
+        __syncthreads();
+        first_keys(keys, count, K, first);
+    }
+
+    if (A.segments > 1) {
+        // the workgroup that stores a row's last segment joins them, in their order
+        const int64_t local = row - A.first;
+        const int parts = A.segments, words = 2 + (TOP ? A.K : 0);
+        uint64_t* part = A.parts + (local * parts + segment) * words;
+        if (tid == 0) {
+            put_word(part, uint64_t(__float_as_uint(own.m)) | uint64_t(__float_as_uint(own.s)) << 32);
+            put_word(part + 1, uint64_t(__float_as_uint(own.t)));
+        }
+        if constexpr (TOP)
+            if (tid < A.K) put_word(part + 2 + tid, first[tid]);
+        stores_complete();
+        __syncthreads();
+        if (tid == 0) is_last = last_to_arrive(A.arrivals + local, A.tag, parts);
+        __syncthreads();
+        if (!is_last) return;
+        part = A.parts + local * parts * words;
+        Sums all;
+        for (int p = 0; p < parts; ++p) {
+            const uint64_t ms = get_word(part + p * words), t = get_word(part + p * words + 1);
+            Sums o;
+            o.m = __uint_as_float(uint32_t(ms));
+            o.s = __uint_as_float(uint32_t(ms >> 32));
+            o.t = __uint_as_float(uint32_t(t));
+            all.add(o, c);
+        }
+        own = all;
+        if constexpr (TOP) {
+            for (int i = tid; i < parts * A.K; i += kThreads) {
+                const int p = i / A.K;
+                keys[i] = get_word(part + p * words + 2 + (i - p * A.K));
+            }
+            __syncthreads();
+            first_keys(keys, parts * A.K, A.K, first);
+        }
+    }
+
+    // (x - m) scale - log s
+    const float log_s = logf(own.s);
+    if (tid == 0) {
+        const int64_t token = A.wide ? static_cast<const int64_t*>(A.tokens)[row] : static_cast<const int32_t*>(A.tokens)[row];
+        A.logprob[row] = token >= 0 && token < A.V ? (x.one(token) - own.m) * A.scale - log_s : __builtin_nanf("");
+        if (A.entropy) A.entropy[row] = log_s - own.t / own.s * kLn2;
+    }
+    if constexpr (TOP)
+        if (tid < A.K) {
+            A.top_ids[row * A.K + tid] = int32_t(at_of(first[tid]));
+            A.top_logprobs[row * A.K + tid] = (value_of(uint32_t(first[tid] >> 32)) - own.m) * A.scale - log_s;
+        }
+}
+
+template <int T>
+hipError_t logprobs_t(const LogprobArgs& a, unsigned groups, hipStream_t s) {
+    if (a.K) logprobs_kernel<T, true><<<groups, kThreads, 0, s>>>(a);
+    else logprobs_kernel<T, false><<<groups, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Segments of a row: enough for 1024 workgroups (4 a compute unit), of 8 chunks (one a wavefront) at
+// least; joined parts' keys fit the 4096 of LDS, and so do a segment's chunks.
+LogprobPlan logprob_plan(int N, int V, int K) {
+    const int chunks = (V + 7 + kChunk - 1) / kChunk;
+    LogprobPlan p;
+    int64_t n = 1024 / N < 1 ? 1 : 1024 / N;
+    const int64_t most = (chunks + kWaves - 1) / kWaves;
+    if (n > most) n = most;
+    if (n > 64) n = 64;
+    const int64_t least = (chunks + kMaxTop * 64 - 1) / (kMaxTop * 64);
+    if (n < least) n = least;
+    p.segments = int(n);
+    p.part_bytes = n > 1 ? size_t(N) * n * (2 + K) * 8 : 0;
+    p.arrivals_bytes = n > 1 ? size_t(N) * 8 : 0;
+    return p;
+}
+
+hipError_t launch_logprobs(LogprobArgs a, int N, hipStream_t s) {
+    const int64_t most = kLaunchItems / kThreads / a.segments;            // rows of a launch
+    uint64_t* const parts = a.parts;
+    uint64_t* const arrivals = a.arrivals;
+    for (int64_t first = 0; first < N; first += most) {
+        const int64_t n = N - first < most ? N - first : most;
+        a.first = first;
+        if (a.segments > 1) {
+            a.parts = parts + first * a.segments * (2 + a.K);
+            a.arrivals = arrivals + first;
+        }
+        const unsigned groups = unsigned(n * a.segments);
+        const hipError_t e = a.dtype == WB_BF16  ? logprobs_t<WB_BF16>(a, groups, s)
+                             : a.dtype == WB_F16 ? logprobs_t<WB_F16>(a, groups, s)
+                                                 : logprobs_t<WB_F32>(a, groups, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace wb

@@ -124,4 +124,42 @@ __device__ __forceinline__ int64_t wave_scan(int64_t v) {
     return v;
 }
 
+// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division is some 150
+// dependent instructions)
+__device__ __forceinline__ int64_t quotient64(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return int64_t(uint32_t(a) / uint32_t(b));
+    return a / b;
+}
+
+__device__ __forceinline__ int64_t lane64(int64_t v, int lane) {
+    return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v), lane))) |
+                   uint64_t(uint32_t(__builtin_amdgcn_readlane(int(v >> 32), lane))) << 32);
+}
+
+// 64 bits between workgroups of one launch, past the caches that the compute dies do not share
+__device__ __forceinline__ void put_word(uint64_t* p, uint64_t v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t get_word(const uint64_t* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void stores_complete() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// Whether this is the last of `count` workgroups to come here. The counter needs no clearing:
+// it holds the call's tag above its 12 bits of count, whoever finds another tag there puts
+// the call's with a count of 0 (one exchange; it fails only where another workgroup's has
+// succeeded), and the last one takes the tag out again, so that a replay of a captured call,
+// which has the same tag, starts over. Nothing waits here.
+constexpr int kCountBits = 12;
+__device__ __forceinline__ bool last_to_arrive(uint64_t* c, uint64_t tag, int count) {
+    uint64_t v = __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (v >> kCountBits != tag)
+        __hip_atomic_compare_exchange_strong(c, &v, tag << kCountBits, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+    v = __hip_atomic_fetch_add(c, uint64_t(1), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const bool last = int(v & ((1u << kCountBits) - 1)) + 1 == count;
+    if (last) __hip_atomic_store(c, uint64_t(0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return last;
+}
+
 }  // namespace wb

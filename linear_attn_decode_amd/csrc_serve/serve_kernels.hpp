@@ -109,6 +109,43 @@ struct ChunkPlan {
 ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width);
 hipError_t launch_chunk(const ChunkArgs& a, hipStream_t stream);
 
+struct RotateArgs {
+    wb_heads q = {}, k = {};
+    const void* positions = nullptr;
+    const double* freqs = nullptr;
+    float magnitude = 1.f, eps = 0.f;
+    int dtype = 0, D = 0, rot = 0;
+    bool wide = false;            // 64-bit positions
+    bool interleaved = false;
+    int lanes = 4;                // of a head
+    int waves_per_token = 1;
+    int64_t first = 0, last = 0;  // tokens of the launch
+};
+hipError_t launch_rotate(RotateArgs a, int N, hipStream_t stream);
+
+struct LogprobArgs {
+    const void* logits = nullptr;
+    int64_t row = 0;
+    const void* tokens = nullptr;
+    float* logprob = nullptr;
+    float* entropy = nullptr;
+    int32_t* top_ids = nullptr;
+    float* top_logprobs = nullptr;
+    uint64_t* parts = nullptr;    // [rows][segments][2 + K] sums and top keys of segments
+    uint64_t* arrivals = nullptr; // [rows] segments stored
+    uint64_t tag = 0;             // of this call, as for AttendArgs
+    float scale = 1.f;
+    int dtype = 0, V = 0, K = 0, segments = 1;
+    bool wide = false;            // 64-bit tokens
+    int64_t first = 0;            // row of the launch
+};
+struct LogprobPlan {
+    int segments;
+    size_t part_bytes, arrivals_bytes;
+};
+LogprobPlan logprob_plan(int N, int V, int K);
+hipError_t launch_logprobs(LogprobArgs a, int N, hipStream_t stream);
+
 struct NormArgs {
     const void* x = nullptr;
     const void* residual = nullptr;

@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int kMaxRequests = 65536, kMaxQueryHeads = 4096, kMaxColumns = 65536;
+constexpr int kMaxHeadColumns = 1024, kMaxVocabulary = 1 << 24, kMaxAlternatives = 64;
 constexpr int64_t kMaxTokens = int64_t(1) << 30;
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -56,6 +57,11 @@ int check_chunk(const wb_kv_cache* c, int N, int R, int Hq, int width) {
     if (v) return v;
     if (N < 0) return WB_EINVAL;
     return int64_t(N) * Hq > 0x7FFFFFFF ? WB_EUNSUPPORTED : WB_OK;
+}
+
+int check_logprobs(int N, int V, int K) {
+    if (N < 0 || V < 1 || K < 0 || K > V) return WB_EINVAL;
+    return V > kMaxVocabulary || K > kMaxAlternatives ? WB_EUNSUPPORTED : WB_OK;
 }
 
 size_t work_bytes_of(const wb::AttendPlan& p) {
@@ -296,6 +302,101 @@ int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t 
     a.slots = p.slots;
     a.groups = p.groups;
     return hip_status(wb::launch_chunk(a, static_cast<hipStream_t>(stream)));
+}
+
+int qk_rotate(const wb_heads* q, const wb_heads* k, int dtype, int N, int D, const void* positions, int positions64,
+              const double* freqs, int rot, int interleaved, float magnitude, float eps, void* stream) {
+    if (dtype != WB_BF16 && dtype != WB_F16 && dtype != WB_F32) return WB_EINVAL;
+    if (!q || N < 0 || D < 1 || rot < 0 || rot > D || rot % 2) return WB_EINVAL;
+    if (!(eps >= 0.f) || magnitude != magnitude) return WB_EINVAL;
+    if (D > kMaxHeadColumns) return WB_EUNSUPPORTED;
+    const unsigned size = unsigned(element_size(dtype));
+    for (const wb_heads* x : {q, k}) {
+        if (!x) continue;
+        if (x->H < 1) return WB_EINVAL;
+        if (x->H > kMaxQueryHeads) return WB_EUNSUPPORTED;
+        if (N == 0) continue;
+        if (!x->x || !x->out) return WB_EINVAL;
+        // (rows and heads of outputs do not overlap; in place is element for element)
+        if (x->out == x->x && ((N > 1 && x->out_row != x->row) || (x->H > 1 && x->out_head != x->head))) return WB_EINVAL;
+        const int64_t heads = x->H > 1 ? (x->H - 1) * x->out_head : 0, rows = N > 1 ? (N - 1) * x->out_row : 0;
+        if ((x->H > 1 && x->out_head < D) || (N > 1 && x->out_row < D)) return WB_EINVAL;
+        if (x->H > 1 && N > 1 && x->out_row < heads + D && x->out_head < rows + D) return WB_EINVAL;
+        if (x->weight && (x->weight == x->out || x->weight == x->x)) return WB_EINVAL;
+        if (!aligned(x->x, size) || !aligned(x->out, size) || !aligned(x->weight, size)) return WB_EALIGN;
+    }
+    if (N == 0) return WB_OK;
+    if (rot && (!positions || !freqs)) return WB_EINVAL;
+    if (k && (k->out == q->out || k->out == q->x || q->out == k->x)) return WB_EINVAL;
+    if (!aligned(positions, positions64 ? 8 : 4) || !aligned(freqs, 8)) return WB_EALIGN;
+    wb::RotateArgs a;
+    a.q = *q;
+    if (k) a.k = *k;
+    a.positions = positions;
+    a.freqs = freqs;
+    a.magnitude = magnitude;
+    a.eps = eps;
+    a.dtype = dtype;
+    a.D = D;
+    a.rot = rot;
+    a.wide = positions64 != 0;
+    a.interleaved = interleaved != 0;
+    return hip_status(wb::launch_rotate(a, N, static_cast<hipStream_t>(stream)));
+}
+
+int token_logprobs_work(int N, int V, int K, size_t* bytes) {
+    if (!bytes) return WB_EINVAL;
+    const int v = check_logprobs(N, V, K);
+    if (v) return v;
+    *bytes = 0;
+    if (N) {
+        const wb::LogprobPlan p = wb::logprob_plan(N, V, K);
+        *bytes = p.part_bytes + p.arrivals_bytes;
+    }
+    return WB_OK;
+}
+
+int token_logprobs(const void* logits, int64_t row, int dtype, int N, int V, const void* tokens, int tokens64, float scale,
+                   float* logprob, float* entropy, int K, int32_t* top_ids, float* top_logprobs, void* work,
+                   size_t work_bytes, void* stream) {
+    if (dtype != WB_BF16 && dtype != WB_F16 && dtype != WB_F32) return WB_EINVAL;
+    const int v = check_logprobs(N, V, K);
+    if (v) return v;
+    if (!(scale > 0.f)) return WB_EINVAL;
+    if (scale < 0x1p-100f || scale > 0x1p100f) return WB_EUNSUPPORTED;
+    if (N == 0) return WB_OK;
+    if (!logits || !tokens || !logprob || (K && (!top_ids || !top_logprobs))) return WB_EINVAL;
+    if (N > 1 && row < V) return WB_EINVAL;
+    if (!aligned(logits, unsigned(element_size(dtype))) || !aligned(tokens, tokens64 ? 8 : 4) || !aligned(logprob, 4) ||
+        !aligned(entropy, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+        return WB_EALIGN;
+    const wb::LogprobPlan p = wb::logprob_plan(N, V, K);
+    const size_t need = p.part_bytes + p.arrivals_bytes;
+    if (need) {
+        if (!work) return WB_EINVAL;
+        if (work_bytes < need) return WB_ESIZE;
+        if (!aligned(work, 16)) return WB_EALIGN;
+    }
+    wb::LogprobArgs a;
+    a.logits = logits;
+    a.row = N > 1 ? row : V;
+    a.tokens = tokens;
+    a.logprob = logprob;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    if (need) {
+        a.parts = static_cast<uint64_t*>(work);
+        a.arrivals = reinterpret_cast<uint64_t*>(static_cast<uint8_t*>(work) + p.part_bytes);
+        a.tag = next_tag();
+    }
+    a.scale = scale;
+    a.dtype = dtype;
+    a.V = V;
+    a.K = K;
+    a.segments = p.segments;
+    a.wide = tokens64 != 0;
+    return hip_status(wb::launch_logprobs(a, N, static_cast<hipStream_t>(stream)));
 }
 
 int norm_quant(const void* x, int64_t x_row, const void* residual, int64_t r_row, void* residual_out, int64_t ro_row,

@@ -1,6 +1,6 @@
 """Python binding of the serving operators around the recurrent-state layers of a hybrid
-language model (C ABI: ``include/wbserve.h``): the paged key-value cache of its
-full-attention layers and the norm with an 8-bit output.
+language model (C ABI: ``include/wbserve.h``): rotary positions, the paged key-value cache and
+attention of its full-attention layers, the norm with an 8-bit output, and log probabilities.
 
 Argument marshalling only, as for the write-back calls: tensors are checked for type,
 shape, device and layout (ValueError), then pointers and the stream are forwarded.
@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import struct
 
 _P = ctypes.c_void_p
@@ -31,7 +32,13 @@ class KVCacheDesc(ctypes.Structure):
                 ("page", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class HeadsDesc(ctypes.Structure):
+    _fields_ = [("x", _P), ("out", _P), ("weight", _P), ("row", _I64), ("head", _I64), ("out_row", _I64),
+                ("out_head", _I64), ("H", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _C = ctypes.POINTER(KVCacheDesc)
+_HD = ctypes.POINTER(HeadsDesc)
 SERVE_SIGNATURES = {
     "kv_plan_pages": (_I, [_P, _P, _I, _P, _I, _P, _I, _P, _I, _P, _I64, _P, _P, _P, _P, _P, _P]),
     "kv_plan_work": (_I, [_I, _I64, _I]),
@@ -41,6 +48,9 @@ SERVE_SIGNATURES = {
     "kv_attend_work": (_I, [_C, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "kv_attend_chunk": (_I, [_C, _P, _I64, _I64, _I, _I, _I, _I, _P, _I, _P, _P, _F, _I, _P, _P, _P, _SZ, _P]),
     "kv_attend_chunk_work": (_I, [_C, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "qk_rotate": (_I, [_HD, _HD, _I, _I, _I, _P, _I, _P, _I, _I, _F, _F, _P]),
+    "token_logprobs": (_I, [_P, _I64, _I, _I, _I, _P, _I, _F, _P, _P, _I, _P, _P, _P, _SZ, _P]),
+    "token_logprobs_work": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
     "norm_quant": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I, _I, _I, _F, _I, _P, _I64, _P, _P]),
 }
 
@@ -55,6 +65,7 @@ _torch = None
 _fn = {}
 _codes = {}
 _desc = struct.Struct("PPPPqiiii")         # wb_kv_cache
+_heads = struct.Struct("PPPqqqqii")        # wb_heads
 
 
 def _load():
@@ -64,7 +75,7 @@ def _load():
     from . import lib
     h = lib()
     for name, (res, args) in SERVE_SIGNATURES.items():
-        _fn[name] = ctypes.CFUNCTYPE(res, *(_P if a is _C else a for a in args))((name, h))
+        _fn[name] = ctypes.CFUNCTYPE(res, *(_P if a in (_C, _HD) else a for a in args))((name, h))
     _codes.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32, torch.float8_e4m3fn: E4M3})
     _torch = torch
 
@@ -188,6 +199,14 @@ def _chunk_work(code, pages, H, page, D, N, R, Hq, width):
     scale = fake if code == E4M3 else 0
     _check(_fn["kv_attend_chunk_work"](_desc.pack(fake, fake, scale, scale, pages, page, H, D, code), N, R, Hq, width,
                                        ctypes.byref(need)), "kv_attend_chunk")
+    return need.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _logprob_work(N, V, K):
+    """Workspace bytes of token_logprobs."""
+    need = _SZ()
+    _check(_fn["token_logprobs_work"](N, V, K, ctypes.byref(need)), "token_logprobs")
     return need.value
 
 
@@ -362,6 +381,109 @@ def kv_attend_chunk(q, k_cache, v_cache, table, lens, starts, o, scale=None, win
     _call("kv_attend_chunk", dev, c, q.data_ptr(), q_row if N > 1 else 0, q_head if Hq > 1 else 0, _codes[kind], N, R, Hq,
           table.data_ptr(), width, lens.data_ptr(), starts.data_ptr(), D ** -0.5 if scale is None else scale,
           window if window < _MAX else 0, o.data_ptr(), lsep, held.data_ptr() if n else None, n, _stream_of(dev, stream))
+
+
+def _rotated(x, out, weight, name, kind, N, D, dev):
+    """A wb_heads of x [N, H, D]: strided tokens and heads, contiguous columns."""
+    out = x if out is None else out
+    shape = x.shape
+    if not (len(shape) == 3 and x.dtype is kind and out.dtype is kind and shape[0] == N and shape[2] == D and out.shape == shape
+            and x.get_device() == out.get_device() == dev and x.stride(2) == out.stride(2) == 1 and shape[1] <= _MAX):
+        bad = out if x.dim() == 3 and x.dtype is kind and x.shape == (N, x.shape[1], D) and x.get_device() == dev and x.stride(2) == 1 else x
+        _refuse(bad, name if bad is x else name + "_out", f"{kind} [{N}, {shape[1] if len(shape) == 3 else 'heads'}, {D}] with contiguous heads", dev)
+    w = 0 if weight is None else _ptr(weight, name + "_weight", kind, (D,), dev)
+    return _heads.pack(x.data_ptr(), out.data_ptr(), w, x.stride(0), x.stride(1), out.stride(0), out.stride(1), shape[1], 0)
+
+
+def qk_rotate(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+              magnitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys for each head, and their rotary positions, in one pass: with
+    ``q_weight`` / ``k_weight`` ([D]; None: no norm) y = x / sqrt(mean(x^2) + eps) * weight, then pairs of
+    the first ``rot = 2 len(freqs)`` columns, (i, i + rot / 2) or, ``interleaved``, (2 i, 2 i + 1), are turned
+    by ``positions[n] * freqs[i]`` radians and multiplied by ``magnitude``. ``q`` [N, Hq, D] and ``k``
+    [N, H, D] (or None) are bfloat16, float16 or float32, tokens and heads may be strided (views of a fused
+    projection); ``q_out`` and ``k_out`` get the results (default: in place). ``positions`` int32 or int64 [N];
+    ``freqs`` float64 [rot / 2], as ``rotary_frequencies`` gives them. Outputs overlap nothing but their own input."""
+    if _torch is None:
+        _load()
+    dev = _device(q, "q")
+    kind = q.dtype
+    code = _codes.get(kind, E4M3)
+    if code == E4M3 or q.dim() != 3:
+        raise ValueError(f"q: expected bfloat16, float16 or float32 [N, Hq, D], got {kind} {tuple(q.shape)}")
+    N, _, D = q.shape
+    if N > _MAX or D > _MAX:
+        raise ValueError(f"q: {tuple(q.shape)} is too large")
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs: expected 1 dimension, got {freqs.dim()}")
+    half = freqs.shape[0]
+    if 2 * half > D:
+        raise ValueError(f"freqs: {half} pairs are more than the {D} columns of a head")
+    wide = positions.dtype is _torch.int64
+    f = _ptr(freqs, "freqs", _torch.float64, (half,), dev)
+    p = _ptr(positions, "positions", _torch.int64 if wide else _torch.int32, (N,), dev)
+    qd = _rotated(q, q_out, q_weight, "q", kind, N, D, dev)
+    kd = None if k is None else _rotated(k, k_out, k_weight, "k", kind, N, D, dev)
+    _call("qk_rotate", dev, qd, kd, code, N, D, p, wide, f, 2 * half, interleaved, magnitude, eps, _stream_of(dev, stream))
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, context: int = 0, slow: float = 1.0,
+                       fast: float = 32.0, device=None):
+    """``freqs`` (float64 [rot / 2]) for ``qk_rotate``: base^(-2 i / rot) radians a position. For contexts
+    ``factor`` times as long as the trained one: with ``context`` 0 all are divided by ``factor`` (positions
+    interpolated); else by parts: pairs that make at most ``slow`` turns in ``context`` positions are divided,
+    those that make ``fast`` or more stay, and between them the two are mixed linearly in the turns. A larger
+    ``base`` and ``magnitude`` of ``qk_rotate`` are the caller's."""
+    import torch
+    if rot < 0 or rot % 2 or not base > 0 or not factor > 0 or context < 0 or not 0 <= slow < fast:
+        raise ValueError(f"rot, base, factor, context, slow, fast: {rot}, {base}, {factor}, {context}, {slow}, {fast} are out of range")
+    f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+    if context:
+        keep = ((context * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    else:
+        f = f / factor
+    return f.to("cuda" if device is None else device)
+
+
+def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None, scale: float = 1.0, stream=None):
+    """Log probabilities of given tokens: ``logprob`` (float32 [N]) gets log softmax(scale * logits)[n, tokens[n]]
+    (NaN for a token outside [0, V): padding), ``entropy`` (float32 [N], optional) the rows' entropies, and
+    ``top_ids`` (int32 [N, K]) with ``top_logprobs`` (float32 [N, K]) the K most probable tokens, equal logits by
+    their column (K at most 64; both or neither). ``logits`` [N, V] are bfloat16, float16 or float32, rows may be
+    strided; ``tokens`` int32 or int64 [N]; ``scale`` is 1 / temperature. Logits of -infinity have probability 0;
+    a row with a NaN or +infinity, or with nothing else than -infinity, has NaN. No output overlaps an input."""
+    if _torch is None:
+        _load()
+    dev = _device(logits, "logits")
+    kind = logits.dtype
+    code = _codes.get(kind, E4M3)
+    if code == E4M3 or logits.dim() != 2:
+        raise ValueError(f"logits: expected bfloat16, float16 or float32 [N, V], got {kind} {tuple(logits.shape)}")
+    shape = N, V = logits.shape
+    if N > _MAX or V > _MAX:
+        raise ValueError(f"logits: {tuple(shape)} is too large")
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids, top_logprobs: both or neither")
+    K = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2:
+            raise ValueError(f"top_ids: expected 2 dimensions, got {top_ids.dim()}")
+        K = top_ids.shape[1]
+        if K > _MAX:
+            raise ValueError(f"top_ids: {tuple(top_ids.shape)} is too large")
+    f32 = _torch.float32
+    p, row = _rows(logits, "logits", kind, shape, dev, V)
+    wide = tokens.dtype is _torch.int64
+    t = _ptr(tokens, "tokens", _torch.int64 if wide else _torch.int32, (N,), dev)
+    lp = _ptr(logprob, "logprob", f32, (N,), dev)
+    e = None if entropy is None else _ptr(entropy, "entropy", f32, (N,), dev)
+    ids = _ptr(top_ids, "top_ids", _torch.int32, (N, K), dev) if K else None
+    tops = _ptr(top_logprobs, "top_logprobs", f32, (N, K), dev) if K else None
+    n = _logprob_work(N, V, K)
+    held = _workspace(n, _torch.uint8, dev, stream) if n else None
+    _call("token_logprobs", dev, p, row, code, N, V, t, wide, scale, lp, e, K, ids, tops, held.data_ptr() if n else None, n,
+          _stream_of(dev, stream))
 
 
 def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, residual=None, residual_out=None,

@@ -1,6 +1,7 @@
 """Float64 definitions of the serving operators (include/wbserve.h): page planning, cache
-writes, attention of one token over a paged cache, the norm with an e4m3 output. Written
-from the formulas; nothing is shared with the GPU code."""
+writes, attention of one token and of chunks over a paged cache, norms and rotary positions, log
+probabilities, the norm with an e4m3 output. Written from the formulas; nothing is shared with the GPU
+code."""
 from __future__ import annotations
 
 import math
@@ -125,6 +126,37 @@ def attend_chunk(q, k, v, scale, window=0):
         o[:, h], w[:, h] = e @ vh / by, e @ np.abs(vh) / by
         lse[some, h] = top[some] + np.log(total[some])
     return o, lse, w, size
+
+
+def rotate(x, weight, eps, positions, freqs, interleaved, magnitude):
+    """Heads x [N, H, D], normed if there is a weight, the first 2 len(freqs) columns turned. Returns
+    (y [N, H, D], the size of each result's terms [N, H, D])."""
+    y = np.array(x, np.float64)
+    if weight is not None:
+        mean = np.mean(y * y, axis=2, keepdims=True) + eps
+        y = np.where(mean > 0, y / np.sqrt(np.where(mean > 0, mean, 1)), 0) * weight
+    half = len(freqs)
+    i = np.arange(half)
+    first, second = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+    angle = np.asarray(positions, np.float64)[:, None] * np.asarray(freqs)
+    c, s = magnitude * np.cos(angle)[:, None], magnitude * np.sin(angle)[:, None]
+    a, b = y[..., first], y[..., second]
+    out, size = y.copy(), np.abs(y)
+    out[..., first], out[..., second] = a * c - b * s, a * s + b * c
+    size[..., first] = size[..., second] = abs(magnitude) * (np.abs(a) + np.abs(b))
+    return out, size
+
+
+def logprobs(x, tokens, K, scale=1.0):
+    """(logprob, entropy, top columns [K], their log probabilities) of one row of logits."""
+    x = np.asarray(x, np.float64)
+    order = np.lexsort((np.arange(len(x)), -np.where(np.isnan(x), -np.inf, x)))[:K]
+    top = np.max(x)
+    with np.errstate(all="ignore"):
+        p = scale * (x - top) - np.log(np.sum(np.exp(scale * (x - top))))
+        w = np.exp(p)
+        entropy = -np.sum(np.where(w > 0, w * p, 0.0)) if not np.isnan(p).any() else np.nan
+    return p[tokens] if 0 <= tokens < len(x) else np.nan, entropy, order, p[order]
 
 
 def norm(x, residual, weight, eps, group):
