@@ -3,8 +3,6 @@
 //   o_i = sum_t e^{s_it - m} v_t / sum_t e^{s_it - m},  s_it = scale q_i . k_t,  t <= position of i
 //
 // in one pass over the stored tokens with a running maximum.
-#include <type_traits>
-
 #include "serve_device.hpp"
 
 namespace wb {
@@ -130,7 +128,7 @@ template <int T>
 struct Mat32;
 template <>
 struct Mat32<WB_BF16> {
-    static constexpr uint32_t kOnes = 0x3F803F80u, kExponent = 0x7F80u;
+    static constexpr uint32_t kExponent = 0x7F80u;
     static __device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                        0, 0);
@@ -138,7 +136,7 @@ struct Mat32<WB_BF16> {
 };
 template <>
 struct Mat32<WB_F16> {
-    static constexpr uint32_t kOnes = 0x3C003C00u, kExponent = 0x7C00u;
+    static constexpr uint32_t kExponent = 0x7C00u;
     static __device__ __forceinline__ f32x16 mul(u32x4 a, u32x4 b, f32x16 c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                       0);
@@ -171,14 +169,14 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
     return ((w & e) + one) & 0x80008000u;
 }
 
-__device__ __forceinline__ s16x4 read_transposed(uint32_t at) {
+__device__ __forceinline__ s16x4 read_transposed(const uint8_t* at) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
 }
 
 // 4 columns of a finished row out to o; the row's log-sum-exp with its first
 template <int QT>
-__device__ __forceinline__ u32x2 quotients(f32x4 v, float by) {
-    return u32x2{pack2<QT>(v[0] / by, v[1] / by), pack2<QT>(v[2] / by, v[3] / by)};
+__device__ __forceinline__ u32x2 scaled(f32x4 v, float by) {
+    return u32x2{pack2<QT>(v[0] * by, v[1] * by), pack2<QT>(v[2] * by, v[3] * by)};
 }
 
 constexpr int waves_per_simd(int D, int NQ) { return D <= 128 && NQ == 1 ? 2 : 1; }
@@ -191,17 +189,10 @@ struct Chunk {
     static constexpr bool kTwoP = KV == WB_E4M3 && QT == WB_F16;
     static constexpr int KS = D / 16;                                // score products of 32 tokens
     static constexpr int DB = D / 32;                                // blocks of value columns
-    static constexpr int NI = D / 32;                                // 16-byte vectors a lane stages of a tile's keys
-    static constexpr int CH = D / 8;                                 // such vectors of a row
-    static constexpr int RPI = 512 / D;                              // rows a wavefront stages at a time
+    static constexpr int CB = D / 64;                                // blocks of 64 columns
     static constexpr int kShift = VT == WB_F16 ? 11 : 0;             // weights enter as 2^kShift times their value
     static constexpr int kRows = 32 * NQ * kWaves;
     static constexpr int kTileBytes = kTile * D * 2;
-
-    // Place of 16-byte vector c of row r in a tile
-    static __device__ __forceinline__ int swizzle(int r) {
-        return D == 64 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r & 3) << 2 | ((r >> 2) & 3);
-    }
 };
 
 template <int KV, int QT, int D, int NQ>
@@ -209,12 +200,13 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     using T = Chunk<KV, QT, D, NQ>;
     using S = Mat32<T::ST>;
     using V = Mat32<T::VT>;
-    constexpr int KS = T::KS, DB = T::DB, NI = T::NI, CH = T::CH, RPI = T::RPI;
+    constexpr int KS = T::KS, DB = T::DB, CB = T::CB;
     constexpr bool E = KV == WB_E4M3;
     constexpr float kThreshold = 4.f;
     __shared__ __attribute__((aligned(1024))) uint8_t stored[2][2][T::kTileBytes];        // [buffer][keys, values]
     __shared__ f32x4 scales[2][2][kTile / 4];
-    __shared__ int bad_page;
+    __shared__ uint32_t strange_bits[kTile][DB];                     // of the tile's values: columns of each token
+    __shared__ int strange, bad_page;
 
     Work w;
     if (!find_work<false>(A, blockIdx.x, w)) return;
@@ -222,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     if (w.parts > 1 && (tiles.from >= tiles.to || uint64_t(w.slot) >= uint64_t(A.slots))) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = lane >> 5, col = lane & 31;
-    if (tid == 0) bad_page = 0;
+    if (tid == 0) strange = bad_page = 0;
 
     // The lane's rows of q: row j of the block is head j % heads of token j / heads
     const int heads = A.heads, heads_here = min(heads, A.G - w.hb * heads);
@@ -248,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
         }
     }
     // (a scale of 0: scores of 0)
-    const float mul = A.scale == 0.f ? kLog2e : fabsf(A.scale) * kLog2e;
+    const float natural = A.scale == 0.f ? 1.f : fabsf(A.scale), mul = natural * kLog2e;
     // of the wavefront: the tokens that any row sees, and those that all of its rows see
     const int row0 = wave * NQ * 32;
     const int first_token = row0 / heads, last_token = min((row0 + NQ * 32 - 1) / heads, tokens - 1);
@@ -267,43 +259,48 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     }
 
     // ------------------------------------------------------------------ staging
-    // Instruction i of wavefront w takes rows (4 i + w) RPI ..+RPI-1 of a tile, which lie in one
-    // page: their page id and address are scalars, the lane's place in them never changes.
-    const int last = max(w.q.n - 1, 0) & ~(RPI - 1);
+    // A tile lies in LDS as blocks of 8 tokens by 64 columns, 1 KB each, block (c, g) at 1024 (8 c + g): keys a row of
+    // 128 bytes after the other, with the 16-byte vectors of row r at place (v ^ (r >> 1) & 7), values as two halves
+    // of 32 columns, 64 bytes a row. Wavefront w stages blocks of tokens 2 w and 2 w + 1. Those tokens lie in one page
+    // each: page id and address are scalars, the lane's place in them never changes.
+    const int last = max(w.q.n - 1, 0) & ~7;
     const __attribute__((address_space(4))) int32_t* table =
         (const __attribute__((address_space(4))) int32_t*)(A.table + size_t(w.r) * A.width);
     const int page_mask = (1 << A.page_log2) - 1;
-    auto token_of = [&](int t, int i) { return min(t * kTile + (4 * i + wave) * RPI, last); };
-    int ids[NI];
+    auto token_of = [&](int t, int j) { return min(t * kTile + 16 * wave + 8 * j, last); };
+    int ids[2];
     auto load_ids = [&](int t) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) ids[i] = table[token_of(t, i) >> A.page_log2];
+        for (int j = 0; j < 2; ++j) ids[j] = table[uint32_t(token_of(t, j)) >> A.page_log2];
     };
     int bad = 0;
-    auto base_of = [&](int t, int i) -> size_t {          // first value of the rows
-        const int page = ids[i];
-        const bool ok = page >= 0 && page < A.c.pages;
+    const uint32_t pages = uint32_t(A.c.pages);
+    auto base_of = [&](int t, int j) -> size_t {          // first value of the tokens
+        const bool ok = uint32_t(ids[j]) < pages;
         bad |= !ok;
-        return (((size_t(ok ? page : 0) * A.c.H + w.kvh) << A.page_log2) + (token_of(t, i) & page_mask)) * D;
+        const uint64_t row = (uint64_t(ok ? uint32_t(ids[j]) : 0u) * uint32_t(A.c.H) + uint32_t(w.kvh)) << A.page_log2;
+        return (row + uint32_t(token_of(t, j) & page_mask)) * D;
     };
-    const int row_in = lane / CH, vec_in = lane & (CH - 1);
-    uint32_t lane_off[2];               // (D = 256: rows of odd i swap vectors 2 further)
+    uint32_t key_off[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        lane_off[i] = uint32_t(row_in * D + 8 * (vec_in ^ T::swizzle((4 * i + wave) * RPI + row_in)));
-    u32x2 kr[E ? NI : 1], vr[E ? NI : 1];
+    for (int j = 0; j < 2; ++j) key_off[j] = uint32_t((lane >> 3) * D + 8 * ((lane & 7) ^ (((lane >> 4) & 3) | j << 2)));
+    const uint32_t value_off = uint32_t(((lane >> 2) & 7) * D + 32 * h + 8 * (lane & 3));
+    u32x2 kr[E ? 2 * CB : 1], vr[E ? 2 * CB : 1];
     float sr = 0.f;
     auto stage = [&](int t, int buf) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const size_t base = base_of(t, i);
-            if constexpr (E) {
-                kr[i] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(A.c.k) + base + lane_off[i & 1]);
-                vr[i] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(A.c.v) + base + lane_off[i & 1]);
-            } else {
-                uint8_t* to = &stored[buf][0][(4 * i + wave) * 1024];
-                lds_load16(static_cast<const uint16_t*>(A.c.k) + base + lane_off[i & 1], to);
-                lds_load16(static_cast<const uint16_t*>(A.c.v) + base + lane_off[i & 1], to + T::kTileBytes);
+        for (int j = 0; j < 2; ++j) {
+            const size_t base = base_of(t, j);
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+                if constexpr (E) {
+                    kr[j * CB + c] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(A.c.k) + base + 64 * c + key_off[j]);
+                    vr[j * CB + c] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(A.c.v) + base + 64 * c + value_off);
+                } else {
+                    uint8_t* to = &stored[buf][0][1024 * (8 * c + 2 * wave + j)];
+                    lds_load16(static_cast<const uint16_t*>(A.c.k) + base + 64 * c + key_off[j], to);
+                    lds_load16(static_cast<const uint16_t*>(A.c.v) + base + 64 * c + value_off, to + T::kTileBytes);
+                }
             }
         }
         if constexpr (E) {
@@ -319,62 +316,83 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     auto put = [&](int buf) {                            // 8-bit rows, converted
         if constexpr (E) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                uint8_t* to = &stored[buf][0][(4 * i + wave) * 1024 + lane * 16];
-                *reinterpret_cast<u32x4*>(to) = e4m3_to8<T::ST>(kr[i]);
-                *reinterpret_cast<u32x4*>(to + T::kTileBytes) = e4m3_to8<T::VT>(vr[i]);
-            }
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < CB; ++c) {
+                    uint8_t* to = &stored[buf][0][1024 * (8 * c + 2 * wave + j) + lane * 16];
+                    *reinterpret_cast<u32x4*>(to) = e4m3_to8<T::ST>(kr[j * CB + c]);
+                    *reinterpret_cast<u32x4*>(to + T::kTileBytes) = e4m3_to8<T::VT>(vr[j * CB + c]);
+                }
             if (wave < 2) reinterpret_cast<float*>(&scales[buf][wave][0])[lane] = sr;
         }
     };
 
     // ------------------------------------------------------------------ one tile
-    const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)&stored[0][0][0]));
-    const int k_at = col * D * 2, k_vec = h ^ T::swizzle(col);
-    // transposing reads: lane l points at 4 columns of token 4 h + (l % 16) / 4 (of 8)
-    const int v_row = 4 * h + ((lane & 15) >> 2), v_vec = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const int v_at = v_row * D * 2 + 8 * (lane & 1);
-
-    auto values = [&](auto masked_, int buf, int base, const u32x4 (&p)[NQ][4], const u32x4 (&p2)[T::kTwoP ? NQ : 1][4]) {
-        constexpr bool MASKED = decltype(masked_)::value;
-        const uint32_t from = lds0 + buf * 2 * T::kTileBytes + T::kTileBytes;
+    // The lane's places: vector 2 i + h of token `col` (4 of them, then 64 columns further), and, for the transposing
+    // reads, 4 columns of token 4 h + (l % 16) / 4 of 8
+    uint32_t key_at[4];
 #pragma unroll
-        for (int db = 0; db < DB; ++db) {
-            f32x16 hidden[NQ];
-            if constexpr (MASKED)
-                for (int qn = 0; qn < NQ; ++qn) hidden[qn] = f32x16{};
+    for (int i = 0; i < 4; ++i) key_at[i] = (col >> 3) * 1024 + (col & 7) * 128 + (((2 * i + h) ^ ((col >> 1) & 7)) << 4);
+    const uint32_t value_at = (4 * h + ((lane & 15) >> 2)) * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+
+    // Infinities and NaN among the values of a tile that some row does not see whole stay out of the products, where
+    // a weight of 0 would make NaN of them: each wavefront looks through its tokens; where there are any, they
+    // become 0 and their columns' bits are set. The rows that see such a token get their NaN behind the products.
+    auto strange_values = [&](int t, int buf) {
+        uint8_t* own_rows[2 * CB];
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < 2 * CB; ++i) {
+            own_rows[i] = &stored[buf][1][1024 * (8 * (i >> 1) + 2 * wave + (i & 1)) + lane * 16];
+            const u32x4 x = *reinterpret_cast<const u32x4*>(own_rows[i]);
+            any |= not_finite<T::VT>(x[0]) | not_finite<T::VT>(x[1]) | not_finite<T::VT>(x[2]) | not_finite<T::VT>(x[3]);
+        }
+        if (__any(any != 0) && lane == 0) strange = t + 1;
+        __syncthreads();
+        if (strange != t + 1) return false;
+#pragma unroll 1
+        for (int i = 0; i < 2 * CB; ++i) {
+            u32x4 x = *reinterpret_cast<const u32x4*>(own_rows[i]);
+            uint32_t bits = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t f = not_finite<T::VT>(x[e]) >> 15;          // bits 0 and 16
+                bits |= ((f | f >> 15) & 3u) << (2 * e);
+                x[e] &= ~(f * 0xFFFFu);
+            }
+            *reinterpret_cast<u32x4*>(own_rows[i]) = x;
+            // the lane holds columns 8 (lane % 4) ..+7 of half h of row (lane / 4) % 8
+            reinterpret_cast<uint8_t*>(&strange_bits[16 * wave + 8 * (i & 1) + ((lane >> 2) & 7)][2 * (i >> 1) + h])[lane & 3] = uint8_t(bits);
+        }
+        __syncthreads();
+        return true;
+    };
+    auto poison_rows = [&](int base) {
+#pragma unroll
+        for (int qn = 0; qn < NQ; ++qn)
+#pragma unroll
+            for (int db = 0; db < DB; ++db) {
+                uint32_t bits = 0;
+                const int from = max(lower[qn] - base, 0), to = min(limit[qn] - base, kTile);
+                for (int i = from; i < to; ++i) bits |= strange_bits[i][db];
+                bits >>= 4 * h;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (bits >> (8 * (i >> 2) + (i & 3)) & 1) acc[qn][db][i] = __builtin_nanf("");
+            }
+    };
+    auto values = [&](int buf, const u32x4 (&p)[NQ][4], const u32x4 (&p2)[T::kTwoP ? NQ : 1][4]) {
+        const uint8_t* from = &stored[buf][1][value_at];
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {                 // 16 tokens
                 u32x4 a;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int row = 16 * s + 8 * u;
-                    const uint32_t at = from + row * D * 2 + v_at + (((4 * db + v_vec) ^ T::swizzle(row + v_row)) << 4);
-                    const u32x2 x = __builtin_bit_cast(u32x2, read_transposed(at));
+                    const u32x2 x = __builtin_bit_cast(u32x2, read_transposed(from + 1024 * (8 * (db >> 1) + 2 * s + u) + 512 * (db & 1)));
                     a[2 * u] = x[0];
                     a[2 * u + 1] = x[1];
-                }
-                if constexpr (MASKED) {
-                    // Infinities and NaN stay out of the product, where a weight of 0 would make
-                    // NaN of them; a second one counts those that a row sees.
-                    u32x4 flag;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t f = (not_finite<T::VT>(a[e]) >> 15) * 0xFFFFu;
-                        flag[e] = f & V::kOnes;
-                        a[e] &= ~f;
-                    }
-#pragma unroll
-                    for (int qn = 0; qn < NQ; ++qn) {
-                        u32x4 seen;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tok = base + 16 * s + 8 * (e >> 1) + 4 * h + 2 * (e & 1);
-                            seen[e] = (tok >= lower[qn] && tok < limit[qn] ? V::kOnes & 0xFFFFu : 0u) |
-                                      (tok + 1 >= lower[qn] && tok + 1 < limit[qn] ? V::kOnes & 0xFFFF0000u : 0u);
-                        }
-                        hidden[qn] = V::mul(flag, seen, hidden[qn]);
-                    }
                 }
 #pragma unroll
                 for (int qn = 0; qn < NQ; ++qn) {
@@ -382,14 +400,9 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                     if constexpr (T::kTwoP) acc[qn][db] = V::mul(a, p2[qn][s], acc[qn][db]);
                 }
             }
-            if constexpr (MASKED)
-                for (int qn = 0; qn < NQ; ++qn)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[qn][db][i] = hidden[qn][i] > 0.f ? __builtin_nanf("") : acc[qn][db][i];
-        }
     };
 
-    auto compute = [&](int t, int buf) {
+    auto compute = [&](int t, int buf, bool found) {
         const int base = t * kTile;
         if (!active || base >= any_hi || base + kTile <= any_lo) return;
         const bool masked = base + kTile > all_hi || base < all_lo;
@@ -400,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
             for (int qn = 0; qn < NQ; ++qn) s[qn][b] = f32x16{};
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(&stored[buf][0][32 * b * D * 2 + k_at + ((k_vec ^ (2 * i)) << 4)]);
+                const u32x4 a = *reinterpret_cast<const u32x4*>(&stored[buf][0][key_at[i & 3] + 8192 * (i >> 2) + 4096 * b]);
 #pragma unroll
                 for (int qn = 0; qn < NQ; ++qn) s[qn][b] = S::mul(a, qf[qn][i], s[qn][b]);
             }
@@ -415,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                 }
             }
         }
-        uint32_t strange = 0;
         if (masked) {
 #pragma unroll
             for (int qn = 0; qn < NQ; ++qn)
@@ -426,11 +438,6 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                         const int tok = base + 32 * b + 8 * (i >> 2) + 4 * h + (i & 3);
                         if (tok < lower[qn] || tok >= limit[qn]) s[qn][b][i] = -INFINITY;
                     }
-#pragma unroll 4
-            for (int i = 0; i < T::kTileBytes / 1024; ++i) {
-                const u32x4 x = *reinterpret_cast<const u32x4*>(&stored[buf][1][i * 1024 + lane * 16]);
-                strange |= not_finite<T::VT>(x[0]) | not_finite<T::VT>(x[1]) | not_finite<T::VT>(x[2]) | not_finite<T::VT>(x[3]);
-            }
         }
         u32x4 p[NQ][4], p2[T::kTwoP ? NQ : 1][4];
 #pragma unroll
@@ -449,7 +456,16 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                 for (int db = 0; db < DB; ++db) acc[qn][db] *= keep;
                 m[qn] = m_new;
             }
-            const float ref = (m[qn] == -INFINITY ? 0.f : m[qn] * mul) - T::kShift;
+            float ref = (m[qn] == -INFINITY ? 0.f : m[qn] * mul) - T::kShift;
+            if (__any(!(fabsf(ref) < 0x1p100f))) {
+                // (scores near the ends of float32's range: their differences first)
+                const float by = m[qn] == -INFINITY ? 0.f : m[qn];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[qn][b][i] -= by;
+                ref = -T::kShift;
+            }
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -480,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                     }
                 }
         }
-        if (masked && __any(strange != 0)) values(std::true_type(), buf, base, p, p2);
-        else values(std::false_type(), buf, base, p, p2);
+        values(buf, p, p2);
+        if (found) poison_rows(base);
     };
 
     // ------------------------------------------------------------------ the part's tiles
@@ -499,7 +515,9 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
             stage(t + 1, buf ^ 1);
             load_ids(min(t + 2, tiles.to - 1));
         }
-        compute(t, buf);
+        const bool partial = (t + 1) * kTile > past + t0 + 1 || (A.window && t * kTile < past + t0 + tokens - A.window);
+        const bool found = partial && strange_values(t, buf);
+        compute(t, buf, found);
         if (E && t + 1 < tiles.to) put(buf ^ 1);
     }
     __syncthreads();
@@ -514,17 +532,17 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
         if (poison) total = __builtin_nanf("");
         if (w.parts == 1) {
             if (row_at[qn] < 0) continue;
-            const float by = total == 0.f ? 1.f : total;
+            const float by = total == 0.f ? 0.f : 1.f / total;
             uint16_t* o = static_cast<uint16_t*>(A.o) + row_at[qn] * D;
 #pragma unroll
             for (int db = 0; db < DB; ++db)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const f32x4 v = {acc[qn][db][4 * g], acc[qn][db][4 * g + 1], acc[qn][db][4 * g + 2], acc[qn][db][4 * g + 3]};
-                    *reinterpret_cast<u32x2*>(o + 32 * db + 8 * g + 4 * h) = quotients<QT>(v, by);
+                    *reinterpret_cast<u32x2*>(o + 32 * db + 8 * g + 4 * h) = scaled<QT>(v, by);
                 }
             if (A.lse && h == 0)
-                A.lse[row_at[qn]] = total == 0.f ? -INFINITY : (m[qn] * mul - T::kShift) * kLn2 + logf(total);
+                A.lse[row_at[qn]] = total == 0.f ? -INFINITY : m[qn] * natural + (logf(total) - T::kShift * kLn2);
         } else if (row_at[qn] >= 0) {
             const size_t at = size_t(w.slot) * T::kRows + (wave * NQ + qn) * 32 + col;
             float* o = A.part_o + at * D;
@@ -535,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                     *reinterpret_cast<f32x4*>(o + 32 * db + 8 * g + 4 * h) =
                         f32x4{acc[qn][db][4 * g], acc[qn][db][4 * g + 1], acc[qn][db][4 * g + 2], acc[qn][db][4 * g + 3]};
             if (h == 0) {
-                A.part_ml[2 * at] = m[qn] == -INFINITY ? -INFINITY : m[qn] * mul - T::kShift;
+                A.part_ml[2 * at] = m[qn];
                 A.part_ml[2 * at + 1] = total;
             }
         }
@@ -544,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
 
 // Joins the parts of split blocks: as many workgroups as parts, the p-th of a block for the
 // p-th share of its rows, a lane per 4 columns.
-template <int QT, int D>
+template <int QT, int D, int SHIFT>
 __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A) {
     Work w;
     if (!find_work<true>(A, blockIdx.x, w)) return;
@@ -553,6 +571,7 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
     const int heads_here = min(A.heads, A.G - w.hb * A.heads);
     const int64_t step = int64_t(A.c.H) * A.head_blocks;          // slots between a block's parts
     const Tiles all = tiles_of(A, w.q, w.block, 0, 1);
+    const float natural = A.scale == 0.f ? 1.f : fabsf(A.scale), mul = natural * kLog2e;
     for (int e = threadIdx.x; e < (r1 - r0) * (D / 4); e += kThreads) {
         const int j = r0 + e / (D / 4), d = 4 * (e % (D / 4));
         const int token = j / A.heads, head = j - token * A.heads;
@@ -567,15 +586,15 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
             const float mc = A.part_ml[2 * at], lc = A.part_ml[2 * at + 1];
             const f32x4 vc = *reinterpret_cast<const f32x4*>(A.part_o + at * D + d);
             const float top = fmaxf(m, mc), ref = top == -INFINITY ? 0.f : top;
-            const float f = __builtin_amdgcn_exp2f(m - ref), fc = __builtin_amdgcn_exp2f(mc - ref);
+            const float f = __builtin_amdgcn_exp2f((m - ref) * mul), fc = __builtin_amdgcn_exp2f((mc - ref) * mul);
             l = l * f + lc * fc;
             v = v * f + vc * fc;
             m = top;
         }
         const size_t row = (size_t(w.q.first) + w.block * A.tokens + token) * A.Hq + w.kvh * A.G + w.hb * A.heads + head;
-        const float by = l == 0.f ? 1.f : l;
-        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(A.o) + row * D + d) = quotients<QT>(v, by);
-        if (A.lse && d == 0) A.lse[row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+        const float by = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(A.o) + row * D + d) = scaled<QT>(v, by);
+        if (A.lse && d == 0) A.lse[row] = l == 0.f ? -INFINITY : m * natural + (logf(l) - SHIFT * kLn2);
     }
 }
 
@@ -588,7 +607,7 @@ hipError_t chunk_d(const ChunkArgs& a, hipStream_t s) {
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.slots) return e;
-    join_chunks_kernel<QT, D><<<unsigned(a.slots), kThreads, 0, s>>>(a);
+    join_chunks_kernel<QT, D, Chunk<KV, QT, D, 1>::kShift><<<unsigned(a.slots), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int KV, int QT>
