@@ -10,6 +10,8 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kTile = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -143,8 +145,9 @@ struct Mat32<WB_F16> {
     }
 };
 template <int T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    return uint32_t(Elem<T>::put(a)) | uint32_t(Elem<T>::put(b)) << 16;
+__device__ __forceinline__ uint32_t pack2(float a, float b) {        // (one instruction)
+    if constexpr (T == WB_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
 }
 template <int T>
 __device__ __forceinline__ float low(uint32_t w) { return Elem<T>::get(uint16_t(w)); }
@@ -171,6 +174,18 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
 
 __device__ __forceinline__ s16x4 read_transposed(const uint8_t* at) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
+}
+
+// 16 bytes a lane from `base` + `off` bytes straight to LDS (the lane's after `to`, which like `base` is the same for
+// all lanes). Written as assembly because behind the builtin the compiler lets every later read of LDS wait for all
+// such loads: the next tile's would not stay in flight behind this one's products. It writes no register, so there is
+// none for the compiler to use too early; lds_loads_wait() and a barrier come before the data is read.
+__device__ __forceinline__ void lds_load16_async(const void* base, uint32_t off, const uint8_t* to) {
+    const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) uint8_t*)to));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(base)
+                 : "memory");
 }
 
 // 4 columns of a finished row out to o; the row's log-sum-exp with its first
@@ -298,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                     vr[j * CB + c] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(A.c.v) + base + 64 * c + value_off);
                 } else {
                     uint8_t* to = &stored[buf][0][1024 * (8 * c + 2 * wave + j)];
-                    lds_load16(static_cast<const uint16_t*>(A.c.k) + base + 64 * c + key_off[j], to);
-                    lds_load16(static_cast<const uint16_t*>(A.c.v) + base + 64 * c + value_off, to + T::kTileBytes);
+                    lds_load16_async(static_cast<const uint16_t*>(A.c.k) + base + 64 * c, 2 * key_off[j], to);
+                    lds_load16_async(static_cast<const uint16_t*>(A.c.v) + base + 64 * c, 2 * value_off, to + T::kTileBytes);
                 }
             }
         }
@@ -339,12 +354,10 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     // a weight of 0 would make NaN of them: each wavefront looks through its tokens; where there are any, they
     // become 0 and their columns' bits are set. The rows that see such a token get their NaN behind the products.
     auto strange_values = [&](int t, int buf) {
-        uint8_t* own_rows[2 * CB];
         uint32_t any = 0;
 #pragma unroll
         for (int i = 0; i < 2 * CB; ++i) {
-            own_rows[i] = &stored[buf][1][1024 * (8 * (i >> 1) + 2 * wave + (i & 1)) + lane * 16];
-            const u32x4 x = *reinterpret_cast<const u32x4*>(own_rows[i]);
+            const u32x4 x = *reinterpret_cast<const u32x4*>(&stored[buf][1][1024 * (8 * (i >> 1) + 2 * wave + (i & 1)) + lane * 16]);
             any |= not_finite<T::VT>(x[0]) | not_finite<T::VT>(x[1]) | not_finite<T::VT>(x[2]) | not_finite<T::VT>(x[3]);
         }
         if (__any(any != 0) && lane == 0) strange = t + 1;
@@ -352,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
         if (strange != t + 1) return false;
 #pragma unroll 1
         for (int i = 0; i < 2 * CB; ++i) {
-            u32x4 x = *reinterpret_cast<const u32x4*>(own_rows[i]);
+            u32x4* at = reinterpret_cast<u32x4*>(&stored[buf][1][1024 * (8 * (i >> 1) + 2 * wave + (i & 1)) + lane * 16]);
+            u32x4 x = *at;
             uint32_t bits = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -360,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
                 bits |= ((f | f >> 15) & 3u) << (2 * e);
                 x[e] &= ~(f * 0xFFFFu);
             }
-            *reinterpret_cast<u32x4*>(own_rows[i]) = x;
+            *at = x;
             // the lane holds columns 8 (lane % 4) ..+7 of half h of row (lane / 4) % 8
             reinterpret_cast<uint8_t*>(&strange_bits[16 * wave + 8 * (i & 1) + ((lane >> 2) & 7)][2 * (i >> 1) + h])[lane & 3] = uint8_t(bits);
         }
@@ -430,14 +444,20 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
         }
         if (masked) {
 #pragma unroll
-            for (int qn = 0; qn < NQ; ++qn)
+            for (int qn = 0; qn < NQ; ++qn) {
+                const int to = limit[qn] - base - 4 * h, from = lower[qn] - base - 4 * h;
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int tok = base + 32 * b + 8 * (i >> 2) + 4 * h + (i & 3);
-                        if (tok < lower[qn] || tok >= limit[qn]) s[qn][b][i] = -INFINITY;
-                    }
+                    for (int i = 0; i < 16; ++i)
+                        if (32 * b + 8 * (i >> 2) + (i & 3) >= to) s[qn][b][i] = -INFINITY;
+                if (A.window)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (32 * b + 8 * (i >> 2) + (i & 3) < from) s[qn][b][i] = -INFINITY;
+            }
         }
         u32x4 p[NQ][4], p2[T::kTwoP ? NQ : 1][4];
 #pragma unroll
