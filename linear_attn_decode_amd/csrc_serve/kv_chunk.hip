@@ -13,7 +13,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves, kTile = 64;
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kTile = 64, kRows = 32 * kWaves;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------------------- where a workgroup works
@@ -176,16 +176,19 @@ __device__ __forceinline__ s16x4 read_transposed(const uint8_t* at) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
 }
 
-// 16 bytes a lane from `base` + `off` bytes straight to LDS (the lane's after `to`, which like `base` is the same for
-// all lanes). Written as assembly because behind the builtin the compiler lets every later read of LDS wait for all
-// such loads: the next tile's would not stay in flight behind this one's products. It writes no register, so there is
-// none for the compiler to use too early; lds_loads_wait() and a barrier come before the data is read.
-__device__ __forceinline__ void lds_load16_async(const void* base, uint32_t off, const uint8_t* to) {
-    const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) uint8_t*)to));
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(off), "s"(base)
-                 : "memory");
+// 16 bytes a lane from `base` + `off` bytes straight to LDS, the lane's after byte `to` of it (`base` and `to` are the same
+// for all lanes). Written as assembly because behind the builtin the compiler lets every later read of LDS wait for
+// all such loads: the next tile's would not stay in flight behind this one's products. It writes no register, so there
+// is none for the compiler to use too early; lds_loads_wait() and a barrier come before the data is read.
+__device__ __forceinline__ void lds_load16_async(const uint8_t* base, uint32_t off, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(off), "s"(base) : "memory");
+}
+
+// -infinity in place of x where d is negative. (A selection by sign bits: conditions in scalar registers, 32 of them
+// at once, would push what the loop keeps there out.)
+__device__ __forceinline__ float hide(float x, int d) {
+    const uint32_t gone = uint32_t(d >> 31);
+    return __uint_as_float((gone & 0xFF800000u) | (~gone & __float_as_uint(x)));
 }
 
 // 4 columns of a finished row out to o; the row's log-sum-exp with its first
@@ -194,10 +197,10 @@ __device__ __forceinline__ u32x2 scaled(f32x4 v, float by) {
     return u32x2{pack2<QT>(v[0] * by, v[1] * by), pack2<QT>(v[2] * by, v[3] * by)};
 }
 
-constexpr int waves_per_simd(int D, int NQ) { return D <= 128 && NQ == 1 ? 2 : 1; }
+constexpr int waves_per_simd(int D) { return D <= 128 ? 2 : 1; }
 
-// KV: the cache's type; QT: the type of q and o; D: columns; NQ: blocks of 32 rows a wavefront
-template <int KV, int QT, int D, int NQ>
+// KV: the cache's type; QT: the type of q and o; D: columns
+template <int KV, int QT, int D>
 struct Chunk {
     static constexpr int ST = QT;                                    // operands of the scores
     static constexpr int VT = KV == WB_E4M3 ? WB_BF16 : KV;          // of the values
@@ -206,17 +209,24 @@ struct Chunk {
     static constexpr int DB = D / 32;                                // blocks of value columns
     static constexpr int CB = D / 64;                                // blocks of 64 columns
     static constexpr int kShift = VT == WB_F16 ? 11 : 0;             // weights enter as 2^kShift times their value
-    static constexpr int kRows = 32 * NQ * kWaves;
     static constexpr int kTileBytes = kTile * D * 2;
 };
 
-template <int KV, int QT, int D, int NQ>
-__global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(const ChunkArgs A) {
-    using T = Chunk<KV, QT, D, NQ>;
+// The kernel's arguments, read again here: held from its start, or through its loop, they would cost registers there
+__device__ __forceinline__ const __attribute__((address_space(4))) ChunkArgs& arguments_again() {
+    auto p = (const __attribute__((address_space(4))) ChunkArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return *p;
+}
+
+template <int KV, int QT, int D>
+__global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(const ChunkArgs A) {
+    using T = Chunk<KV, QT, D>;
     using S = Mat32<T::ST>;
     using V = Mat32<T::VT>;
     constexpr int KS = T::KS, DB = T::DB, CB = T::CB;
     constexpr bool E = KV == WB_E4M3;
+    constexpr int kRowBytes = D * (E ? 1 : 2);
     constexpr float kThreshold = 4.f;
     __shared__ __attribute__((aligned(1024))) uint8_t stored[2][2][T::kTileBytes];        // [buffer][keys, values]
     __shared__ f32x4 scales[2][2][kTile / 4];
@@ -231,90 +241,84 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     const int h = lane >> 5, col = lane & 31;
     if (tid == 0) strange = bad_page = 0;
 
-    // The lane's rows of q: row j of the block is head j % heads of token j / heads
-    const int heads = A.heads, heads_here = min(heads, A.G - w.hb * heads);
-    const int past = w.q.n - w.q.m, t0 = w.block * A.tokens, tokens = min(A.tokens, w.q.m - t0);
-    int64_t row_at[NQ];                 // row of o and lse, or -1
-    int limit[NQ], lower[NQ];           // tokens [lower, limit) are seen
-    u32x4 qf[NQ][KS];
-#pragma unroll
-    for (int qn = 0; qn < NQ; ++qn) {
-        const int j = (wave * NQ + qn) * 32 + col, token = j / heads, head = j - token * heads;
-        const bool ok = token < tokens && head < heads_here;
-        const int64_t row = int64_t(w.q.first) + t0 + token;
-        const int hq = w.kvh * A.G + w.hb * heads + head;
-        row_at[qn] = ok ? row * A.Hq + hq : -1;
-        limit[qn] = ok ? past + t0 + token + 1 : 0;
-        lower[qn] = A.window ? max(limit[qn] - A.window, 0) : 0;
-        const uint16_t* q = static_cast<const uint16_t*>(A.q) + row * A.q_row + int64_t(hq) * A.q_head + 8 * h;
+    const auto& C = arguments_again();
+
+    // The lane's row of q: row j of the block is head j % heads of token j / heads
+    const int past = w.q.n - w.q.m, t0 = w.block * C.tokens, tokens = min(C.tokens, w.q.m - t0);
+    int limit, lower;                   // tokens [lower, limit) are seen
+    u32x4 qf[KS];
+    {
+        const int j = wave * 32 + col, token = j / C.heads, head = j - token * C.heads;
+        const bool ok = token < tokens && head < min(C.heads, C.G - w.hb * C.heads);
+        const int hq = w.kvh * C.G + w.hb * C.heads + head;
+        limit = ok ? past + t0 + token + 1 : 0;
+        lower = C.window ? max(limit - C.window, 0) : 0;
+        const uint16_t* q = static_cast<const uint16_t*>(C.q) + (int64_t(w.q.first) + t0 + token) * C.q_row +
+                            int64_t(hq) * C.q_head + 8 * h;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
-            qf[qn][i] = u32x4{0, 0, 0, 0};
-            if (ok && A.scale != 0.f) qf[qn][i] = *reinterpret_cast<const u32x4*>(q + 16 * i);
-            if (A.scale < 0.f) qf[qn][i] ^= 0x80008000u;
+            qf[i] = u32x4{0, 0, 0, 0};
+            if (ok && C.scale != 0.f) qf[i] = *reinterpret_cast<const u32x4*>(q + 16 * i);
+            if (C.scale < 0.f) qf[i] ^= 0x80008000u;
         }
     }
     // (a scale of 0: scores of 0)
-    const float natural = A.scale == 0.f ? 1.f : fabsf(A.scale), mul = natural * kLog2e;
-    // of the wavefront: the tokens that any row sees, and those that all of its rows see
-    const int row0 = wave * NQ * 32;
-    const int first_token = row0 / heads, last_token = min((row0 + NQ * 32 - 1) / heads, tokens - 1);
-    const bool active = first_token < tokens;
-    const int any_hi = past + t0 + last_token + 1, all_hi = past + t0 + first_token + 1;
-    const int any_lo = A.window ? max(all_hi - A.window, 0) : 0, all_lo = A.window ? max(any_hi - A.window, 0) : 0;
+    const float mul = (C.scale == 0.f ? 1.f : fabsf(C.scale)) * kLog2e;
+    // Tiles that some row of the wavefront sees, and those of which every row of the block sees all
+    const int first_token = wave * 32 / C.heads, last_token = min((wave * 32 + 31) / C.heads, tokens - 1);
+    int any_from = C.window ? max(past + t0 + first_token + 1 - C.window, 0) / kTile : 0;
+    int any_to = first_token < tokens ? (past + t0 + last_token + kTile) / kTile : 0;
+    const int whole_from = C.window ? (max(past + t0 + tokens - C.window, 0) + kTile - 1) / kTile : 0;
+    const int whole_to = (past + t0 + 1) / kTile;
+    const bool windowed = C.window != 0;
 
-    f32x16 acc[NQ][DB];
-    float m[NQ], l[NQ];
+    f32x16 acc[DB];
 #pragma unroll
-    for (int qn = 0; qn < NQ; ++qn) {
-#pragma unroll
-        for (int i = 0; i < DB; ++i) acc[qn][i] = f32x16{};
-        m[qn] = -INFINITY;
-        l[qn] = 0.f;
-    }
+    for (int i = 0; i < DB; ++i) acc[i] = f32x16{};
+    float m = -INFINITY, l = 0.f;
 
     // ------------------------------------------------------------------ staging
     // A tile lies in LDS as blocks of 8 tokens by 64 columns, 1 KB each, block (c, g) at 1024 (8 c + g): keys a row of
     // 128 bytes after the other, with the 16-byte vectors of row r at place (v ^ (r >> 1) & 7), values as two halves
     // of 32 columns, 64 bytes a row. Wavefront w stages blocks of tokens 2 w and 2 w + 1. Those tokens lie in one page
     // each: page id and address are scalars, the lane's place in them never changes.
-    const int last = max(w.q.n - 1, 0) & ~7;
+    const int last = max(w.q.n - 1, 0) & ~7, log2 = C.page_log2;
     const __attribute__((address_space(4))) int32_t* table =
-        (const __attribute__((address_space(4))) int32_t*)(A.table + size_t(w.r) * A.width);
-    const int page_mask = (1 << A.page_log2) - 1;
-    auto token_of = [&](int t, int j) { return min(t * kTile + 16 * wave + 8 * j, last); };
-    int ids[2];
+        (const __attribute__((address_space(4))) int32_t*)(C.table + size_t(w.r) * C.width);
+    const uint32_t pages = uint32_t(C.c.pages), page_rows = uint32_t(C.c.H) << log2;
+    const uint8_t* const k0 = static_cast<const uint8_t*>(C.c.k) + (size_t(w.kvh) << log2) * kRowBytes;
+    const uint8_t* const v0 = static_cast<const uint8_t*>(C.c.v) + (size_t(w.kvh) << log2) * kRowBytes;
+    auto token_of = [&](int t, int j) { return uint32_t(min(t * kTile + 16 * wave + 8 * j, last)); };
+    uint32_t ids[2], bad = 0;
     auto load_ids = [&](int t) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) ids[j] = table[uint32_t(token_of(t, j)) >> A.page_log2];
+        for (int j = 0; j < 2; ++j) ids[j] = uint32_t(table[token_of(t, j) >> log2]);
     };
-    int bad = 0;
-    const uint32_t pages = uint32_t(A.c.pages);
-    auto base_of = [&](int t, int j) -> size_t {          // first value of the tokens
-        const bool ok = uint32_t(ids[j]) < pages;
-        bad |= !ok;
-        const uint64_t row = (uint64_t(ok ? uint32_t(ids[j]) : 0u) * uint32_t(A.c.H) + uint32_t(w.kvh)) << A.page_log2;
-        return (row + uint32_t(token_of(t, j) & page_mask)) * D;
-    };
-    uint32_t key_off[2];
+    uint32_t key_off[2], value_off;          // bytes, in the tokens' rows
 #pragma unroll
-    for (int j = 0; j < 2; ++j) key_off[j] = uint32_t((lane >> 3) * D + 8 * ((lane & 7) ^ (((lane >> 4) & 3) | j << 2)));
-    const uint32_t value_off = uint32_t(((lane >> 2) & 7) * D + 32 * h + 8 * (lane & 3));
+    for (int j = 0; j < 2; ++j) key_off[j] = (lane >> 3) * kRowBytes + (E ? 8 : 16) * ((lane & 7) ^ (((lane >> 4) & 3) | j << 2));
+    value_off = ((lane >> 2) & 7) * kRowBytes + (E ? 8 : 16) * (4 * h + (lane & 3));
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+                       uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)&stored[0][0][0]))) + 2048 * wave;
     u32x2 kr[E ? 2 * CB : 1], vr[E ? 2 * CB : 1];
     float sr = 0.f;
     auto stage = [&](int t, int buf) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const size_t base = base_of(t, j);
+            const uint32_t id = ids[j] < pages ? ids[j] : 0u;
+            bad |= id ^ ids[j];                                  // (not 0 for an id outside the cache)
+            const uint64_t at = (uint64_t(id) * page_rows + (token_of(t, j) & ((1u << log2) - 1))) * kRowBytes;
+            const uint8_t* k = k0 + at;
+            const uint8_t* v = v0 + at;
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
                 if constexpr (E) {
-                    kr[j * CB + c] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(A.c.k) + base + 64 * c + key_off[j]);
-                    vr[j * CB + c] = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(A.c.v) + base + 64 * c + value_off);
+                    kr[j * CB + c] = *reinterpret_cast<const u32x2*>(k + 64 * c + key_off[j]);
+                    vr[j * CB + c] = *reinterpret_cast<const u32x2*>(v + 64 * c + value_off);
                 } else {
-                    uint8_t* to = &stored[buf][0][1024 * (8 * c + 2 * wave + j)];
-                    lds_load16_async(static_cast<const uint16_t*>(A.c.k) + base + 64 * c, 2 * key_off[j], to);
-                    lds_load16_async(static_cast<const uint16_t*>(A.c.v) + base + 64 * c, 2 * value_off, to + T::kTileBytes);
+                    const uint32_t to = lds0 + 2 * T::kTileBytes * buf + 8192 * c + 1024 * j;
+                    lds_load16_async(k + 128 * c, key_off[j], to);
+                    lds_load16_async(v + 128 * c, value_off, to + T::kTileBytes);
                 }
             }
         }
@@ -322,9 +326,9 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
             // scales of the tile's tokens: keys' by wavefront 0, values' by wavefront 1
             if (wave < 2) {
                 const int tok = min(t * kTile + lane, max(w.q.n - 1, 0));
-                int page = A.table[size_t(w.r) * A.width + (tok >> A.page_log2)];
-                page = page >= 0 && page < A.c.pages ? page : 0;
-                sr = (wave ? A.c.v_scale : A.c.k_scale)[((size_t(page) * A.c.H + w.kvh) << A.page_log2) + (tok & page_mask)];
+                uint32_t page = uint32_t(C.table[size_t(w.r) * C.width + (tok >> log2)]);
+                page = page < pages ? page : 0;
+                sr = (wave ? C.c.v_scale : C.c.k_scale)[uint64_t(page) * page_rows + (uint32_t(w.kvh) << log2) + (tok & ((1 << log2) - 1))];
             }
         }
     };
@@ -343,13 +347,6 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     };
 
     // ------------------------------------------------------------------ one tile
-    // The lane's places: vector 2 i + h of token `col` (4 of them, then 64 columns further), and, for the transposing
-    // reads, 4 columns of token 4 h + (l % 16) / 4 of 8
-    uint32_t key_at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) key_at[i] = (col >> 3) * 1024 + (col & 7) * 128 + (((2 * i + h) ^ ((col >> 1) & 7)) << 4);
-    const uint32_t value_at = (4 * h + ((lane & 15) >> 2)) * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-
     // Infinities and NaN among the values of a tile that some row does not see whole stay out of the products, where
     // a weight of 0 would make NaN of them: each wavefront looks through its tokens; where there are any, they
     // become 0 and their columns' bits are set. The rows that see such a token get their NaN behind the products.
@@ -383,141 +380,134 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
     };
     auto poison_rows = [&](int base) {
 #pragma unroll
-        for (int qn = 0; qn < NQ; ++qn)
+        for (int db = 0; db < DB; ++db) {
+            uint32_t bits = 0;
+            const int from = max(lower - base, 0), to = min(limit - base, kTile);
+            for (int i = from; i < to; ++i) bits |= strange_bits[i][db];
+            bits >>= 4 * h;
 #pragma unroll
-            for (int db = 0; db < DB; ++db) {
-                uint32_t bits = 0;
-                const int from = max(lower[qn] - base, 0), to = min(limit[qn] - base, kTile);
-                for (int i = from; i < to; ++i) bits |= strange_bits[i][db];
-                bits >>= 4 * h;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (bits >> (8 * (i >> 2) + (i & 3)) & 1) acc[qn][db][i] = __builtin_nanf("");
-            }
-    };
-    auto values = [&](int buf, const u32x4 (&p)[NQ][4], const u32x4 (&p2)[T::kTwoP ? NQ : 1][4]) {
-        const uint8_t* from = &stored[buf][1][value_at];
-#pragma unroll
-        for (int db = 0; db < DB; ++db)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {                 // 16 tokens
-                u32x4 a;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const u32x2 x = __builtin_bit_cast(u32x2, read_transposed(from + 1024 * (8 * (db >> 1) + 2 * s + u) + 512 * (db & 1)));
-                    a[2 * u] = x[0];
-                    a[2 * u + 1] = x[1];
-                }
-#pragma unroll
-                for (int qn = 0; qn < NQ; ++qn) {
-                    acc[qn][db] = V::mul(a, p[qn][s], acc[qn][db]);
-                    if constexpr (T::kTwoP) acc[qn][db] = V::mul(a, p2[qn][s], acc[qn][db]);
-                }
-            }
+            for (int i = 0; i < 16; ++i)
+                acc[db][i] = __uint_as_float(__float_as_uint(acc[db][i]) |
+                                             (uint32_t(int(bits << (31 - 8 * (i >> 2) - (i & 3))) >> 31) & 0x7FC00000u));      // (NaN)
+        }
     };
 
-    auto compute = [&](int t, int buf, bool found) {
-        const int base = t * kTile;
-        if (!active || base >= any_hi || base + kTile <= any_lo) return;
-        const bool masked = base + kTile > all_hi || base < all_lo;
-        f32x16 s[NQ][2];
+    // The lane's places: vector 2 i + h of token `col` (4 of them, then 64 columns further), and, for the transposing
+    // reads, 4 columns of token 4 h + (l % 16) / 4 of 8
+    uint32_t key_at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) key_at[i] = (col >> 3) * 1024 + (col & 7) * 128 + (((2 * i + h) ^ ((col >> 1) & 7)) << 4);
+    const uint32_t value_at = (4 * h + ((lane & 15) >> 2)) * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+
+    auto compute = [&](int t, int buf) {
+        const bool partial = t < whole_from || t >= whole_to;
+        const bool found = partial && strange_values(t, buf);
+        if (t < any_from || t >= any_to) return;
+        int to = limit - t * kTile - 4 * h, from = lower - t * kTile - 4 * h;         // of the lane's tokens
+        f32x16 s[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-#pragma unroll
-            for (int qn = 0; qn < NQ; ++qn) s[qn][b] = f32x16{};
+            s[b] = f32x16{};
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 const u32x4 a = *reinterpret_cast<const u32x4*>(&stored[buf][0][key_at[i & 3] + 8192 * (i >> 2) + 4096 * b]);
-#pragma unroll
-                for (int qn = 0; qn < NQ; ++qn) s[qn][b] = S::mul(a, qf[qn][i], s[qn][b]);
+                s[b] = S::mul(a, qf[i], s[b]);
             }
             if constexpr (E) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const f32x4 ks = scales[buf][0][8 * b + 2 * g + h];
 #pragma unroll
-                    for (int qn = 0; qn < NQ; ++qn)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) s[qn][b][4 * g + e] *= ks[e];
+                    for (int e = 0; e < 4; ++e) s[b][4 * g + e] *= ks[e];
                 }
             }
         }
-        if (masked) {
+        if (partial) {
+            asm volatile("" : "+v"(to), "+v"(from));             // (or every tile would go through the selections)
 #pragma unroll
-            for (int qn = 0; qn < NQ; ++qn) {
-                const int to = limit[qn] - base - 4 * h, from = lower[qn] - base - 4 * h;
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[b][i] = hide(s[b][i], to - 1 - (32 * b + 8 * (i >> 2) + (i & 3)));
+            if (windowed)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (32 * b + 8 * (i >> 2) + (i & 3) >= to) s[qn][b][i] = -INFINITY;
-                if (A.window)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (32 * b + 8 * (i >> 2) + (i & 3) < from) s[qn][b][i] = -INFINITY;
-            }
+                    for (int i = 0; i < 16; ++i) s[b][i] = hide(s[b][i], 32 * b + 8 * (i >> 2) + (i & 3) - from);
         }
-        u32x4 p[NQ][4], p2[T::kTwoP ? NQ : 1][4];
+        float top = -INFINITY;
 #pragma unroll
-        for (int qn = 0; qn < NQ; ++qn) {
-            float top = -INFINITY;
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+        top = max_xor32(top);
+        if (__any((top - m) * mul > kThreshold)) {
+            const float m_new = fmaxf(m, top);
+            const float keep = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - m_new) * mul);
+            l *= keep;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[qn][b][i]);
-            top = max_xor32(top);
-            if (__any((top - m[qn]) * mul > kThreshold)) {
-                const float m_new = fmaxf(m[qn], top);
-                const float keep = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[qn] - m_new) * mul);
-                l[qn] *= keep;
-#pragma unroll
-                for (int db = 0; db < DB; ++db) acc[qn][db] *= keep;
-                m[qn] = m_new;
-            }
-            float ref = (m[qn] == -INFINITY ? 0.f : m[qn] * mul) - T::kShift;
-            if (__any(!(fabsf(ref) < 0x1p100f))) {
-                // (scores near the ends of float32's range: their differences first)
-                const float by = m[qn] == -INFINITY ? 0.f : m[qn];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[qn][b][i] -= by;
-                ref = -T::kShift;
-            }
+            for (int db = 0; db < DB; ++db) acc[db] *= keep;
+            m = m_new;
+        }
+        float ref = (m == -INFINITY ? 0.f : m * mul) - T::kShift;
+        if (__any(!(fabsf(ref) < 0x1p100f))) {
+            // (scores near the ends of float32's range: their differences first)
+            const float by = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float e[4];
+                for (int i = 0; i < 16; ++i) s[b][i] -= by;
+            ref = -T::kShift;
+        }
+        u32x4 p[4], p2[T::kTwoP ? 4 : 1];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[qn][b][4 * g + k], mul, -ref));
-                        l[qn] += e[k];
-                    }
-                    if constexpr (E) {
-                        const f32x4 vs = scales[buf][1][8 * b + 2 * g + h];
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][4 * g + k], mul, -ref));
+                    l += e[k];
+                }
+                if constexpr (E) {
+                    const f32x4 vs = scales[buf][1][8 * b + 2 * g + h];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) e[k] *= vs[k];
+                    if (partial) {                              // (a hidden token's scale may be anything)
+                        asm volatile("" : "+v"(to), "+v"(from));
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            e[k] *= vs[k];
-                            const int tok = base + 32 * b + 8 * g + 4 * h + k;
-                            if (masked && (tok < lower[qn] || tok >= limit[qn])) e[k] = 0.f;      // (its scale may be anything)
+                            const int tok = 32 * b + 8 * g + k;
+                            e[k] = __uint_as_float(__float_as_uint(e[k]) & ~uint32_t(((to - 1 - tok) | (tok - from)) >> 31));
                         }
                     }
-                    u32x4& to = p[qn][2 * b + (g >> 1)];
-                    to[2 * (g & 1)] = pack2<T::VT>(e[0], e[1]);
-                    to[2 * (g & 1) + 1] = pack2<T::VT>(e[2], e[3]);
-                    if constexpr (T::kTwoP) {
-                        u32x4& to2 = p2[qn][2 * b + (g >> 1)];
-                        const uint32_t h0 = to[2 * (g & 1)], h1 = to[2 * (g & 1) + 1];
-                        to2[2 * (g & 1)] = pack2<T::VT>(e[0] - low<T::VT>(h0), e[1] - high<T::VT>(h0));
-                        to2[2 * (g & 1) + 1] = pack2<T::VT>(e[2] - low<T::VT>(h1), e[3] - high<T::VT>(h1));
-                    }
                 }
-        }
-        values(buf, p, p2);
-        if (found) poison_rows(base);
+                u32x4& x = p[2 * b + (g >> 1)];
+                x[2 * (g & 1)] = pack2<T::VT>(e[0], e[1]);
+                x[2 * (g & 1) + 1] = pack2<T::VT>(e[2], e[3]);
+                if constexpr (T::kTwoP) {
+                    u32x4& y = p2[2 * b + (g >> 1)];
+                    const uint32_t h0 = x[2 * (g & 1)], h1 = x[2 * (g & 1) + 1];
+                    y[2 * (g & 1)] = pack2<T::VT>(e[0] - low<T::VT>(h0), e[1] - high<T::VT>(h0));
+                    y[2 * (g & 1) + 1] = pack2<T::VT>(e[2] - low<T::VT>(h1), e[3] - high<T::VT>(h1));
+                }
+            }
+        const uint8_t* values = &stored[buf][1][value_at];
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int s4 = 0; s4 < 4; ++s4) {              // 16 tokens
+                u32x4 a;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const u32x2 x = __builtin_bit_cast(u32x2, read_transposed(values + 1024 * (8 * (db >> 1) + 2 * s4 + u) + 512 * (db & 1)));
+                    a[2 * u] = x[0];
+                    a[2 * u + 1] = x[1];
+                }
+                acc[db] = V::mul(a, p[s4], acc[db]);
+                if constexpr (T::kTwoP) acc[db] = V::mul(a, p2[s4], acc[db]);
+            }
+        if (found) poison_rows(t * kTile);
     };
 
     // ------------------------------------------------------------------ the part's tiles
@@ -527,55 +517,51 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D, NQ)) chunk_kernel(
         load_ids(min(tiles.from + 1, tiles.to - 1));
         put(0);
     }
+    int buf = 0;
     for (int t = tiles.from; t < tiles.to; ++t) {
-        const int buf = (t - tiles.from) & 1;
         lds_loads_wait();
         __syncthreads();
         if (t + 1 < tiles.to) {
             stage(t + 1, buf ^ 1);
             load_ids(min(t + 2, tiles.to - 1));
         }
-        const bool partial = (t + 1) * kTile > past + t0 + 1 || (A.window && t * kTile < past + t0 + tokens - A.window);
-        const bool found = partial && strange_values(t, buf);
-        compute(t, buf, found);
+        compute(t, buf);
         if (E && t + 1 < tiles.to) put(buf ^ 1);
+        buf ^= 1;
     }
     __syncthreads();
     if (bad && lane == 0) bad_page = 1;
     __syncthreads();
-    const bool poison = w.q.bad || bad_page;
 
     // ------------------------------------------------------------------ sums out
+    const auto& B = arguments_again();
+    l = w.q.bad || bad_page ? __builtin_nanf("") : add_xor32_f32(l);
+    const int j = wave * 32 + col, token = j / B.heads, head = j - token * B.heads;
+    if (token >= tokens || head >= min(B.heads, B.G - w.hb * B.heads)) return;
+    if (w.parts == 1) {
+        const size_t row = (size_t(w.q.first) + t0 + token) * B.Hq + w.kvh * B.G + w.hb * B.heads + head;
+        const float by = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* o = static_cast<uint16_t*>(B.o) + row * D + 4 * h;
 #pragma unroll
-    for (int qn = 0; qn < NQ; ++qn) {
-        float total = add_xor32_f32(l[qn]);
-        if (poison) total = __builtin_nanf("");
-        if (w.parts == 1) {
-            if (row_at[qn] < 0) continue;
-            const float by = total == 0.f ? 0.f : 1.f / total;
-            uint16_t* o = static_cast<uint16_t*>(A.o) + row_at[qn] * D;
+        for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<u32x2*>(o + 32 * db + 8 * g) =
+                    scaled<QT>(f32x4{acc[db][4 * g], acc[db][4 * g + 1], acc[db][4 * g + 2], acc[db][4 * g + 3]}, by);
+        if (B.lse && h == 0)
+            B.lse[row] = l == 0.f ? -INFINITY : m * (B.scale == 0.f ? 1.f : fabsf(B.scale)) + (logf(l) - T::kShift * kLn2);
+    } else {
+        const size_t at = size_t(w.slot) * kRows + j;
+        float* o = B.part_o + at * D + 4 * h;
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const f32x4 v = {acc[qn][db][4 * g], acc[qn][db][4 * g + 1], acc[qn][db][4 * g + 2], acc[qn][db][4 * g + 3]};
-                    *reinterpret_cast<u32x2*>(o + 32 * db + 8 * g + 4 * h) = scaled<QT>(v, by);
-                }
-            if (A.lse && h == 0)
-                A.lse[row_at[qn]] = total == 0.f ? -INFINITY : m[qn] * natural + (logf(total) - T::kShift * kLn2);
-        } else if (row_at[qn] >= 0) {
-            const size_t at = size_t(w.slot) * T::kRows + (wave * NQ + qn) * 32 + col;
-            float* o = A.part_o + at * D;
+        for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int db = 0; db < DB; ++db)
-#pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    *reinterpret_cast<f32x4*>(o + 32 * db + 8 * g + 4 * h) =
-                        f32x4{acc[qn][db][4 * g], acc[qn][db][4 * g + 1], acc[qn][db][4 * g + 2], acc[qn][db][4 * g + 3]};
-            if (h == 0) {
-                A.part_ml[2 * at] = m[qn];
-                A.part_ml[2 * at + 1] = total;
-            }
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4*>(o + 32 * db + 8 * g) =
+                    f32x4{acc[db][4 * g], acc[db][4 * g + 1], acc[db][4 * g + 2], acc[db][4 * g + 3]};
+        if (h == 0) {
+            B.part_ml[2 * at] = m;
+            B.part_ml[2 * at + 1] = l;
         }
     }
 }
@@ -602,7 +588,7 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
             const int64_t slot = w.slot0 + p * step;
             const int64_t n = all.to - all.from;
             if (n * p / w.parts >= n * (p + 1) / w.parts || uint64_t(slot) >= uint64_t(A.slots)) continue;      // (a part without tiles)
-            const size_t at = size_t(slot) * A.rows + j;
+            const size_t at = size_t(slot) * kRows + j;
             const float mc = A.part_ml[2 * at], lc = A.part_ml[2 * at + 1];
             const f32x4 vc = *reinterpret_cast<const f32x4*>(A.part_o + at * D + d);
             const float top = fmaxf(m, mc), ref = top == -INFINITY ? 0.f : top;
@@ -620,14 +606,10 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
 
 template <int KV, int QT, int D>
 hipError_t chunk_d(const ChunkArgs& a, hipStream_t s) {
-    if (D <= 128 && a.rows == 256) {
-        if constexpr (D <= 128) chunk_kernel<KV, QT, D, 2><<<a.groups, kThreads, 0, s>>>(a);
-    } else {
-        chunk_kernel<KV, QT, D, 1><<<a.groups, kThreads, 0, s>>>(a);
-    }
+    chunk_kernel<KV, QT, D><<<unsigned(a.groups), kThreads, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.slots) return e;
-    join_chunks_kernel<QT, D, Chunk<KV, QT, D, 1>::kShift><<<unsigned(a.slots), kThreads, 0, s>>>(a);
+    join_chunks_kernel<QT, D, Chunk<KV, QT, D>::kShift><<<unsigned(a.slots), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 template <int KV, int QT>
@@ -647,13 +629,11 @@ constexpr int kPartTiles = 4;
 ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width) {
     const int G = Hq / c.H;
     ChunkPlan p;
-    // rows of a block: 128, or 256 where a wavefront's registers hold 64 and requests have as many
-    p.rows = 128;
-    p.heads = G < p.rows ? G : p.rows;
+    p.heads = G < kRows ? G : kRows;
     p.head_blocks = (G + p.heads - 1) / p.heads;
-    p.tokens = p.rows / p.heads;
+    p.tokens = kRows / p.heads;
     p.part_tiles = kPartTiles;
-    p.target = 256 * waves_per_simd(c.D, p.rows / 128);
+    p.target = 256 * waves_per_simd(c.D);
     const int64_t by_tokens = int64_t(N) / p.tokens + R, blocks = (N < by_tokens ? N : by_tokens) * int64_t(c.H) * p.head_blocks;
     const int64_t tiles = (int64_t(width) * c.page + kTile - 1) / kTile;
     p.slots = 0;
@@ -664,8 +644,8 @@ ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width) {
         p.slots = most < 2 * p.target ? most : 2 * p.target;
     }
     p.groups = blocks + (p.slots ? p.target : 0);
-    p.part_o_bytes = size_t(p.slots) * p.rows * c.D * 4;
-    p.part_ml_bytes = size_t(p.slots) * p.rows * 8;
+    p.part_o_bytes = size_t(p.slots) * kRows * c.D * 4;
+    p.part_ml_bytes = size_t(p.slots) * kRows * 8;
     return p;
 }
 

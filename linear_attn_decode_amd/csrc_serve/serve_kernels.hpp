@@ -89,20 +89,19 @@ struct ChunkArgs {
     const int32_t* starts = nullptr;
     void* o = nullptr;
     float* lse = nullptr;
-    float* part_o = nullptr;      // [slots][rows][D] sums of the parts of split blocks
-    float* part_ml = nullptr;     // [slots][rows][2] their maximum and weight sum
+    float* part_o = nullptr;      // [slots][128][D] sums of the parts of split blocks
+    float* part_ml = nullptr;     // [slots][128][2] their maximum and weight sum
     float scale = 0.f;
     int N = 0, R = 0, Hq = 0, width = 0, window = 0, q_dtype = 0, page_log2 = 0;
     int G = 1;                    // query heads of a key-value head
-    int rows = 0;                 // of a block: `heads` query heads of `tokens` new tokens
-    int heads = 1, tokens = 1;
+    int heads = 1, tokens = 1;    // of a block of rows: query heads of new tokens
     int head_blocks = 1;          // blocks of a key-value head's query heads
     int part_tiles = 1;           // key tiles of a part at least
     int target = 1;               // parts that all tiles are cut into, about
     int64_t slots = 0, groups = 0;
 };
 struct ChunkPlan {
-    int rows, heads, tokens, head_blocks, part_tiles, target;
+    int heads, tokens, head_blocks, part_tiles, target;
     int64_t slots, groups;        // parts of split blocks at most (0: nothing is split); workgroups
     size_t part_o_bytes, part_ml_bytes;
 };

@@ -293,7 +293,6 @@ int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t 
     a.q_dtype = q_dtype;
     a.page_log2 = page_log2(c->page);
     a.G = Hq / c->H;
-    a.rows = p.rows;
     a.heads = p.heads;
     a.tokens = p.tokens;
     a.head_blocks = p.head_blocks;
