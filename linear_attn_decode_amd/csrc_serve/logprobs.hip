@@ -103,8 +103,13 @@ __device__ __forceinline__ void first_keys(uint64_t* keys, int n, int K, uint64_
         if (tid < n) {
             const uint64_t mine = keys[tid];
             int place = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) place += keys[j] > mine;
+            const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(keys);
+#pragma unroll 8
+            for (int j = 0; j < n / 2; ++j) {
+                const ulonglong2 k = pairs[j];
+                place += (k.x > mine) + (k.y > mine);
+            }
+            if (n & 1) place += keys[n - 1] > mine;
             if (place < K) out[place] = mine;
         }
         __syncthreads();
@@ -133,8 +138,8 @@ __device__ __forceinline__ void first_keys(uint64_t* keys, int n, int K, uint64_
 template <int T, bool TOP>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A) {
     // chunks' maxima, then vectors' (64 of each of the top K chunks), then columns
-    constexpr int kKeys = TOP ? kMaxTop * 64 : 1;
-    __shared__ uint64_t keys[kKeys];
+    constexpr int kKeys = TOP ? kMaxTop * 64 : 2;
+    __shared__ __attribute__((aligned(16))) uint64_t keys[kKeys];
     __shared__ uint64_t first[TOP ? kMaxTop : 1];
     __shared__ float sums[kWaves][3];
     __shared__ int count, is_last;
@@ -296,14 +301,15 @@ hipError_t logprobs_t(const LogprobArgs& a, unsigned groups, hipStream_t s) {
 
 }  // namespace
 
-// Segments of a row: enough for 1024 workgroups (4 a compute unit), of 8 chunks (one a wavefront) at
-// least; joined parts' keys fit the 4096 of LDS, and so do a segment's chunks.
+// Segments of a row: enough for 1024 workgroups (4 a compute unit), of 32 chunks at least, and of 3 K / 2 where
+// alternatives are wanted (with K chunks or fewer in a segment none of its vectors could be left out); joined parts'
+// keys fit the 4096 of LDS, and so do a segment's chunks.
 LogprobPlan logprob_plan(int N, int V, int K) {
     const int chunks = (V + 7 + kChunk - 1) / kChunk;
     LogprobPlan p;
     int64_t n = 1024 / N < 1 ? 1 : 1024 / N;
-    const int64_t most = (chunks + kWaves - 1) / kWaves;
-    if (n > most) n = most;
+    const int64_t most = chunks / (3 * K / 2 > 32 ? 3 * K / 2 : 32);
+    if (n > most) n = most < 1 ? 1 : most;
     if (n > 64) n = 64;
     const int64_t least = (chunks + kMaxTop * 64 - 1) / (kMaxTop * 64);
     if (n < least) n = least;
