@@ -127,19 +127,47 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs A) {
             sn[u][i] = unit < turned ? sines[W * unit + i] : 0.f;
         }
     }
-    for (int head = part * slots + slot; head < A.q.H + A.k.H; head += A.waves_per_token * slots) {
-        const bool is_k = head >= A.q.H;
-        const wb_heads& x = is_k ? A.k : A.q;
-        const int h = is_k ? head - A.q.H : head;
-        const int64_t from = token * x.row + int64_t(h) * x.head, to = token * x.out_row + int64_t(h) * x.out_head;
-        float a[U][W], b[U][W];
+    // The weights of queries and keys stay in registers, the next head's columns are on their way behind this one's
+    const int heads = A.q.H + A.k.H, step = A.waves_per_token * slots;
+    float wq[2][U][W], wk[2][U][W];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = i ? c1[u] : c0[u];
+#pragma unroll
+            for (int e = 0; e < W; ++e) wq[i][u][e] = wk[i][u][e] = 0.f;
+            if (c < A.D && A.q.weight) Vec<T, W>::load(A.q.weight, c, wq[i][u]);
+            if (c < A.D && A.k.weight) Vec<T, W>::load(A.k.weight, c, wk[i][u]);
+        }
+    float a[U][W], b[U][W], a_next[U][W], b_next[U][W];
+    auto fetch = [&](int head) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < W; ++i) a[u][i] = b[u][i] = 0.f;
-            if (c0[u] < A.D) Vec<T, W>::load(x.x, from + c0[u], a[u]);
-            if (c1[u] < A.D) Vec<T, W>::load(x.x, from + c1[u], b[u]);
+            for (int i = 0; i < W; ++i) a_next[u][i] = b_next[u][i] = 0.f;
+            if (head < heads) {
+                const bool is_k = head >= A.q.H;
+                const void* x = is_k ? A.k.x : A.q.x;
+                const int64_t from = is_k ? token * A.k.row + int64_t(head - A.q.H) * A.k.head : token * A.q.row + int64_t(head) * A.q.head;
+                if (c0[u] < A.D) Vec<T, W>::load(x, from + c0[u], a_next[u]);
+                if (c1[u] < A.D) Vec<T, W>::load(x, from + c1[u], b_next[u]);
+            }
         }
+    };
+    fetch(part * slots + slot);
+    for (int head = part * slots + slot; head < heads; head += step) {
+        const bool is_k = head >= A.q.H;
+        const wb_heads& x = is_k ? A.k : A.q;
+        const int64_t to = token * x.out_row + int64_t(is_k ? head - A.q.H : head) * x.out_head;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                a[u][i] = a_next[u][i];
+                b[u][i] = b_next[u][i];
+            }
+        fetch(head + step);
         if (x.weight) {
             float sum = 0.f;
 #pragma unroll
@@ -178,15 +206,10 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs A) {
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                float w0[W], w1[W];
-#pragma unroll
-                for (int i = 0; i < W; ++i) w0[i] = w1[i] = 0.f;
-                if (c0[u] < A.D) Vec<T, W>::load(x.weight, c0[u], w0);
-                if (c1[u] < A.D) Vec<T, W>::load(x.weight, c1[u], w1);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    a[u][i] = a[u][i] * by * w0[i];
-                    b[u][i] = b[u][i] * by * w1[i];
+                    a[u][i] = a[u][i] * by * (is_k ? wk[0][u][i] : wq[0][u][i]);
+                    b[u][i] = b[u][i] * by * (is_k ? wk[1][u][i] : wq[1][u][i]);
                 }
             }
         }
