@@ -18,41 +18,41 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kPairs = 512;                    // of a head at most (1024 columns)
 
-// Elements of W values, loaded and stored as widely as their alignment (W elements, at most 16 bytes) allows
+// W values as they are stored, loaded and stored as widely as their alignment (W elements, at most 16 bytes) allows
 template <int T, int W>
 struct Vec {
-    static __device__ __forceinline__ void load(const void* p, int64_t at, float (&x)[W]) {
+    static constexpr int N = T == WB_F32 ? W : (W + 1) / 2;
+    uint32_t w[N];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const void* p, int64_t at) {
         if constexpr (T == WB_F32) {
-            const float* s = static_cast<const float*>(p) + at;
-            if constexpr (W == 1) {
-                x[0] = s[0];
-            } else {
+            const uint32_t* s = static_cast<const uint32_t*>(p) + at;
+            if constexpr (W == 1) w[0] = s[0];
+            else
 #pragma unroll
-                for (int i = 0; i < W; i += 4) {
-                    const f32x4 v = *reinterpret_cast<const f32x4*>(s + i);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i + e] = v[e];
-                }
-            }
+                for (int i = 0; i < W; i += 4) *reinterpret_cast<u32x4*>(w + i) = *reinterpret_cast<const u32x4*>(s + i);
         } else {
             const uint16_t* s = static_cast<const uint16_t*>(p) + at;
-            uint32_t w[W > 1 ? W / 2 : 1];
             if constexpr (W == 8) *reinterpret_cast<u32x4*>(w) = *reinterpret_cast<const u32x4*>(s);
             else if constexpr (W == 4) *reinterpret_cast<u32x2*>(w) = *reinterpret_cast<const u32x2*>(s);
             else w[0] = s[0];
-#pragma unroll
-            for (int i = 0; i < W; ++i) x[i] = Elem<T>::get(uint16_t(w[i / 2] >> (16 * (i & 1))));
         }
     }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (T == WB_F32) return __uint_as_float(w[i]);
+        else return Elem<T>::get(uint16_t(w[i / 2] >> (16 * (i & 1))));
+    }
+    template <bool PAST>
     static __device__ __forceinline__ void store(void* p, int64_t at, const float (&x)[W]) {
         if constexpr (T == WB_F32) {
             float* d = static_cast<float*>(p) + at;
-            if constexpr (W == 1) {
-                d[0] = x[0];
-            } else {
+            if constexpr (W == 1) d[0] = x[0];
+            else
 #pragma unroll
-                for (int i = 0; i < W; i += 4) *reinterpret_cast<f32x4*>(d + i) = f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
-            }
+                for (int i = 0; i < W; i += 4) put<PAST>(f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]}, d + i);
         } else {
             uint16_t* d = static_cast<uint16_t*>(p) + at;
             if constexpr (W == 1) {
@@ -62,10 +62,15 @@ struct Vec {
 #pragma unroll
                 for (int i = 0; i < W / 2; ++i)
                     w[i] = uint32_t(Elem<T>::put(x[2 * i])) | uint32_t(Elem<T>::put(x[2 * i + 1])) << 16;
-                if constexpr (W == 8) *reinterpret_cast<u32x4*>(d) = *reinterpret_cast<const u32x4*>(w);
-                else *reinterpret_cast<u32x2*>(d) = *reinterpret_cast<const u32x2*>(w);
+                if constexpr (W == 8) put<PAST>(*reinterpret_cast<const u32x4*>(w), d);
+                else put<PAST>(*reinterpret_cast<const u32x2*>(w), d);
             }
         }
+    }
+    template <bool PAST, typename V>
+    static __device__ __forceinline__ void put(V v, void* d) {
+        if constexpr (PAST) __builtin_nontemporal_store(v, static_cast<V*>(d));
+        else *static_cast<V*>(d) = v;
     }
 };
 
@@ -87,8 +92,8 @@ __device__ __forceinline__ uint32_t slot_reduce(uint32_t v, int lanes) {
     return v;
 }
 
-// U: units (W pairs) of a lane, at `lanes` units' distance
-template <int T, int W, int U>
+// U: units (W pairs) of a lane, at `lanes` units' distance; PAST: outputs are stored past the caches
+template <int T, int W, int U, bool PAST>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs A) {
     __shared__ float table[kWaves][2][kPairs];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -129,30 +134,27 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs A) {
     }
     // The weights of queries and keys stay in registers, the next head's columns are on their way behind this one's
     const int heads = A.q.H + A.k.H, step = A.waves_per_token * slots;
-    float wq[2][U][W], wk[2][U][W];
+    Vec<T, W> wq[2][U], wk[2][U], next[2][U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int c = i ? c1[u] : c0[u];
-#pragma unroll
-            for (int e = 0; e < W; ++e) wq[i][u][e] = wk[i][u][e] = 0.f;
-            if (c < A.D && A.q.weight) Vec<T, W>::load(A.q.weight, c, wq[i][u]);
-            if (c < A.D && A.k.weight) Vec<T, W>::load(A.k.weight, c, wk[i][u]);
+            wq[i][u].clear();
+            wk[i][u].clear();
+            if (c < A.D && A.q.weight) wq[i][u].load(A.q.weight, c);
+            if (c < A.D && A.k.weight) wk[i][u].load(A.k.weight, c);
         }
-    float a[U][W], b[U][W], a_next[U][W], b_next[U][W];
     auto fetch = [&](int head) {
+        const bool is_k = head >= A.q.H;
+        const void* x = is_k ? A.k.x : A.q.x;
+        const int64_t from = is_k ? token * A.k.row + int64_t(head - A.q.H) * A.k.head : token * A.q.row + int64_t(head) * A.q.head;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int i = 0; i < W; ++i) a_next[u][i] = b_next[u][i] = 0.f;
-            if (head < heads) {
-                const bool is_k = head >= A.q.H;
-                const void* x = is_k ? A.k.x : A.q.x;
-                const int64_t from = is_k ? token * A.k.row + int64_t(head - A.q.H) * A.k.head : token * A.q.row + int64_t(head) * A.q.head;
-                if (c0[u] < A.D) Vec<T, W>::load(x, from + c0[u], a_next[u]);
-                if (c1[u] < A.D) Vec<T, W>::load(x, from + c1[u], b_next[u]);
-            }
+            next[0][u].clear();
+            next[1][u].clear();
+            if (head < heads && c0[u] < A.D) next[0][u].load(x, from + c0[u]);
+            if (head < heads && c1[u] < A.D) next[1][u].load(x, from + c1[u]);
         }
     };
     fetch(part * slots + slot);
@@ -160,12 +162,13 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs A) {
         const bool is_k = head >= A.q.H;
         const wb_heads& x = is_k ? A.k : A.q;
         const int64_t to = token * x.out_row + int64_t(is_k ? head - A.q.H : head) * x.out_head;
+        float a[U][W], b[U][W];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < W; ++i) {
-                a[u][i] = a_next[u][i];
-                b[u][i] = b_next[u][i];
+                a[u][i] = next[0][u].get(i);
+                b[u][i] = next[1][u].get(i);
             }
         fetch(head + step);
         if (x.weight) {
@@ -208,8 +211,8 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs A) {
             for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
-                    a[u][i] = a[u][i] * by * (is_k ? wk[0][u][i] : wq[0][u][i]);
-                    b[u][i] = b[u][i] * by * (is_k ? wk[1][u][i] : wq[1][u][i]);
+                    a[u][i] = a[u][i] * by * (is_k ? wk[0][u] : wq[0][u]).get(i);
+                    b[u][i] = b[u][i] * by * (is_k ? wk[1][u] : wq[1][u]).get(i);
                 }
             }
         }
@@ -240,18 +243,20 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const RotateArgs A) {
                     b[u][i] = d[i];
                 }
             }
-            if (c0[u] < A.D) Vec<T, W>::store(x.out, to + c0[u], a[u]);
-            if (c1[u] < A.D) Vec<T, W>::store(x.out, to + c1[u], b[u]);
+            if (c0[u] < A.D) Vec<T, W>::template store<PAST>(x.out, to + c0[u], a[u]);
+            if (c1[u] < A.D) Vec<T, W>::template store<PAST>(x.out, to + c1[u], b[u]);
         }
     }
 }
 
 template <int T>
 hipError_t rotate_t(const RotateArgs& a, int W, int units, unsigned groups, hipStream_t s) {
-    if (W == 8) rotate_kernel<T, 8, 1><<<groups, kThreads, 0, s>>>(a);
-    else if (W == 4) rotate_kernel<T, 4, 1><<<groups, kThreads, 0, s>>>(a);
-    else if (units <= 64) rotate_kernel<T, 1, 1><<<groups, kThreads, 0, s>>>(a);
-    else rotate_kernel<T, 1, 8><<<groups, kThreads, 0, s>>>(a);
+    if (W == 8 && a.past) rotate_kernel<T, 8, 1, true><<<groups, kThreads, 0, s>>>(a);
+    else if (W == 8) rotate_kernel<T, 8, 1, false><<<groups, kThreads, 0, s>>>(a);
+    else if (W == 4 && a.past) rotate_kernel<T, 4, 1, true><<<groups, kThreads, 0, s>>>(a);
+    else if (W == 4) rotate_kernel<T, 4, 1, false><<<groups, kThreads, 0, s>>>(a);
+    else if (units <= 64) rotate_kernel<T, 1, 1, false><<<groups, kThreads, 0, s>>>(a);
+    else rotate_kernel<T, 1, 8, false><<<groups, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
@@ -283,6 +288,9 @@ hipError_t launch_rotate(RotateArgs a, int N, hipStream_t s) {
     const int slots = 64 / a.lanes, rounds = (a.q.H + a.k.H + slots - 1) / slots;
     int64_t wanted = (8192 + int64_t(N) - 1) / N;
     a.waves_per_token = int(wanted < rounds ? wanted : rounds);
+    // Outputs that the 256 MB last-level cache could not hold are stored past the caches (32773 tokens of 40 heads of 128,
+    // 336 MB: 146 us against 154); what fits is left there for the calls that read it.
+    a.past = int64_t(N) * (a.q.H + a.k.H) * a.D * (a.dtype == WB_F32 ? 4 : 2) > int64_t(256) << 20;
     const int64_t most = kLaunchItems / (64 * int64_t(a.waves_per_token));      // tokens of a launch
     for (int64_t first = 0; first < N; first += most) {
         a.first = first;

@@ -116,6 +116,7 @@ struct RotateArgs {
     int dtype = 0, D = 0, rot = 0;
     bool wide = false;            // 64-bit positions
     bool interleaved = false;
+    bool past = false;            // outputs past the caches
     int lanes = 4;                // of a head
     int waves_per_token = 1;
     int64_t first = 0, last = 0;  // tokens of the launch
