@@ -136,11 +136,12 @@ struct LogprobArgs {
     uint64_t tag = 0;             // of this call, as for AttendArgs
     float scale = 1.f;
     int dtype = 0, V = 0, K = 0, segments = 1;
+    int chunk = 1;                // vectors of a lane in a chunk
     bool wide = false;            // 64-bit tokens
     int64_t first = 0;            // row of the launch
 };
 struct LogprobPlan {
-    int segments;
+    int segments, chunk;
     size_t part_bytes, arrivals_bytes;
 };
 LogprobPlan logprob_plan(int N, int V, int K);
