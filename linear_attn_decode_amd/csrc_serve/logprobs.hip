@@ -19,8 +19,9 @@ namespace wb {
 namespace {
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kMaxTop = 64;
+constexpr int kMaxTop = 64, kMaxGroups = 512;
 constexpr int kMaxKeys = 4096;                    // in LDS
+constexpr int kOrdered = 128;                     // keys that are ordered by comparing all pairs
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Order of values as whole numbers: larger ones first, -0 as 0, NaN as -infinity
@@ -103,57 +104,134 @@ struct Sums {
         s += q.s;
         t += q.t;
     }
+    __device__ __forceinline__ void over_lanes() {
+        float top = ref;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        move(top);
+        s = __uint_as_float(lanes_reduce<OpAdd, 64>(__float_as_uint(s)));
+        t = __uint_as_float(lanes_reduce<OpAdd, 64>(__float_as_uint(t)));
+    }
 };
 
-// The first K of n keys in order, out[0 .. K) (0 where there are fewer), by all threads of the
-// workgroup; `keys` has room for the next power of two past n and is left in any order.
-__device__ __forceinline__ void first_keys(uint64_t* keys, int n, int K, uint64_t* out) {
-    const int tid = threadIdx.x;
-    if (n <= kThreads) {
-        // each key's place is the number of larger ones
-        for (int i = tid; i < K; i += kThreads)
-            if (i >= n) out[i] = 0;
-        if (tid < n) {
-            const uint64_t mine = keys[tid];
-            int place = 0;
-            const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(keys);
-#pragma unroll 8
-            for (int j = 0; j < n / 2; ++j) {
-                const ulonglong2 k = pairs[j];
-                place += (k.x > mine) + (k.y > mine);
-            }
-            if (n & 1) place += keys[n - 1] > mine;
-            if (place < K) out[place] = mine;
+// The places of the K largest of n <= 64 M values, equal ones by their place, by one wavefront: the K-th largest bit by
+// bit, with ballots. Returns a bound that they reach and no other value passes, 0 if there are no more than K.
+template <int M>
+__device__ __forceinline__ uint32_t largest_of(const uint32_t* values, int n, int K, int* places) {
+    const int lane = threadIdx.x & 63;
+    uint32_t v[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) v[i] = 64 * i + lane < n ? values[64 * i + lane] : 0;       // (0 is below every value's order)
+    uint32_t least = 0;
+    int reach = 0;
+    for (uint32_t bit = 0x80000000u; bit && reach != K; bit >>= 1) {
+        int count = 0;
+#pragma unroll
+        for (int i = 0; i < M; ++i) count += __popcll(__ballot(v[i] >= (least | bit)));
+        if (count >= K) {
+            least |= bit;
+            reach = count;
         }
-        __syncthreads();
-        return;
     }
-    int size = 2 * kThreads;
-    while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kThreads) keys[i] = 0;
-    __syncthreads();
-    for (int run = 2; run <= size; run *= 2)
-        for (int step = run / 2; step; step /= 2) {
-            for (int i = tid; i < size / 2; i += kThreads) {
-                const int lo = 2 * i - (i & (step - 1)), hi = lo + step;
-                const uint64_t a = keys[lo], b = keys[hi];
-                if ((a < b) == ((lo & run) == 0)) {
-                    keys[lo] = b;
-                    keys[hi] = a;
-                }
-            }
-            __syncthreads();
-        }
-    for (int i = tid; i < K; i += kThreads) out[i] = keys[i];
-    __syncthreads();
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < M; ++i) above += __popcll(__ballot(v[i] > least));
+    int equal = K - above, at = 0;             // of those at the bound, the first
+    const uint64_t before = (uint64_t(1) << lane) - 1;
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        const uint64_t same = __ballot(v[i] == least);
+        const bool take = v[i] > least || (v[i] == least && __popcll(same & before) < equal);
+        const uint64_t taken = __ballot(take);
+        if (take) places[at + __popcll(taken & before)] = 64 * i + lane;
+        at += __popcll(taken);
+        equal -= min(equal, int(__popcll(same)));
+    }
+    return least;
+}
+__device__ __forceinline__ uint32_t largest_values(const uint32_t* values, int n, int K, int* places) {
+    if (n <= K) {
+        if (int(threadIdx.x & 63) < n) places[threadIdx.x & 63] = threadIdx.x & 63;          // (K <= 64)
+        return 0;
+    }
+    if (n <= 64) return largest_of<1>(values, n, K, places);
+    if (n <= 128) return largest_of<2>(values, n, K, places);
+    if (n <= 256) return largest_of<4>(values, n, K, places);
+    return largest_of<8>(values, n, K, places);
 }
 
-// J: vectors of a lane in a chunk, which is what a wavefront takes at a time
-template <int T, bool TOP, int J>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A) {
+// The first K of n distinct keys in order, out[0 .. K) (0 where there are fewer), by all threads of the workgroup, which
+// have all stored their keys. `spare` has room for kOrdered keys, `bins` for 256 counts.
+__device__ __forceinline__ void order_keys(const uint64_t* keys, int n, int K, uint64_t* out) {
+    // each key's place is the number of larger ones
+    const int tid = threadIdx.x;
+    for (int i = n + tid; i < K; i += kThreads) out[i] = 0;
+    if (tid < n) {
+        const uint64_t mine = keys[tid];
+        int place = 0;
+        const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(keys);
+#pragma unroll 8
+        for (int j = 0; j < n / 2; ++j) {
+            const ulonglong2 k = pairs[j];
+            place += (k.x > mine) + (k.y > mine);
+        }
+        if (n & 1) place += keys[n - 1] > mine;
+        if (place < K) out[place] = mine;
+    }
+    __syncthreads();
+}
+__device__ __forceinline__ void first_keys(const uint64_t* keys, int n, int K, uint64_t* out, uint64_t* spare, int* bins) {
+    const int tid = threadIdx.x;
+    if (n <= kOrdered) return order_keys(keys, n, K, out);
+    // Digit by digit, from the highest, the K-th key's; until those at or above its digits are few enough to be ordered
+    __shared__ int state[3];                     // its digit; keys above the digits so far; keys taken
+    uint64_t prefix = 0;
+    int above = 0, shift = 64, at_or_above;
+    do {
+        shift -= 8;
+        __syncthreads();
+        if (tid < 256) bins[tid] = 0;
+        if (tid == 0) state[2] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads)
+            if (shift == 56 || keys[i] >> (shift + 8) == prefix) atomicAdd(&bins[keys[i] >> shift & 255], 1);
+        __syncthreads();
+        if (tid < 64) {
+            // lane l holds digits 255 - 4 l ..252 - 4 l
+            int c[4], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum += c[i] = bins[255 - 4 * tid - i];
+            int before = int(wave_scan(sum)) - sum + above;
+            if (before < K && before + sum >= K) {
+                int i = 0;
+                while (before + c[i] < K) before += c[i++];
+                state[0] = 255 - 4 * tid - i;
+                state[1] = before;
+            }
+        }
+        __syncthreads();
+        above = state[1];
+        prefix = prefix << 8 | uint64_t(state[0]);
+        at_or_above = above + bins[state[0]];
+    } while (at_or_above > kOrdered);            // (keys differ: behind the last digit those are K)
+    for (int i = tid; i < n; i += kThreads)
+        if (keys[i] >> shift >= prefix) spare[atomicAdd(&state[2], 1)] = keys[i];
+    __syncthreads();
+    order_keys(spare, at_or_above, K, out);
+}
+
+// A wavefront takes chunks of 64 J vectors at a time. TOP: vectors of a group, whose maximum is kept: 8 (64 columns), 64 J
+// (a chunk), or 0: no alternatives are wanted.
+template <int T, int TOP, int J>
+__global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs A) {
     constexpr int kKeys = TOP ? kMaxKeys : 2;
     __shared__ __attribute__((aligned(16))) uint64_t keys[kKeys];
     __shared__ uint64_t first[TOP ? kMaxTop : 1];
+    __shared__ __attribute__((aligned(16))) uint64_t spare[TOP ? kOrdered : 2];
+    __shared__ uint32_t maxima[TOP ? kMaxGroups : 1];
+    __shared__ int group_at[TOP ? kMaxTop : 1];
+    __shared__ uint32_t bound;
+    __shared__ int bins[TOP ? 256 : 1];
     __shared__ float sums[kWaves][3];
     __shared__ int count, is_last;
 
@@ -217,18 +295,12 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A)
                 }
         }
         if constexpr (TOP) {
-            const uint32_t best = lanes_reduce<OpMax, 64>(order_of(top));
-            if (lane == 0) keys[k - c0] = uint64_t(best) << 32 | (0xFFFFFFFFu - uint32_t(k));
+            constexpr int kLanes = TOP / J, kGroups = 64 / kLanes;
+            const uint32_t best = lanes_reduce<OpMax, kLanes>(order_of(top)), group = uint32_t(k) * kGroups + lane / kLanes;
+            if (lane % kLanes == 0) maxima[group - c0 * kGroups] = best;
         }
     }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        Sums o;
-        o.ref = __shfl_xor(own.ref, d);
-        o.s = __shfl_xor(own.s, d);
-        o.t = __shfl_xor(own.t, d);
-        own.add(o);
-    }
+    own.over_lanes();
     if (lane == 0) {
         sums[wave][0] = own.ref;
         sums[wave][1] = own.s;
@@ -241,35 +313,50 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A)
     for (int w = 1; w < kWaves; ++w) own.add(Sums{sums[w][0], sums[w][1], sums[w][2]});
 
     if constexpr (TOP) {
-        const int K = A.K, n = c1 - c0, held = min(K, n);
-        first_keys(keys, n, K, first);
-        const uint32_t least = n >= K ? uint32_t(first[K - 1] >> 32) : 0;      // no column below it is taken
-        // columns of those chunks (keys past the room are counted, not stored)
-        for (int i = wave; i < held * J; i += kWaves) {
-            const int v = 64 * (J * int(at_of(first[i / J])) + i % J) + lane;
-            float y[8];
-            x.get(v, y);
-            if (v < vectors && order_of(largest(y)) >= least)
+        const int K = A.K, n = (c1 - c0) * (64 * J / TOP), held = min(K, n);
+        if (wave == 0) {
+            const uint32_t least = largest_values(maxima, n, K, group_at);
+            if (lane == 0) bound = least;
+        }
+        __syncthreads();
+        const uint32_t least = bound;                                          // no column below it is taken
+        const int group0 = c0 * (64 * J / TOP);
+        // Columns of those groups, two vectors of a lane on their way at a time (keys past the room are counted, not
+        // stored)
+        for (int from = 0; from < held * TOP; from += 2 * kThreads) {
+            float y[2][8];
+            int at[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int64_t at = int64_t(v) * 8 - x.off + e;
-                    if (order_of(y[e]) >= least && at >= 0 && at < A.V) {
-                        const int place = atomicAdd(&count, 1);
-                        if (place < kKeys) keys[place] = key_of(y[e], uint32_t(at));
-                    }
+            for (int u = 0; u < 2; ++u) {
+                const int i = from + u * kThreads + tid;
+                at[u] = A.V;
+                if (i < held * TOP) {
+                    const int v = TOP * (group0 + group_at[i / TOP]) + i % TOP;
+                    x.get(v, y[u]);
+                    at[u] = v * 8 - x.off;
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                if (at[u] < A.V && order_of(largest(y[u])) >= least)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (order_of(y[u][e]) >= least && at[u] + e >= 0 && at[u] + e < A.V) {
+                            const int place = atomicAdd(&count, 1);
+                            if (place < kKeys) keys[place] = key_of(y[u][e], uint32_t(at[u] + e));
+                        }
         }
         __syncthreads();
         const int found = count;
         if (found <= kKeys) {
-            first_keys(keys, found, K, first);
+            first_keys(keys, found, K, first, spare, bins);
         } else {
             // vectors first
             __syncthreads();
             if (tid == 0) count = 0;
             __syncthreads();
-            for (int i = wave; i < held * J; i += kWaves) {
-                const int v = 64 * (J * int(at_of(first[i / J])) + i % J) + lane;
+            for (int i = tid; i < held * TOP; i += kThreads) {
+                const int v = TOP * (group0 + group_at[i / TOP]) + i % TOP;
                 float y[8];
                 x.get(v, y);
                 const uint32_t o = order_of(largest(y));
@@ -277,7 +364,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A)
             }
             __syncthreads();
             const int n_vectors = count;
-            first_keys(keys, n_vectors, K, first);
+            first_keys(keys, n_vectors, K, first, spare, bins);
             if (tid == 0) count = 0;
             uint64_t mine = 0;
             if (tid < 8 * min(K, n_vectors)) {
@@ -287,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A)
             __syncthreads();
             if (mine) keys[atomicAdd(&count, 1)] = mine;
             __syncthreads();
-            first_keys(keys, count, K, first);
+            first_keys(keys, count, K, first, spare, bins);
         }
     }
 
@@ -309,22 +396,29 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A)
         if (!is_last) return;
         part = A.parts + local * parts * words;
         Sums all;
-        for (int p = 0; p < parts; ++p) {
-            const uint64_t ms = get_word(part + p * words), t = get_word(part + p * words + 1);
-            Sums o;
-            o.ref = __uint_as_float(uint32_t(ms));
-            o.s = __uint_as_float(uint32_t(ms >> 32));
-            o.t = __uint_as_float(uint32_t(t));
-            all.add(o);
+        if (lane < parts) {                       // (64 parts at most)
+            const uint64_t ms = get_word(part + lane * words), tt = get_word(part + lane * words + 1);
+            all = Sums{__uint_as_float(uint32_t(ms)), __uint_as_float(uint32_t(ms >> 32)), __uint_as_float(uint32_t(tt))};
         }
+        all.over_lanes();
         own = all;
         if constexpr (TOP) {
             for (int i = tid; i < parts * A.K; i += kThreads) {
                 const int p = i / A.K;
                 keys[i] = get_word(part + p * words + 2 + (i - p * A.K));
+                if (i < kMaxGroups) maxima[i] = uint32_t(keys[i] >> 32);
             }
             __syncthreads();
-            first_keys(keys, parts * A.K, A.K, first);
+            if (parts * A.K > kMaxGroups) {
+                first_keys(keys, parts * A.K, A.K, first, spare, bins);
+            } else {
+                // (equal values are in the order of their columns here)
+                if (wave == 0) largest_values(maxima, parts * A.K, A.K, group_at);
+                __syncthreads();
+                if (tid < A.K) spare[tid] = keys[group_at[tid]];
+                __syncthreads();
+                order_keys(spare, A.K, A.K, first);
+            }
         }
     }
 
@@ -348,29 +442,34 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const LogprobArgs A)
 
 template <int T>
 hipError_t logprobs_t(const LogprobArgs& a, unsigned groups, hipStream_t s) {
-    if (a.K && a.chunk == 1) logprobs_kernel<T, true, 1><<<groups, kThreads, 0, s>>>(a);
-    else if (a.K) logprobs_kernel<T, true, 2><<<groups, kThreads, 0, s>>>(a);
-    else if (a.chunk == 1) logprobs_kernel<T, false, 1><<<groups, kThreads, 0, s>>>(a);
-    else logprobs_kernel<T, false, 2><<<groups, kThreads, 0, s>>>(a);
+    if (!a.K && a.chunk == 1) logprobs_kernel<T, 0, 1><<<groups, kThreads, 0, s>>>(a);
+    else if (!a.K) logprobs_kernel<T, 0, 2><<<groups, kThreads, 0, s>>>(a);
+    else if (a.group == 8) logprobs_kernel<T, 8, 1><<<groups, kThreads, 0, s>>>(a);
+    else if (a.group == 64) logprobs_kernel<T, 64, 1><<<groups, kThreads, 0, s>>>(a);
+    else logprobs_kernel<T, 128, 2><<<groups, kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Segments of a row: enough for 1024 workgroups (4 a compute unit), of 32 chunks at least, and of 3 K / 2 where
-// alternatives are wanted (with K chunks or fewer in a segment nothing could be left out); joined parts' keys fit LDS,
-// and so do a segment's chunks. Chunks of 512 columns where rows are split, so that segments can be short; of 1024
-// where a workgroup has a whole row, for half the maxima.
+// Segments of a row: enough for 1024 workgroups (4 a compute unit), of 16 chunks of 512 columns at least, and so that their
+// alternatives can be ordered as one list. A segment's groups, whose maxima are kept: the largest of which there are
+// twice as many as alternatives wanted (or hardly anything could be left out), up to 512, and whose vectors, of the
+// first K groups, fit LDS.
 LogprobPlan logprob_plan(int N, int V, int K) {
     const int chunks = (V + 7 + 511) / 512;
     LogprobPlan p;
     int64_t n = 1024 / N < 1 ? 1 : 1024 / N;
-    const int64_t most = chunks / (3 * K / 2 > 32 ? 3 * K / 2 : 32);
-    if (n > most) n = most < 1 ? 1 : most;
+    if (n > chunks / 16) n = chunks / 16 < 1 ? 1 : chunks / 16;
     if (n > 64) n = 64;
-    const int64_t least = (chunks + kMaxKeys - 1) / kMaxKeys;
+    if (K && n > kMaxGroups / K) n = kMaxGroups / K;
+    const bool wide = K * 128 <= kMaxKeys;
+    const int64_t room = wide ? 2 * kMaxGroups : kMaxGroups, least = (chunks + room - 1) / room;
     if (n < least) n = least;
-    p.chunk = n > 1 || chunks < 128 ? 1 : 2;
+    const int64_t c = (chunks + n - 1) / n;
+    p.group = wide && c / 2 >= 2 * K ? 128 : c >= 2 * K || c > kMaxGroups / 8 ? 64 : 8;
+    if (p.group == 64 && c > kMaxGroups) p.group = 128;
+    p.chunk = K ? (p.group == 128 ? 2 : 1) : c >= 256 ? 2 : 1;
     p.segments = int(n);
     p.part_bytes = n > 1 ? size_t(N) * n * (2 + K) * 8 : 0;
     p.arrivals_bytes = n > 1 ? size_t(N) * 8 : 0;

@@ -137,11 +137,12 @@ struct LogprobArgs {
     float scale = 1.f;
     int dtype = 0, V = 0, K = 0, segments = 1;
     int chunk = 1;                // vectors of a lane in a chunk
+    int group = 8;                // vectors of a group whose maximum is kept
     bool wide = false;            // 64-bit tokens
     int64_t first = 0;            // row of the launch
 };
 struct LogprobPlan {
-    int segments, chunk;
+    int segments, chunk, group;
     size_t part_bytes, arrivals_bytes;
 };
 LogprobPlan logprob_plan(int N, int V, int K);

@@ -395,6 +395,7 @@ int token_logprobs(const void* logits, int64_t row, int dtype, int N, int V, con
     a.K = K;
     a.segments = p.segments;
     a.chunk = p.chunk;
+    a.group = p.group;
     a.wide = tokens64 != 0;
     return hip_status(wb::launch_logprobs(a, N, static_cast<hipStream_t>(stream)));
 }

@@ -86,7 +86,7 @@ def test_rows_and_segments(N, V):
 
 
 @pytest.mark.parametrize("N", [2, 2000])
-@pytest.mark.parametrize("V", [3000, 40000])
+@pytest.mark.parametrize("V", [700, 3000, 40000, 140000])
 def test_orders_that_fill_every_stage(N, V):
     """Constant rows, rising and falling ones, a few values many times, all but some columns at -infinity:
     equal logits by their column, and many candidates."""
@@ -96,7 +96,7 @@ def test_orders_that_fill_every_stage(N, V):
              torch.full((V,), torch.finfo(torch.float32).min).index_fill(0, torch.tensor([V - 1]), 0.0)]
     x = torch.stack([kinds[r % len(kinds)] for r in range(N)]).cuda()
     tokens = [(77, 0, V - 1, 5)[r % 4] for r in range(N)]
-    for K in (64, 3):
+    for K in (64, 32, 3):
         run(x, tokens, K, rows=range(min(N, 10)))
 
 
