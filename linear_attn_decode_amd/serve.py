@@ -383,16 +383,14 @@ def kv_attend_chunk(q, k_cache, v_cache, table, lens, starts, o, scale=None, win
           window if window < _MAX else 0, o.data_ptr(), lsep, held.data_ptr() if n else None, n, _stream_of(dev, stream))
 
 
-def _rotated(x, out, weight, name, kind, N, D, dev):
-    """A wb_heads of x [N, H, D]: strided tokens and heads, contiguous columns."""
-    out = x if out is None else out
-    shape = x.shape
-    if not (len(shape) == 3 and x.dtype is kind and out.dtype is kind and shape[0] == N and shape[2] == D and out.shape == shape
-            and x.get_device() == out.get_device() == dev and x.stride(2) == out.stride(2) == 1 and shape[1] <= _MAX):
-        bad = out if x.dim() == 3 and x.dtype is kind and x.shape == (N, x.shape[1], D) and x.get_device() == dev and x.stride(2) == 1 else x
-        _refuse(bad, name if bad is x else name + "_out", f"{kind} [{N}, {shape[1] if len(shape) == 3 else 'heads'}, {D}] with contiguous heads", dev)
-    w = 0 if weight is None else _ptr(weight, name + "_weight", kind, (D,), dev)
-    return _heads.pack(x.data_ptr(), out.data_ptr(), w, x.stride(0), x.stride(1), out.stride(0), out.stride(1), shape[1], 0)
+def _check_heads(x, out, weight, name, kind, N, D, dev):
+    """What is wrong with heads x [N, H, D], their output or their weight."""
+    for t, what in ((x, name), (out, name + "_out")):
+        if not (t.dim() == 3 and t.dtype is kind and t.shape[0] == N and t.shape[2] == D and t.shape == x.shape
+                and t.get_device() == dev and t.stride(2) == 1 and t.shape[1] <= _MAX):
+            _refuse(t, what, f"{kind} [{N}, heads, {D}] with contiguous heads", dev)
+    if weight is not None:
+        _ptr(weight, name + "_weight", kind, (D,), dev)
 
 
 def qk_rotate(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6, interleaved: bool = False,
@@ -411,20 +409,43 @@ def qk_rotate(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float =
     code = _codes.get(kind, E4M3)
     if code == E4M3 or q.dim() != 3:
         raise ValueError(f"q: expected bfloat16, float16 or float32 [N, Hq, D], got {kind} {tuple(q.shape)}")
-    N, _, D = q.shape
-    if N > _MAX or D > _MAX:
-        raise ValueError(f"q: {tuple(q.shape)} is too large")
+    shape = N, Hq, D = q.shape
+    if N > _MAX or D > _MAX or Hq > _MAX:
+        raise ValueError(f"q: {tuple(shape)} is too large")
     if freqs.dim() != 1:
         raise ValueError(f"freqs: expected 1 dimension, got {freqs.dim()}")
     half = freqs.shape[0]
     if 2 * half > D:
         raise ValueError(f"freqs: {half} pairs are more than the {D} columns of a head")
     wide = positions.dtype is _torch.int64
-    f = _ptr(freqs, "freqs", _torch.float64, (half,), dev)
-    p = _ptr(positions, "positions", _torch.int64 if wide else _torch.int32, (N,), dev)
-    qd = _rotated(q, q_out, q_weight, "q", kind, N, D, dev)
-    kd = None if k is None else _rotated(k, k_out, k_weight, "k", kind, N, D, dev)
-    _call("qk_rotate", dev, qd, kd, code, N, D, p, wide, f, 2 * half, interleaved, magnitude, eps, _stream_of(dev, stream))
+    if not (freqs.dtype is _torch.float64 and (wide or positions.dtype is _torch.int32) and positions.shape == (N,)
+            and freqs.get_device() == positions.get_device() == dev and freqs.is_contiguous() and positions.is_contiguous()):
+        _ptr(freqs, "freqs", _torch.float64, (half,), dev)
+        _ptr(positions, "positions", _torch.int64 if wide else _torch.int32, (N,), dev)
+    o = q if q_out is None else q_out
+    row, head, col = q.stride()
+    o_row, o_head, o_col = o.stride() if o.dim() == 3 else (0, 0, 0)
+    w = 0 if q_weight is None else q_weight.data_ptr()
+    if not (o.dtype is kind and o.shape == shape and o.get_device() == dev and col == o_col == 1
+            and (w == 0 or (q_weight.dtype is kind and q_weight.shape == (D,) and q_weight.get_device() == dev
+                            and q_weight.is_contiguous()))):
+        _check_heads(q, o, q_weight, "q", kind, N, D, dev)
+    qd = _heads.pack(q.data_ptr(), o.data_ptr(), w, row, head, o_row, o_head, Hq, 0)
+    kd = None
+    if k is not None:
+        o = k if k_out is None else k_out
+        shape = k.shape
+        row, head, col = k.stride() if k.dim() == 3 else (0, 0, 0)
+        o_row, o_head, o_col = o.stride() if o.dim() == 3 else (0, 0, 0)
+        w = 0 if k_weight is None else k_weight.data_ptr()
+        if not (k.dtype is kind and o.dtype is kind and o.shape == shape and col == o_col == 1 and shape[0] == N and shape[2] == D
+                and shape[1] <= _MAX and k.get_device() == o.get_device() == dev
+                and (w == 0 or (k_weight.dtype is kind and k_weight.shape == (D,) and k_weight.get_device() == dev
+                                and k_weight.is_contiguous()))):
+            _check_heads(k, o, k_weight, "k", kind, N, D, dev)
+        kd = _heads.pack(k.data_ptr(), o.data_ptr(), w, row, head, o_row, o_head, shape[1], 0)
+    _call("qk_rotate", dev, qd, kd, code, N, D, positions.data_ptr(), wide, freqs.data_ptr(), 2 * half, interleaved, magnitude,
+          eps, _stream_of(dev, stream))
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, context: int = 0, slow: float = 1.0,
@@ -475,15 +496,26 @@ def token_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logp
     f32 = _torch.float32
     p, row = _rows(logits, "logits", kind, shape, dev, V)
     wide = tokens.dtype is _torch.int64
-    t = _ptr(tokens, "tokens", _torch.int64 if wide else _torch.int32, (N,), dev)
-    lp = _ptr(logprob, "logprob", f32, (N,), dev)
-    e = None if entropy is None else _ptr(entropy, "entropy", f32, (N,), dev)
-    ids = _ptr(top_ids, "top_ids", _torch.int32, (N, K), dev) if K else None
-    tops = _ptr(top_logprobs, "top_logprobs", f32, (N, K), dev) if K else None
+    rows = (N,)
+    if not (logprob.dtype is f32 and (wide or tokens.dtype is _torch.int32) and logprob.shape == rows and tokens.shape == rows
+            and logprob.get_device() == tokens.get_device() == dev and logprob.is_contiguous() and tokens.is_contiguous()
+            and (entropy is None or (entropy.dtype is f32 and entropy.shape == rows and entropy.get_device() == dev
+                                     and entropy.is_contiguous()))
+            and (not K or (top_ids.dtype is _torch.int32 and top_logprobs.dtype is f32 and top_ids.shape == top_logprobs.shape
+                           == (N, K) and top_ids.get_device() == top_logprobs.get_device() == dev
+                           and top_ids.is_contiguous() and top_logprobs.is_contiguous()))):
+        _ptr(tokens, "tokens", _torch.int64 if wide else _torch.int32, rows, dev)
+        _ptr(logprob, "logprob", f32, rows, dev)
+        if entropy is not None:
+            _ptr(entropy, "entropy", f32, rows, dev)
+        if K:
+            _ptr(top_ids, "top_ids", _torch.int32, (N, K), dev)
+            _ptr(top_logprobs, "top_logprobs", f32, (N, K), dev)
     n = _logprob_work(N, V, K)
     held = _workspace(n, _torch.uint8, dev, stream) if n else None
-    _call("token_logprobs", dev, p, row, code, N, V, t, wide, scale, lp, e, K, ids, tops, held.data_ptr() if n else None, n,
-          _stream_of(dev, stream))
+    _call("token_logprobs", dev, p, row, code, N, V, tokens.data_ptr(), wide, scale, logprob.data_ptr(),
+          None if entropy is None else entropy.data_ptr(), K, top_ids.data_ptr() if K else None,
+          top_logprobs.data_ptr() if K else None, held.data_ptr() if n else None, n, _stream_of(dev, stream))
 
 
 def norm_quant(x, weight, codes, scales, eps: float = 1e-6, group: int = 0, residual=None, residual_out=None,
