@@ -45,19 +45,36 @@ struct Work {
     int64_t slot, slot0;
 };
 
-// The work of number `at`, among all parts, or among those of split blocks only. False: there
-// are not so many. Every wavefront finds it for itself: lane l sums over requests [l per,
-// (l + 1) per), a scan finds the lane, a second one the request among its.
+// The work of number `at`, among all parts, or among those of split blocks only. False: there are not so many. Every
+// wavefront finds it for itself: lane l sums over requests [l per, (l + 1) per), a scan finds the lane, a second one the
+// request among its. Up to 64 requests are taken by their spans, long ones first, so that what is started last is short
+// (16 ragged requests to 2500 tokens, 8-bit: 111 us, 145 in the order they come).
 template <bool SPLIT_ONLY>
 __device__ __forceinline__ bool find_work(const ChunkArgs& A, int64_t at, Work& w) {
     const int lane = threadIdx.x & 63, per = (A.R + 63) / 64;
     const int per_block = A.c.H * A.head_blocks;
+    Request mine_q{};
+    int id = lane;
     int64_t cost = 0;
-    for (int i = 0; i < per; ++i) {
-        const int r = lane * per + i;
-        if (r < A.R) {
-            const Request q = request_of(A, r);
-            cost += int64_t(q.blocks) * q.span;
+    if (per == 1) {
+        if (lane < A.R) mine_q = request_of(A, lane);
+        cost = int64_t(mine_q.blocks) * mine_q.span;
+        int place = 0;
+        for (int j = 0; j < A.R; ++j) {
+            const int other = __builtin_amdgcn_readlane(mine_q.span, j);
+            place += other > mine_q.span || (other == mine_q.span && j < lane);
+        }
+        if (lane >= A.R) place = lane;
+        id = __builtin_amdgcn_ds_permute(4 * place, lane);
+        mine_q.blocks = __builtin_amdgcn_ds_permute(4 * place, mine_q.blocks);
+        mine_q.span = __builtin_amdgcn_ds_permute(4 * place, mine_q.span);
+    } else {
+        for (int i = 0; i < per; ++i) {
+            const int r = lane * per + i;
+            if (r < A.R) {
+                const Request q = request_of(A, r);
+                cost += int64_t(q.blocks) * q.span;
+            }
         }
     }
     cost = lane64(wave_scan(cost), 63) * per_block;
@@ -66,19 +83,21 @@ __device__ __forceinline__ bool find_work(const ChunkArgs& A, int64_t at, Work& 
     auto parts_in = [&](const Request& q) { return (q.span + most - 1) / most; };
     // (parts in the lower half, those of split blocks in the upper one)
     auto count = [&](const Request& q) {
-        const int parts = parts_in(q);
+        const int parts = q.blocks ? parts_in(q) : 1;
         const int64_t n = int64_t(q.blocks) * per_block * parts;
         return n | (parts > 1 ? n : 0) << 32;
     };
     auto key = [&](int64_t v) { return SPLIT_ONLY ? v >> 32 : v & 0xFFFFFFFF; };
     int64_t mine = 0;
-    for (int i = 0; i < per; ++i)
-        if (lane * per + i < A.R) mine += count(request_of(A, lane * per + i));
+    if (per == 1) mine = count(mine_q);
+    else
+        for (int i = 0; i < per; ++i)
+            if (lane * per + i < A.R) mine += count(request_of(A, lane * per + i));
     const int64_t upto = wave_scan(mine);
     if (key(lane64(upto, 63)) <= at) return false;
     const int who = __ffsll((unsigned long long)__ballot(key(upto) > at)) - 1;
     int64_t before = lane64(upto, who) - lane64(mine, who);
-    w.r = min((who + 1) * per, A.R) - 1;
+    w.r = per == 1 ? __builtin_amdgcn_readlane(id, who) : min((who + 1) * per, A.R) - 1;
     for (int base = who * per; per > 1 && base < (who + 1) * per; base += 64) {
         const int r = base + lane;
         const int64_t n = r < (who + 1) * per && r < A.R ? count(request_of(A, r)) : 0;
@@ -92,7 +111,7 @@ __device__ __forceinline__ bool find_work(const ChunkArgs& A, int64_t at, Work& 
         }
         before = lane64(sum, 63);
     }
-    w.r = __builtin_amdgcn_readfirstlane(w.r);
+    w.r = __builtin_amdgcn_readfirstlane(min(w.r, A.R - 1));
     w.q = request_of(A, w.r);
     w.q.first = __builtin_amdgcn_readfirstlane(w.q.first);
     w.q.m = __builtin_amdgcn_readfirstlane(w.q.m);
