@@ -45,72 +45,62 @@ struct Work {
     int64_t slot, slot0;
 };
 
+// A part has at most this many key tiles: all tiles are cut into about A.target parts of at least A.part_tiles.
+// (tiles: of all blocks of one head block)
+__device__ __forceinline__ int part_limit(const ChunkArgs& A, int64_t tiles) {
+    const int64_t all = tiles * (A.c.H * A.head_blocks);
+    const int64_t most = max(int64_t(A.part_tiles), quotient64(all + A.target - 1, int64_t(A.target)));
+    return int(min(most, int64_t(1) << 30));
+}
+// Parts of a request's blocks (lower half), and of those that are split (upper half)
+__device__ __forceinline__ int64_t count_parts(const ChunkArgs& A, int blocks, int span, int most) {
+    const int parts = blocks ? (span + most - 1) / most : 1;
+    const int64_t n = int64_t(blocks) * (A.c.H * A.head_blocks) * parts;
+    return n | (parts > 1 ? n : 0) << 32;
+}
+
 // The work of number `at`, among all parts, or among those of split blocks only. False: there are not so many. Every
-// wavefront finds it for itself: lane l sums over requests [l per, (l + 1) per), a scan finds the lane, a second one the
-// request among its. Up to 64 requests are taken by their spans, long ones first, so that what is started last is short
-// (16 ragged requests to 2500 tokens, 8-bit: 111 us, 145 in the order they come).
+// wavefront finds it for itself. Up to 64 requests are a lane's each, taken by their spans, long ones first, so that
+// what is started last is short (16 ragged requests to 2500 tokens, 8-bit: 111 us, 145 in the order they come). Of
+// more, a launch before this one has summed the parts (count_requests_kernel), and the sums are searched, 64 places a step.
 template <bool SPLIT_ONLY>
 __device__ __forceinline__ bool find_work(const ChunkArgs& A, int64_t at, Work& w) {
-    const int lane = threadIdx.x & 63, per = (A.R + 63) / 64;
+    const int lane = threadIdx.x & 63;
     const int per_block = A.c.H * A.head_blocks;
-    Request mine_q{};
-    int id = lane;
-    int64_t cost = 0;
-    if (per == 1) {
-        if (lane < A.R) mine_q = request_of(A, lane);
-        cost = int64_t(mine_q.blocks) * mine_q.span;
+    auto key = [&](int64_t v) { return SPLIT_ONLY ? v >> 32 : v & 0xFFFFFFFF; };
+    int64_t before;
+    int most;
+    if (A.R <= 64) {
+        Request q{};
+        if (lane < A.R) q = request_of(A, lane);
+        most = part_limit(A, lane64(wave_scan(int64_t(q.blocks) * q.span), 63));
         int place = 0;
         for (int j = 0; j < A.R; ++j) {
-            const int other = __builtin_amdgcn_readlane(mine_q.span, j);
-            place += other > mine_q.span || (other == mine_q.span && j < lane);
+            const int other = __builtin_amdgcn_readlane(q.span, j);
+            place += other > q.span || (other == q.span && j < lane);
         }
         if (lane >= A.R) place = lane;
-        id = __builtin_amdgcn_ds_permute(4 * place, lane);
-        mine_q.blocks = __builtin_amdgcn_ds_permute(4 * place, mine_q.blocks);
-        mine_q.span = __builtin_amdgcn_ds_permute(4 * place, mine_q.span);
+        const int id = __builtin_amdgcn_ds_permute(4 * place, lane);
+        q.blocks = __builtin_amdgcn_ds_permute(4 * place, q.blocks);
+        q.span = __builtin_amdgcn_ds_permute(4 * place, q.span);
+        const int64_t mine = count_parts(A, q.blocks, q.span, most), upto = wave_scan(mine);
+        if (key(lane64(upto, 63)) <= at) return false;
+        const int who = __ffsll((unsigned long long)__ballot(key(upto) > at)) - 1;
+        before = lane64(upto, who) - lane64(mine, who);
+        w.r = __builtin_amdgcn_readlane(id, who);
     } else {
-        for (int i = 0; i < per; ++i) {
-            const int r = lane * per + i;
-            if (r < A.R) {
-                const Request q = request_of(A, r);
-                cost += int64_t(q.blocks) * q.span;
-            }
+        if (key(A.before[A.R]) <= at) return false;
+        most = int(A.before[A.R + 1]);
+        int from = 0;                                        // the last request with no more than `at` parts before it
+        for (int n = A.R, step; n > 1; n = min(step, A.R - from)) {
+            step = (n + 63) / 64;
+            const uint64_t upto = __ballot(lane * step < n && key(A.before[from + min(lane * step, n - 1)]) <= at);
+            from += (63 - __builtin_clzll(upto | 1)) * step;
         }
+        w.r = from;
+        before = A.before[from];
     }
-    cost = lane64(wave_scan(cost), 63) * per_block;
-    const int64_t most64 = max(int64_t(A.part_tiles), quotient64(cost + A.target - 1, int64_t(A.target)));
-    const int most = int(min(most64, int64_t(1) << 30));         // tiles of a part
     auto parts_in = [&](const Request& q) { return (q.span + most - 1) / most; };
-    // (parts in the lower half, those of split blocks in the upper one)
-    auto count = [&](const Request& q) {
-        const int parts = q.blocks ? parts_in(q) : 1;
-        const int64_t n = int64_t(q.blocks) * per_block * parts;
-        return n | (parts > 1 ? n : 0) << 32;
-    };
-    auto key = [&](int64_t v) { return SPLIT_ONLY ? v >> 32 : v & 0xFFFFFFFF; };
-    int64_t mine = 0;
-    if (per == 1) mine = count(mine_q);
-    else
-        for (int i = 0; i < per; ++i)
-            if (lane * per + i < A.R) mine += count(request_of(A, lane * per + i));
-    const int64_t upto = wave_scan(mine);
-    if (key(lane64(upto, 63)) <= at) return false;
-    const int who = __ffsll((unsigned long long)__ballot(key(upto) > at)) - 1;
-    int64_t before = lane64(upto, who) - lane64(mine, who);
-    w.r = per == 1 ? __builtin_amdgcn_readlane(id, who) : min((who + 1) * per, A.R) - 1;
-    for (int base = who * per; per > 1 && base < (who + 1) * per; base += 64) {
-        const int r = base + lane;
-        const int64_t n = r < (who + 1) * per && r < A.R ? count(request_of(A, r)) : 0;
-        const int64_t sum = before + wave_scan(n);
-        const uint64_t past = __ballot(key(sum) > at);
-        if (past) {
-            const int l = __ffsll((unsigned long long)past) - 1;
-            w.r = base + l;
-            before = lane64(sum, l) - lane64(n, l);
-            break;
-        }
-        before = lane64(sum, 63);
-    }
     w.r = __builtin_amdgcn_readfirstlane(min(w.r, A.R - 1));
     w.q = request_of(A, w.r);
     w.q.first = __builtin_amdgcn_readfirstlane(w.q.first);
@@ -130,6 +120,47 @@ __device__ __forceinline__ bool find_work(const ChunkArgs& A, int64_t at, Work& 
     w.slot0 = split0 + (rev * w.parts * per_block + head);
     w.slot = w.slot0 + int64_t(w.part) * per_block;
     return w.q.m > 0;
+}
+
+// before[r]: the parts of requests 0 .. r - 1; behind them, the key tiles of a part. (Of more than 64 requests: requests
+// of 600 tokens, one of them new, 128 of them 64 us, 68 where each wavefront sums them for itself, 4096 1.66 ms and 5.35.)
+constexpr int kCountThreads = 1024;
+__global__ void __launch_bounds__(kCountThreads) count_requests_kernel(const ChunkArgs A) {
+    __shared__ int64_t sums[kCountThreads / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    auto scan = [&](int64_t v, int64_t& all) {                  // v summed over the threads up to this one
+        const int64_t in = wave_scan(v);
+        __syncthreads();
+        if (lane == 63) sums[wave] = in;
+        __syncthreads();
+        int64_t below = 0;
+        all = 0;
+        for (int i = 0; i < kCountThreads / 64; ++i) {
+            if (i < wave) below += sums[i];
+            all += sums[i];
+        }
+        return below + in;
+    };
+    int64_t tiles = 0, all;
+    for (int r = tid; r < A.R; r += kCountThreads) {
+        const Request q = request_of(A, r);
+        tiles += int64_t(q.blocks) * q.span;
+    }
+    scan(tiles, all);
+    const int most = part_limit(A, all);
+    int64_t done = 0;
+    for (int base = 0; base < A.R; base += kCountThreads) {
+        const int r = base + tid;
+        Request q{};
+        if (r < A.R) q = request_of(A, r);
+        const int64_t mine = r < A.R ? count_parts(A, q.blocks, q.span, most) : 0, upto = scan(mine, all);
+        if (r < A.R) A.before[r] = done + upto - mine;
+        done += all;
+    }
+    if (tid == 0) {
+        A.before[A.R] = done;
+        A.before[A.R + 1] = most;
+    }
 }
 
 // Key tiles [from, to) of a part
@@ -253,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
     __shared__ int strange, bad_page;
 
     Work w;
-    if (!find_work<false>(A, blockIdx.x, w)) return;
+    if (!find_work<false>(A, A.launched + blockIdx.x, w)) return;
     const Tiles tiles = tiles_of(A, w.q, w.block, w.part, w.parts);
     if (w.parts > 1 && (tiles.from >= tiles.to || uint64_t(w.slot) >= uint64_t(A.slots))) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -624,10 +655,15 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
 }
 
 template <int KV, int QT, int D>
-hipError_t chunk_d(const ChunkArgs& a, hipStream_t s) {
-    chunk_kernel<KV, QT, D><<<unsigned(a.groups), kThreads, 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.slots) return e;
+hipError_t chunk_d(ChunkArgs a, hipStream_t s) {
+    constexpr int64_t most = kLaunchItems / kThreads;
+    for (; a.launched < a.groups; a.launched += most) {
+        const int64_t groups = a.groups - a.launched < most ? a.groups - a.launched : most;
+        chunk_kernel<KV, QT, D><<<unsigned(groups), kThreads, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (!a.slots) return hipSuccess;
     join_chunks_kernel<QT, D, Chunk<KV, QT, D>::kShift><<<unsigned(a.slots), kThreads, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -665,10 +701,16 @@ ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width) {
     p.groups = blocks + (p.slots ? p.target : 0);
     p.part_o_bytes = size_t(p.slots) * kRows * c.D * 4;
     p.part_ml_bytes = size_t(p.slots) * kRows * 8;
+    p.before_bytes = R > 64 ? size_t(R + 2) * 8 : 0;
     return p;
 }
 
 hipError_t launch_chunk(const ChunkArgs& a, hipStream_t s) {
+    if (a.before) {
+        count_requests_kernel<<<1, kCountThreads, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if (a.c.dtype == WB_BF16) return chunk_t<WB_BF16, WB_BF16>(a, s);
     if (a.c.dtype == WB_F16) return chunk_t<WB_F16, WB_F16>(a, s);
     return a.q_dtype == WB_BF16 ? chunk_t<WB_E4M3, WB_BF16>(a, s) : chunk_t<WB_E4M3, WB_F16>(a, s);

@@ -91,6 +91,7 @@ struct ChunkArgs {
     float* lse = nullptr;
     float* part_o = nullptr;      // [slots][128][D] sums of the parts of split blocks
     float* part_ml = nullptr;     // [slots][128][2] their maximum and weight sum
+    int64_t* before = nullptr;    // [R + 2] parts of the requests before each, tiles of a part (more than 64 requests)
     float scale = 0.f;
     int N = 0, R = 0, Hq = 0, width = 0, window = 0, q_dtype = 0, page_log2 = 0;
     int G = 1;                    // query heads of a key-value head
@@ -98,12 +99,12 @@ struct ChunkArgs {
     int head_blocks = 1;          // blocks of a key-value head's query heads
     int part_tiles = 1;           // key tiles of a part at least
     int target = 1;               // parts that all tiles are cut into, about
-    int64_t slots = 0, groups = 0;
+    int64_t slots = 0, groups = 0, launched = 0;     // workgroups in all, and in the launches before
 };
 struct ChunkPlan {
     int heads, tokens, head_blocks, part_tiles, target;
     int64_t slots, groups;        // parts of split blocks at most (0: nothing is split); workgroups
-    size_t part_o_bytes, part_ml_bytes;
+    size_t part_o_bytes, part_ml_bytes, before_bytes;
 };
 ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width);
 hipError_t launch_chunk(const ChunkArgs& a, hipStream_t stream);

@@ -245,7 +245,7 @@ int kv_attend_chunk_work(const wb_kv_cache* c, int N, int R, int Hq, int width, 
     const int v = check_chunk(c, N, R, Hq, width);
     if (v) return v;
     const wb::ChunkPlan p = wb::chunk_plan(*c, N, R, Hq, width);
-    *bytes = p.part_o_bytes + p.part_ml_bytes;
+    *bytes = p.part_o_bytes + p.part_ml_bytes + p.before_bytes;
     return WB_OK;
 }
 
@@ -263,7 +263,7 @@ int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t 
         !aligned(starts, 4) || !aligned(lse, 4))
         return WB_EALIGN;
     const wb::ChunkPlan p = wb::chunk_plan(*c, N, R, Hq, width);
-    const size_t need = p.part_o_bytes + p.part_ml_bytes;
+    const size_t need = p.part_o_bytes + p.part_ml_bytes + p.before_bytes;
     if (need) {
         if (!work) return WB_EINVAL;
         if (work_bytes < need) return WB_ESIZE;
@@ -283,6 +283,7 @@ int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t 
     if (need) {
         a.part_o = static_cast<float*>(work);
         a.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(work) + p.part_o_bytes);
+        if (p.before_bytes) a.before = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(work) + p.part_o_bytes + p.part_ml_bytes);
     }
     a.scale = scale;
     a.N = N;
