@@ -343,3 +343,63 @@ def test_rows_of_logits_past_32_bits():
     x = torch.zeros((3, 2 ** 31 + 1000), dtype=torch.bfloat16, device="cuda")[:, :5000]
     x.copy_(3 * torch.randn((3, 5000), generator=torch.Generator().manual_seed(9)))
     check_logprobs(x, [0, 4999, 17], 7)
+
+
+def test_binding_refusals():
+    """Every wrong argument is named, and nothing is launched."""
+    import linear_attn_decode_amd as wb
+    bf, f8, f32, f64, i, long = torch.bfloat16, torch.float8_e4m3fn, torch.float32, torch.float64, torch.int32, torch.int64
+    cu = lambda *a, dtype=bf: torch.zeros(*a, device="cuda").to(dtype)
+    k, q, o = cu(4, 2, 16, 64), cu(5, 4, 64), cu(5, 4, 64)
+    t, n, s = cu(3, 2, dtype=i), cu(3, dtype=i), cu(4, dtype=i)
+    good = dict(q=q, k_cache=k, v_cache=k.clone(), table=t, lens=n, starts=s, o=o)
+    host = lambda x: x.cpu()
+    for match, kw in [("q, table: expected", dict(q=q[0])), ("q, table: expected", dict(table=n)), ("q, table: expected", dict(q=cu(5, 4, 64, dtype=i))),
+                      ("q: expected", dict(q=cu(5, 4, 128))), ("q: expected", dict(q=host(q))), ("q: expected", dict(q=cu(5, 4, 128)[..., ::2])),
+                      ("o: expected", dict(o=cu(5, 4, 128))), ("o: expected", dict(o=cu(4, 4, 64))), ("o: expected", dict(o=cu(5, 8, 64)[:, ::2])),
+                      ("o: expected", dict(o=cu(5, 4, 64, dtype=f32))), ("table: expected", dict(table=t.long())),
+                      ("table: expected", dict(table=cu(3, 4, dtype=i)[:, ::2])), ("lens: expected", dict(lens=s)), ("lens: expected", dict(lens=n.long())),
+                      ("starts: expected", dict(starts=n)), ("starts: expected", dict(starts=host(s))), ("lse: expected", dict(lse=cu(5, 4))),
+                      ("lse: expected", dict(lse=cu(4, 5, dtype=f32))), ("out of range", dict(window=-1)), ("v_cache: expected", dict(v_cache=cu(4, 2, 8, 64))),
+                      ("k_scale, v_scale: only", dict(k_scale=cu(4, 2, 16, dtype=f32), v_scale=cu(4, 2, 16, dtype=f32))),
+                      ("k_scale, v_scale: a float8", dict(k_cache=k.to(f8), v_cache=k.to(f8)))]:
+        with pytest.raises(ValueError, match=match):
+            wb.kv_attend_chunk(**{**good, **kw})
+    with pytest.raises(Exception, match="kv_attend_chunk"):                          # q of another type than the cache
+        wb.kv_attend_chunk(**{**good, "q": q.half(), "o": o.half()})
+    with pytest.raises(Exception, match="kv_attend_chunk"):                          # in place
+        wb.kv_attend_chunk(**{**good, "o": q})
+
+    x, at, freqs = cu(3, 4, 64), cu(3, dtype=i), cu(32, dtype=f64)
+    good = dict(q=x, k=x.clone(), positions=at, freqs=freqs)
+    for match, kw in [("q: expected", dict(q=x[0])), ("q: expected", dict(q=x.to(f8))), ("q: expected", dict(q=cu(3, 4, 128)[..., ::2])),
+                      ("freqs: expected", dict(freqs=freqs.float())), ("freqs: expected", dict(freqs=freqs.view(1, 32))),
+                      ("freqs: 33 pairs", dict(freqs=cu(33, dtype=f64))), ("freqs: expected", dict(freqs=host(freqs))),
+                      ("positions: expected", dict(positions=at.float())), ("positions: expected", dict(positions=cu(4, dtype=i))),
+                      ("positions: expected", dict(positions=cu(6, dtype=long)[::2])), ("q_weight: expected", dict(q_weight=cu(32))),
+                      ("q_weight: expected", dict(q_weight=cu(64, dtype=f32))), ("k_weight: expected", dict(k_weight=cu(1, 64))),
+                      ("k: expected", dict(k=cu(2, 4, 64))), ("k: expected", dict(k=cu(3, 4, 32))), ("k: expected", dict(k=x.float())),
+                      ("k: expected", dict(k=x[0])), ("q_out: expected", dict(q_out=cu(3, 5, 64))), ("k_out: expected", dict(k_out=x.float())),
+                      ("q_out: expected", dict(q_out=cu(3, 4, 128)[..., ::2])), ("q_out: expected", dict(q_out=x[0]))]:
+        with pytest.raises(ValueError, match=match):
+            wb.qk_rotate(**{**good, **kw})
+    for kw in (dict(q_out=cu(1, 1, 64).expand(3, 4, 64)), dict(k=x), dict(eps=-1.0), dict(magnitude=math.nan)):
+        with pytest.raises(Exception, match="qk_rotate"):
+            wb.qk_rotate(**{**good, **kw})
+
+    x, tok, lp = cu(3, 50), cu(3, dtype=long), cu(3, dtype=f32)
+    ids, top = cu(3, 4, dtype=i), cu(3, 4, dtype=f32)
+    good = dict(logits=x, tokens=tok, logprob=lp)
+    for match, kw in [("logits: expected", dict(logits=x[0])), ("logits: expected", dict(logits=x.to(f8))), ("logits: expected", dict(logits=cu(3, 100)[:, ::2])),
+                      ("tokens: expected", dict(tokens=tok.float())), ("tokens: expected", dict(tokens=cu(4, dtype=long))), ("logprob: expected", dict(logprob=cu(3))),
+                      ("logprob: expected", dict(logprob=cu(2, dtype=f32))), ("entropy: expected", dict(entropy=cu(3))),
+                      ("both or neither", dict(top_ids=ids)), ("both or neither", dict(top_logprobs=top)), ("top_ids: expected", dict(top_ids=tok, top_logprobs=top)),
+                      ("top_ids: expected", dict(top_ids=ids.long(), top_logprobs=top)), ("top_logprobs: expected", dict(top_ids=ids, top_logprobs=top[:, :3])),
+                      ("logprob: expected", dict(logprob=host(lp)))]:
+        with pytest.raises(ValueError, match=match):
+            wb.token_logprobs(**{**good, **kw})
+    for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=1e-40), dict(top_ids=cu(3, 51, dtype=i), top_logprobs=cu(3, 51, dtype=f32))):
+        with pytest.raises(Exception, match="token_logprobs"):
+            wb.token_logprobs(**{**good, **kw})
+    torch.cuda.synchronize()
+    assert (o == 0).all() and (lp == 0).all()
