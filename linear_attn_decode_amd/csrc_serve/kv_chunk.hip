@@ -13,7 +13,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves, kTile = 64, kRows = 32 * kWaves;
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kRows = 32 * kWaves;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------------------- where a workgroup works
@@ -31,8 +31,9 @@ __device__ __forceinline__ Request request_of(const ChunkArgs& A, int r) {
     q.bad = n < q.m || n > (A.width << A.page_log2);
     q.n = q.bad ? 0 : n;
     q.blocks = (q.m + A.tokens - 1) / A.tokens;
-    q.span = (q.n + kTile - 1) / kTile;
-    if (A.window) q.span = min(q.span, int((int64_t(A.window) + A.tokens + 2 * kTile - 3) / kTile));
+    const int l2 = A.tile_log2, tile = 1 << l2;
+    q.span = (q.n + tile - 1) >> l2;
+    if (A.window) q.span = min(q.span, int((int64_t(A.window) + A.tokens + 2 * tile - 3) >> l2));
     q.span = max(q.span, 1);
     return q;
 }
@@ -170,7 +171,8 @@ struct Tiles {
 __device__ __forceinline__ Tiles tiles_of(const ChunkArgs& A, const Request& q, int block, int part, int parts) {
     const int t0 = block * A.tokens, t1 = min(t0 + A.tokens, q.m);       // new tokens of the block
     const int past = q.n - q.m;
-    const int lo = A.window ? max(past + t0 - A.window + 1, 0) / kTile : 0, hi = q.bad ? 0 : (past + t1 + kTile - 1) / kTile;
+    const int lo = A.window ? max(past + t0 - A.window + 1, 0) >> A.tile_log2 : 0;
+    const int hi = q.bad ? 0 : (past + t1 + (1 << A.tile_log2) - 1) >> A.tile_log2;
     const int n = max(hi - lo, 0);
     return Tiles{lo + int(int64_t(n) * part / parts), lo + int(int64_t(n) * (part + 1) / parts)};
 }
@@ -247,7 +249,12 @@ __device__ __forceinline__ u32x2 scaled(f32x4 v, float by) {
     return u32x2{pack2<QT>(v[0] * by, v[1] * by), pack2<QT>(v[2] * by, v[3] * by)};
 }
 
-constexpr int waves_per_simd(int D) { return D <= 128 ? 2 : 1; }
+// Key tiles of 64 tokens, of 32 for heads of 256 columns: with 64 such a head's tiles, sums and scores fill a compute
+// unit's memory and registers with one workgroup, whose matrix and vector units then take turns (8192-token prompts,
+// 16 heads of 256, bfloat16: 812 us, 541 with two workgroups). Narrower heads have two either way, and the larger tile has
+// fewer barriers and joins (heads of 128: within 3 % of one another in 16 bits, 8-bit 760 us and 887 with 32).
+constexpr int kWavesPerSimd = 2;
+constexpr int tile_log2(int D) { return D <= 128 ? 6 : 5; }
 
 // KV: the cache's type; QT: the type of q and o; D: columns
 template <int KV, int QT, int D>
@@ -259,6 +266,8 @@ struct Chunk {
     static constexpr int DB = D / 32;                                // blocks of value columns
     static constexpr int CB = D / 64;                                // blocks of 64 columns
     static constexpr int kShift = VT == WB_F16 ? 11 : 0;             // weights enter as 2^kShift times their value
+    static constexpr int kTile = 1 << tile_log2(D);
+    static constexpr int NB = kTile / 32, TB = kTile / 8;            // its blocks of 32 tokens, of 8
     static constexpr int kTileBytes = kTile * D * 2;
 };
 
@@ -270,11 +279,11 @@ __device__ __forceinline__ const __attribute__((address_space(4))) ChunkArgs& ar
 }
 
 template <int KV, int QT, int D>
-__global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(const ChunkArgs A) {
+__global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const ChunkArgs A) {
     using T = Chunk<KV, QT, D>;
     using S = Mat32<T::ST>;
     using V = Mat32<T::VT>;
-    constexpr int KS = T::KS, DB = T::DB, CB = T::CB;
+    constexpr int KS = T::KS, DB = T::DB, CB = T::CB, kTile = T::kTile, NB = T::NB, TB = T::TB;
     constexpr bool E = KV == WB_E4M3;
     constexpr int kRowBytes = D * (E ? 1 : 2);
     constexpr float kThreshold = 4.f;
@@ -338,23 +347,24 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
     const uint32_t pages = uint32_t(C.c.pages), page_rows = uint32_t(C.c.H) << log2;
     const uint8_t* const k0 = static_cast<const uint8_t*>(C.c.k) + (size_t(w.kvh) << log2) * kRowBytes;
     const uint8_t* const v0 = static_cast<const uint8_t*>(C.c.v) + (size_t(w.kvh) << log2) * kRowBytes;
-    auto token_of = [&](int t, int j) { return uint32_t(min(t * kTile + 16 * wave + 8 * j, last)); };
-    uint32_t ids[2], bad = 0;
+    auto token_of = [&](int t, int j) { return uint32_t(min(t * kTile + 8 * NB * wave + 8 * j, last)); };
+    uint32_t ids[NB], bad = 0;
     auto load_ids = [&](int t) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) ids[j] = uint32_t(table[token_of(t, j) >> log2]);
+        for (int j = 0; j < NB; ++j) ids[j] = uint32_t(table[token_of(t, j) >> log2]);
     };
-    uint32_t key_off[2], value_off;          // bytes, in the tokens' rows
+    uint32_t key_off[NB], value_off;         // bytes, in the tokens' rows
 #pragma unroll
-    for (int j = 0; j < 2; ++j) key_off[j] = (lane >> 3) * kRowBytes + (E ? 8 : 16) * ((lane & 7) ^ (((lane >> 4) & 3) | j << 2));
+    for (int j = 0; j < NB; ++j)
+        key_off[j] = (lane >> 3) * kRowBytes + (E ? 8 : 16) * ((lane & 7) ^ (((lane >> 4) & 3) | ((NB * wave + j) & 1) << 2));
     value_off = ((lane >> 2) & 7) * kRowBytes + (E ? 8 : 16) * (4 * h + (lane & 3));
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
-                       uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)&stored[0][0][0]))) + 2048 * wave;
-    u32x2 kr[E ? 2 * CB : 1], vr[E ? 2 * CB : 1];
+                       uint32_t(uintptr_t((__attribute__((address_space(3))) uint8_t*)&stored[0][0][0]))) + 1024 * NB * wave;
+    u32x2 kr[E ? NB * CB : 1], vr[E ? NB * CB : 1];
     float sr = 0.f;
     auto stage = [&](int t, int buf) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < NB; ++j) {
             const uint32_t id = ids[j] < pages ? ids[j] : 0u;
             bad |= id ^ ids[j];                                  // (not 0 for an id outside the cache)
             const uint64_t at = (uint64_t(id) * page_rows + (token_of(t, j) & ((1u << log2) - 1))) * kRowBytes;
@@ -366,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
                     kr[j * CB + c] = *reinterpret_cast<const u32x2*>(k + 64 * c + key_off[j]);
                     vr[j * CB + c] = *reinterpret_cast<const u32x2*>(v + 64 * c + value_off);
                 } else {
-                    const uint32_t to = lds0 + 2 * T::kTileBytes * buf + 8192 * c + 1024 * j;
+                    const uint32_t to = lds0 + 2 * T::kTileBytes * buf + 1024 * (TB * c + j);
                     lds_load16_async(k + 128 * c, key_off[j], to);
                     lds_load16_async(v + 128 * c, value_off, to + T::kTileBytes);
                 }
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
         }
         if constexpr (E) {
             // scales of the tile's tokens: keys' by wavefront 0, values' by wavefront 1
-            if (wave < 2) {
+            if (wave < 2 && lane < kTile) {
                 const int tok = min(t * kTile + lane, max(w.q.n - 1, 0));
                 uint32_t page = uint32_t(C.table[size_t(w.r) * C.width + (tok >> log2)]);
                 page = page < pages ? page : 0;
@@ -385,14 +395,14 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
     auto put = [&](int buf) {                            // 8-bit rows, converted
         if constexpr (E) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < NB; ++j)
 #pragma unroll
                 for (int c = 0; c < CB; ++c) {
-                    uint8_t* to = &stored[buf][0][1024 * (8 * c + 2 * wave + j) + lane * 16];
+                    uint8_t* to = &stored[buf][0][1024 * (TB * c + NB * wave + j) + lane * 16];
                     *reinterpret_cast<u32x4*>(to) = e4m3_to8<T::ST>(kr[j * CB + c]);
                     *reinterpret_cast<u32x4*>(to + T::kTileBytes) = e4m3_to8<T::VT>(vr[j * CB + c]);
                 }
-            if (wave < 2) reinterpret_cast<float*>(&scales[buf][wave][0])[lane] = sr;
+            if (wave < 2 && lane < kTile) reinterpret_cast<float*>(&scales[buf][wave][0])[lane] = sr;
         }
     };
 
@@ -403,16 +413,16 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
     auto strange_values = [&](int t, int buf) {
         uint32_t any = 0;
 #pragma unroll
-        for (int i = 0; i < 2 * CB; ++i) {
-            const u32x4 x = *reinterpret_cast<const u32x4*>(&stored[buf][1][1024 * (8 * (i >> 1) + 2 * wave + (i & 1)) + lane * 16]);
+        for (int i = 0; i < NB * CB; ++i) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(&stored[buf][1][1024 * (TB * (i / NB) + NB * wave + i % NB) + lane * 16]);
             any |= not_finite<T::VT>(x[0]) | not_finite<T::VT>(x[1]) | not_finite<T::VT>(x[2]) | not_finite<T::VT>(x[3]);
         }
         if (__any(any != 0) && lane == 0) strange = t + 1;
         __syncthreads();
         if (strange != t + 1) return false;
 #pragma unroll 1
-        for (int i = 0; i < 2 * CB; ++i) {
-            u32x4* at = reinterpret_cast<u32x4*>(&stored[buf][1][1024 * (8 * (i >> 1) + 2 * wave + (i & 1)) + lane * 16]);
+        for (int i = 0; i < NB * CB; ++i) {
+            u32x4* at = reinterpret_cast<u32x4*>(&stored[buf][1][1024 * (TB * (i / NB) + NB * wave + i % NB) + lane * 16]);
             u32x4 x = *at;
             uint32_t bits = 0;
 #pragma unroll
@@ -423,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
             }
             *at = x;
             // the lane holds columns 8 (lane % 4) ..+7 of half h of row (lane / 4) % 8
-            reinterpret_cast<uint8_t*>(&strange_bits[16 * wave + 8 * (i & 1) + ((lane >> 2) & 7)][2 * (i >> 1) + h])[lane & 3] = uint8_t(bits);
+            reinterpret_cast<uint8_t*>(&strange_bits[8 * (NB * wave + i % NB) + ((lane >> 2) & 7)][2 * (i / NB) + h])[lane & 3] = uint8_t(bits);
         }
         __syncthreads();
         return true;
@@ -454,13 +464,13 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
         const bool found = partial && strange_values(t, buf);
         if (t < any_from || t >= any_to) return;
         int to = limit - t * kTile - 4 * h, from = lower - t * kTile - 4 * h;         // of the lane's tokens
-        f32x16 s[2];
+        f32x16 s[NB];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
             s[b] = f32x16{};
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                const u32x4 a = *reinterpret_cast<const u32x4*>(&stored[buf][0][key_at[i & 3] + 8192 * (i >> 2) + 4096 * b]);
+                const u32x4 a = *reinterpret_cast<const u32x4*>(&stored[buf][0][key_at[i & 3] + 1024 * TB * (i >> 2) + 4096 * b]);
                 s[b] = S::mul(a, qf[i], s[b]);
             }
             if constexpr (E) {
@@ -475,18 +485,18 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
         if (partial) {
             asm volatile("" : "+v"(to), "+v"(from));             // (or every tile would go through the selections)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[b][i] = hide(s[b][i], to - 1 - (32 * b + 8 * (i >> 2) + (i & 3)));
             if (windowed)
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
+                for (int b = 0; b < NB; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[b][i] = hide(s[b][i], 32 * b + 8 * (i >> 2) + (i & 3) - from);
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
         top = max_xor32(top);
@@ -503,14 +513,14 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
             // (scores near the ends of float32's range: their differences first)
             const float by = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[b][i] -= by;
             ref = -T::kShift;
         }
-        u32x4 p[4], p2[T::kTwoP ? 4 : 1];
+        u32x4 p[2 * NB], p2[T::kTwoP ? 2 * NB : 1];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 float e[4];
@@ -546,11 +556,11 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(D)) chunk_kernel(cons
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
-            for (int s4 = 0; s4 < 4; ++s4) {              // 16 tokens
+            for (int s4 = 0; s4 < 2 * NB; ++s4) {         // 16 tokens
                 u32x4 a;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const u32x2 x = __builtin_bit_cast(u32x2, read_transposed(values + 1024 * (8 * (db >> 1) + 2 * s4 + u) + 512 * (db & 1)));
+                    const u32x2 x = __builtin_bit_cast(u32x2, read_transposed(values + 1024 * (TB * (db >> 1) + 2 * s4 + u) + 512 * (db & 1)));
                     a[2 * u] = x[0];
                     a[2 * u + 1] = x[1];
                 }
@@ -678,8 +688,8 @@ hipError_t chunk_t(const ChunkArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Tiles of a part at least, where a request's block is split.
-constexpr int kPartTiles = 4;
+// Tokens of a part at least, where a request's block is split.
+constexpr int kPartTokens = 256;
 
 ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width) {
     const int G = Hq / c.H;
@@ -687,15 +697,16 @@ ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width) {
     p.heads = G < kRows ? G : kRows;
     p.head_blocks = (G + p.heads - 1) / p.heads;
     p.tokens = kRows / p.heads;
-    p.part_tiles = kPartTiles;
-    p.target = 256 * waves_per_simd(c.D);
+    p.tile_log2 = tile_log2(c.D);
+    p.part_tiles = kPartTokens >> p.tile_log2;
+    p.target = 256 * kWavesPerSimd;
     const int64_t by_tokens = int64_t(N) / p.tokens + R, blocks = (N < by_tokens ? N : by_tokens) * int64_t(c.H) * p.head_blocks;
-    const int64_t tiles = (int64_t(width) * c.page + kTile - 1) / kTile;
+    const int64_t tiles = (int64_t(width) * c.page + (1 << p.tile_log2) - 1) >> p.tile_log2;
     p.slots = 0;
-    if (tiles > kPartTiles) {
+    if (tiles > p.part_tiles) {
         // (a block of s tiles has ceil(s / t) parts of at most t >= all tiles / target: fewer than
         // 2 s / t where that is more than one)
-        const int64_t most = blocks * ((tiles + kPartTiles - 1) / kPartTiles);
+        const int64_t most = blocks * ((tiles + p.part_tiles - 1) / p.part_tiles);
         p.slots = most < 2 * p.target ? most : 2 * p.target;
     }
     p.groups = blocks + (p.slots ? p.target : 0);

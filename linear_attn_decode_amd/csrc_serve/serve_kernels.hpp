@@ -97,12 +97,13 @@ struct ChunkArgs {
     int G = 1;                    // query heads of a key-value head
     int heads = 1, tokens = 1;    // of a block of rows: query heads of new tokens
     int head_blocks = 1;          // blocks of a key-value head's query heads
+    int tile_log2 = 6;            // of the tokens of a key tile
     int part_tiles = 1;           // key tiles of a part at least
     int target = 1;               // parts that all tiles are cut into, about
     int64_t slots = 0, groups = 0, launched = 0;     // workgroups in all, and in the launches before
 };
 struct ChunkPlan {
-    int heads, tokens, head_blocks, part_tiles, target;
+    int heads, tokens, head_blocks, tile_log2, part_tiles, target;
     int64_t slots, groups;        // parts of split blocks at most (0: nothing is split); workgroups
     size_t part_o_bytes, part_ml_bytes, before_bytes;
 };

@@ -297,6 +297,7 @@ int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t 
     a.heads = p.heads;
     a.tokens = p.tokens;
     a.head_blocks = p.head_blocks;
+    a.tile_log2 = p.tile_log2;
     a.part_tiles = p.part_tiles;
     a.target = p.target;
     a.slots = p.slots;

@@ -70,15 +70,17 @@ def test_chunk_refusals(lib):
     assert chunk(lib, cache(dtype=serve.E4M3, k_scale=A, v_scale=A), q_dtype=serve.E4M3) == EINVAL
 
 
+TARGET = 512            # parts that all tiles are cut into
+
+
 def plan(N, R, Hq, H, D, page, width):
-    """The split in whole numbers, as the library documents it: (heads of a block, tokens of a block, blocks of a
-    key-value head's query heads, parts wanted, slots)."""
+    """(Tokens of a block of rows, blocks of a key-value head's query heads, tokens of a key tile, slots)."""
     G = Hq // H
-    heads = min(G, 128)
-    tokens, head_blocks, target = 128 // heads, -(-G // heads), 256 * (1 if D == 256 else 2)
+    heads, tile = min(G, 128), 32 if D == 256 else 64
+    tokens, head_blocks, least = 128 // heads, -(-G // heads), 256 // tile
     blocks = min(N, N // tokens + R) * H * head_blocks
-    tiles = -(-width * page // 64)
-    return heads, tokens, head_blocks, target, min(blocks * -(-tiles // 4), 2 * target) if tiles > 4 else 0
+    tiles = -(-width * page // tile)
+    return tokens, head_blocks, tile, min(blocks * -(-tiles // least), 2 * TARGET) if tiles > least else 0
 
 
 @pytest.mark.parametrize("N,R,Hq,H,D,page,width", [(5, 2, 8, 4, 128, 16, 17), (8192, 1, 32, 8, 128, 64, 128), (64, 16, 40, 2, 64, 8, 1000),
@@ -88,12 +90,12 @@ def test_chunk_workspace(lib, N, R, Hq, H, D, page, width):
     before each."""
     n = ctypes.c_size_t()
     assert lib.kv_attend_chunk_work(cache(H=H, D=D, page=page), N, R, Hq, width, n) == OK
-    assert n.value == plan(N, R, Hq, H, D, page, width)[4] * 128 * (4 * D + 8) + (8 * (R + 2) if R > 64 else 0)
+    assert n.value == plan(N, R, Hq, H, D, page, width)[3] * 128 * (4 * D + 8) + (8 * (R + 2) if R > 64 else 0)
 
 
 @pytest.mark.parametrize("seed", range(40))
 def test_parts_stay_within_the_slots(seed):
-    """Parts of t key tiles at most, t = max(4, all tiles / target): those of split blocks have slots, all have workgroups,
+    """Parts of t key tiles at most, t = max(256 tokens, all tiles / target): those of split blocks have slots, all have workgroups,
     and every tile of a block is in one part."""
     rng = np.random.default_rng(seed)
     H, G = int(rng.integers(1, 9)), int(rng.integers(1, 200))
@@ -106,22 +108,22 @@ def test_parts_stay_within_the_slots(seed):
     N, window = int(m.sum()), int(rng.choice([0, 0, 1, 100, 5000]))
     if N == 0:
         return
-    heads, tokens, head_blocks, target, slots = plan(N, R, H * G, H, D, page, width)
+    tokens, head_blocks, tile, slots = plan(N, R, H * G, H, D, page, width)
     per_block = H * head_blocks
-    span = -(-n // 64)
+    span = -(-n // tile)
     if window:
-        span = np.minimum(span, (window + tokens + 126 - 1) // 64)
+        span = np.minimum(span, (window + tokens + 2 * tile - 3) // tile)
     span = np.maximum(span, 1)
     blocks = -(-m // tokens)
-    most = max(4, -(-int((blocks * span).sum()) * per_block // target))
+    most = max(256 // tile, -(-int((blocks * span).sum()) * per_block // TARGET))
     parts = -(-span // most)
     total, split = int((blocks * parts).sum()) * per_block, int((blocks * parts)[parts > 1].sum()) * per_block
-    groups = min(N, N // tokens + R) * per_block + (target if slots else 0)
+    groups = min(N, N // tokens + R) * per_block + (TARGET if slots else 0)
     assert split <= slots and total <= groups, (split, slots, total, groups)
     for r in range(R):
         for b in range(int(blocks[r])):
             t0, t1, past = b * tokens, min((b + 1) * tokens, int(m[r])), int(n[r] - m[r])
-            lo, hi = max(past + t0 - window + 1, 0) // 64 if window else 0, -(-(past + t1) // 64)
+            lo, hi = max(past + t0 - window + 1, 0) // tile if window else 0, -(-(past + t1) // tile)
             assert hi - lo <= span[r]
             ends = [lo + (hi - lo) * p // int(parts[r]) for p in range(int(parts[r]) + 1)]
             assert ends[0] == lo and ends[-1] == hi and all(x <= y for x, y in zip(ends, ends[1:]))
