@@ -2,7 +2,28 @@
 //
 //   o_i = sum_t e^{s_it - m} v_t / sum_t e^{s_it - m},  s_it = scale q_i . k_t,  t <= position of i
 //
-// in one pass over the stored tokens with a running maximum.
+// in one pass over the stored tokens with a running maximum. A key-value head's query heads read the same tokens, so a
+// workgroup takes a block of 128 rows: the heads of as many neighbouring new tokens as give 128. Each of its 4 wavefronts
+// has 32 of them, whose queries stay in registers; the tokens' keys and values go through LDS, which all rows share, in
+// two tiles by turns: the next one's loads go from memory straight to LDS behind this one's products.
+//
+// Scores are taken transposed, K Q^T (32 x 32 x 16 products): a lane ends with 16 tokens of one row, whose maximum and sum
+// need one exchange between two lanes, and whose weights are in place as an operand of V^T P^T, where a product's 16 tokens
+// may come in any order as long as both operands agree. V's operand is read from LDS by transposing reads. Weights never
+// leave registers, and the accumulators hold a row in a lane, so that its rescaling is one factor.
+// The weights' reference moves only when a row's maximum has risen by more than 2^4 (kThreshold): 2^4 is far from the end
+// of either type, and all tiles but a row's first few then go without rescaling the accumulators.
+// Weights enter the second product as one value of 16 bits: within half a step of each, 2^-8 in bfloat16, as large as the
+// rounding of o itself, and averaged over tokens; a second limb would add half as many products again (the float16 query
+// over an 8-bit cache, which has two bfloat16 limbs, pays 13 %: 855 us against 757). Float16 weights are 2^11 of themselves
+// (kShift; at most 2^15 with the lazy reference): what falls below its smallest step is 2^-36 of the largest. The sum of
+// weights is taken in float32 of the weights before they are rounded.
+//
+// Prompts are bound by the matrix units at the power limit (8192 tokens, 32 / 8 heads of 128, bfloat16: 541 to 580 us,
+// 0.95 to 1.02 PFLOP/s, clocks at 1.8 to 2.05 GHz; the same call over zeros 485 us; a large library product 1.16 to 1.23
+// PFLOP/s over random numbers, 1.71 over zeros), in it the exponentials take 7 %, the whole of the softmax 15 %, reading
+// LDS 14 %, staging 16 % (each left out alone). Few rows over long caches are bound by reading the cache: 64 requests of
+// 5 drafted tokens each, 367 MB, 94 us (3.9 TB/s), where the last parts end late and a second launch joins.
 #include "serve_device.hpp"
 
 namespace wb {
@@ -286,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
     constexpr int KS = T::KS, DB = T::DB, CB = T::CB, kTile = T::kTile, NB = T::NB, TB = T::TB;
     constexpr bool E = KV == WB_E4M3;
     constexpr int kRowBytes = D * (E ? 1 : 2);
-    constexpr float kThreshold = 4.f;
+    constexpr float kThreshold = 4.f;            // (in powers of two; 0: an 8192-token prompt 589 us, not 563)
     __shared__ __attribute__((aligned(1024))) uint8_t stored[2][2][T::kTileBytes];        // [buffer][keys, values]
     __shared__ f32x4 scales[2][2][kTile / 4];
     __shared__ uint32_t strange_bits[kTile][DB];                     // of the tile's values: columns of each token
@@ -627,7 +648,9 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
 }
 
 // Joins the parts of split blocks: as many workgroups as parts, the p-th of a block for the
-// p-th share of its rows, a lane per 4 columns.
+// p-th share of its rows, a lane per 4 columns, with the sums of 8 parts on their way at a time (16 new
+// tokens of 16000, 128 parts: 32 us a call; 52 with one part after the other).
+constexpr int kOnWay = 8;
 template <int QT, int D, int SHIFT>
 __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A) {
     Work w;
@@ -637,6 +660,7 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
     const int heads_here = min(A.heads, A.G - w.hb * A.heads);
     const int64_t step = int64_t(A.c.H) * A.head_blocks;          // slots between a block's parts
     const Tiles all = tiles_of(A, w.q, w.block, 0, 1);
+    const int64_t n = all.to - all.from;
     const float natural = A.scale == 0.f ? 1.f : fabsf(A.scale), mul = natural * kLog2e;
     for (int e = threadIdx.x; e < (r1 - r0) * (D / 4); e += kThreads) {
         const int j = r0 + e / (D / 4), d = 4 * (e % (D / 4));
@@ -644,18 +668,38 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
         if (head >= heads_here) continue;
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
         float m = -INFINITY, l = 0.f;
-        for (int p = 0; p < w.parts; ++p) {
-            const int64_t slot = w.slot0 + p * step;
-            const int64_t n = all.to - all.from;
-            if (n * p / w.parts >= n * (p + 1) / w.parts || uint64_t(slot) >= uint64_t(A.slots)) continue;      // (a part without tiles)
-            const size_t at = size_t(slot) * kRows + j;
-            const float mc = A.part_ml[2 * at], lc = A.part_ml[2 * at + 1];
-            const f32x4 vc = *reinterpret_cast<const f32x4*>(A.part_o + at * D + d);
-            const float top = fmaxf(m, mc), ref = top == -INFINITY ? 0.f : top;
-            const float f = __builtin_amdgcn_exp2f((m - ref) * mul), fc = __builtin_amdgcn_exp2f((mc - ref) * mul);
-            l = l * f + lc * fc;
-            v = v * f + vc * fc;
+        for (int p0 = 0; p0 < w.parts; p0 += kOnWay) {
+            float mc[kOnWay], lc[kOnWay];
+            f32x4 vc[kOnWay];
+            bool some[kOnWay];
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kOnWay; ++i) {
+                const int p = p0 + i;
+                const int64_t slot = w.slot0 + p * step;
+                // (a part without tiles has stored nothing; slot 0 is read in its place, and left out)
+                some[i] = p < w.parts && (n >= w.parts || n * p / w.parts < n * (p + 1) / w.parts) && uint64_t(slot) < uint64_t(A.slots);
+                const size_t at = size_t(some[i] ? slot : 0) * kRows + j;
+                mc[i] = A.part_ml[2 * at];
+                lc[i] = A.part_ml[2 * at + 1];
+                vc[i] = *reinterpret_cast<const f32x4*>(A.part_o + at * D + d);
+            }
+#pragma unroll
+            for (int i = 0; i < kOnWay; ++i) {
+                mc[i] = some[i] ? mc[i] : -INFINITY;
+                top = fmaxf(top, mc[i]);
+            }
+            const float ref = top == -INFINITY ? 0.f : top, f = __builtin_amdgcn_exp2f((m - ref) * mul);
+            l *= f;
+            v *= f;
             m = top;
+#pragma unroll
+            for (int i = 0; i < kOnWay; ++i)
+                if (some[i]) {
+                    const float fc = __builtin_amdgcn_exp2f((mc[i] - ref) * mul);
+                    l += lc[i] * fc;
+                    v += vc[i] * fc;
+                }
         }
         const size_t row = (size_t(w.q.first) + w.block * A.tokens + token) * A.Hq + w.kvh * A.G + w.hb * A.heads + head;
         const float by = l == 0.f ? 0.f : 1.f / l;
@@ -688,8 +732,11 @@ hipError_t chunk_t(const ChunkArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Tokens of a part at least, where a request's block is split.
-constexpr int kPartTokens = 256;
+// Tokens of a part at least, where a request's block is split. All tiles are cut into about as many parts as the device
+// holds workgroups (512): twice as many make 64 requests of drafts 102 us, not 94 (the starts of parts, their sums and
+// the join), and windows 64, not 48. (One request's 16 new tokens of 1000: 13.9 us with parts of 128 tokens, 18.0 with 256;
+// of 4000 18.2 and 17.8.)
+constexpr int kPartTokens = 128;
 
 ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width) {
     const int G = Hq / c.H;

@@ -3,7 +3,8 @@
 //   y = x / sqrt(mean x^2 + eps) w,   (a, b) -> (a cos t - b sin t, a sin t + b cos t) magnitude,
 //   t = position * frequency of the pair
 //
-// Each value is read and written once, which bounds it (HBM). A wavefront takes one token and
+// Each value is read and written once, which bounds it (HBM; 32773 tokens of 40 heads of 128, bfloat16: 146 us, 4.58
+// TB/s, where a copy reaches 4.76). A wavefront takes one token and
 // some of its heads: its lanes find the cosines and sines of the token's angles, one or two
 // pairs each, and share them through LDS; then each slot of `lanes` neighbouring lanes takes a
 // head at a time, a lane both members of W pairs (or 2 W columns that are not turned), so that
@@ -283,10 +284,11 @@ hipError_t launch_rotate(RotateArgs a, int N, hipStream_t s) {
     const int W = rotate_vector(a), units = (a.D + 2 * W - 1) / (2 * W);
     a.lanes = 4;
     while (a.lanes < units && a.lanes < 64) a.lanes *= 2;
-    // Wavefronts of a token: one takes all of its heads where there are tokens enough for 8192 of them
-    // (8 a SIMD), which then share its angles; else more, down to one head a slot.
+    // Wavefronts of a token: one takes all of its heads, which then share its angles, where there are tokens enough for
+    // 4096 of them (4 a SIMD); else more, down to one head a slot. (40 heads of 128: 4000 tokens 19.3 us, 21.0 with 8192
+    // and 18.4 with 2048; 1000 tokens 7.5, 7.1 and 8.2.)
     const int slots = 64 / a.lanes, rounds = (a.q.H + a.k.H + slots - 1) / slots;
-    int64_t wanted = (8192 + int64_t(N) - 1) / N;
+    int64_t wanted = (4096 + int64_t(N) - 1) / N;
     a.waves_per_token = int(wanted < rounds ? wanted : rounds);
     // Outputs that the 256 MB last-level cache could not hold are stored past the caches (32773 tokens of 40 heads of 128,
     // 336 MB: 146 us against 154); what fits is left there for the calls that read it.

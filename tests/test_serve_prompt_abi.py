@@ -51,11 +51,11 @@ def test_bad_caches_are_refused(lib, bad, code):
 
 def test_chunk_refusals(lib):
     n = ctypes.c_size_t()
-    assert lib.kv_attend_chunk_work(cache(), 5, 2, 8, 16, n) == OK and n.value == 0      # 256 tokens: nothing is split
-    assert lib.kv_attend_chunk_work(cache(), 5, 2, 8, 17, n) == OK and n.value > 0
-    assert lib.kv_attend_chunk_work(cache(), 5, 2, 8, 17, None) == EINVAL
+    assert lib.kv_attend_chunk_work(cache(), 5, 2, 8, 8, n) == OK and n.value == 0       # 128 tokens: nothing is split
+    assert lib.kv_attend_chunk_work(cache(), 5, 2, 8, 9, n) == OK and n.value > 0
+    assert lib.kv_attend_chunk_work(cache(), 5, 2, 8, 9, None) == EINVAL
     assert chunk(lib, cache(), N=0) == OK
-    assert chunk(lib, cache(), N=0, q=None, table=None, lens=None, starts=None, o=None, width=17) == OK
+    assert chunk(lib, cache(), N=0, q=None, table=None, lens=None, starts=None, o=None, width=9) == OK
     for kw, code in [(dict(N=-1), EINVAL), (dict(R=0), EINVAL), (dict(R=65537), EUNSUPPORTED), (dict(Hq=0), EINVAL), (dict(Hq=9), EINVAL),
                      (dict(Hq=8192), EUNSUPPORTED), (dict(N=1 << 28), EUNSUPPORTED), (dict(width=0), EINVAL),
                      (dict(width=(1 << 26) + 1), EUNSUPPORTED), (dict(q=None), EINVAL), (dict(table=None), EINVAL), (dict(lens=None), EINVAL),
@@ -63,8 +63,8 @@ def test_chunk_refusals(lib):
                      (dict(q_dtype=serve.E4M3), EINVAL), (dict(q_dtype=9), EINVAL), (dict(q_dtype=serve.F16), EUNSUPPORTED),
                      (dict(q=A + 2), EALIGN), (dict(q_row=1020), EALIGN), (dict(q_head=130), EALIGN), (dict(o=B + 8), EALIGN),
                      (dict(table=A + 2), EALIGN), (dict(lens=A + 1), EALIGN), (dict(starts=A + 2), EALIGN), (dict(lse=A + 2), EALIGN),
-                     (dict(o=A), EINVAL), (dict(width=17), EINVAL), (dict(width=17, work=A, work_bytes=n.value - 1), ESIZE),
-                     (dict(width=17, work=A + 8, work_bytes=n.value), EALIGN), (dict(R=65), EINVAL),
+                     (dict(o=A), EINVAL), (dict(width=9), EINVAL), (dict(width=9, work=A, work_bytes=n.value - 1), ESIZE),
+                     (dict(width=9, work=A + 8, work_bytes=n.value), EALIGN), (dict(R=65), EINVAL),
                      (dict(R=65, work=A, work_bytes=67 * 8 - 1), ESIZE)]:
         assert chunk(lib, cache(), **kw) == code, kw
     assert chunk(lib, cache(dtype=serve.E4M3, k_scale=A, v_scale=A), q_dtype=serve.E4M3) == EINVAL
@@ -77,7 +77,7 @@ def plan(N, R, Hq, H, D, page, width):
     """(Tokens of a block of rows, blocks of a key-value head's query heads, tokens of a key tile, slots)."""
     G = Hq // H
     heads, tile = min(G, 128), 32 if D == 256 else 64
-    tokens, head_blocks, least = 128 // heads, -(-G // heads), 256 // tile
+    tokens, head_blocks, least = 128 // heads, -(-G // heads), 128 // tile
     blocks = min(N, N // tokens + R) * H * head_blocks
     tiles = -(-width * page // tile)
     return tokens, head_blocks, tile, min(blocks * -(-tiles // least), 2 * TARGET) if tiles > least else 0
@@ -95,7 +95,7 @@ def test_chunk_workspace(lib, N, R, Hq, H, D, page, width):
 
 @pytest.mark.parametrize("seed", range(40))
 def test_parts_stay_within_the_slots(seed):
-    """Parts of t key tiles at most, t = max(256 tokens, all tiles / target): those of split blocks have slots, all have workgroups,
+    """Parts of t key tiles at most, t = max(128 tokens, all tiles / target): those of split blocks have slots, all have workgroups,
     and every tile of a block is in one part."""
     rng = np.random.default_rng(seed)
     H, G = int(rng.integers(1, 9)), int(rng.integers(1, 200))
@@ -115,7 +115,7 @@ def test_parts_stay_within_the_slots(seed):
         span = np.minimum(span, (window + tokens + 2 * tile - 3) // tile)
     span = np.maximum(span, 1)
     blocks = -(-m // tokens)
-    most = max(256 // tile, -(-int((blocks * span).sum()) * per_block // TARGET))
+    most = max(128 // tile, -(-int((blocks * span).sum()) * per_block // TARGET))
     parts = -(-span // most)
     total, split = int((blocks * parts).sum()) * per_block, int((blocks * parts)[parts > 1].sum()) * per_block
     groups = min(N, N // tokens + R) * per_block + (TARGET if slots else 0)
