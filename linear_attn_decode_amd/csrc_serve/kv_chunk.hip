@@ -254,7 +254,7 @@ __device__ __forceinline__ s16x4 read_transposed(const uint8_t* at) {
 // all such loads: the next tile's would not stay in flight behind this one's products. It writes no register, so there
 // is none for the compiler to use too early; lds_loads_wait() and a barrier come before the data is read.
 __device__ __forceinline__ void lds_load16_async(const uint8_t* base, uint32_t off, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(off), "s"(base) : "memory", "m0");
 }
 
 // -infinity in place of x where d is negative. (A selection by sign bits: conditions in scalar registers, 32 of them
