@@ -457,7 +457,8 @@ hipError_t logprobs_t(const LogprobArgs& a, unsigned groups, hipStream_t s) {
 // alternatives takes 25.5 us, not 18.8, and 128 rows 28.1, not 20.3: every segment finds alternatives of its own), of 16
 // chunks of 512 columns at least, and so that their alternatives can be ordered as one list. A segment's groups, whose maxima are kept: the largest of which there are
 // twice as many as alternatives wanted (or hardly anything could be left out), up to 512, and whose vectors, of the
-// first K groups, fit LDS.
+// first K groups, fit LDS (K 128 of them up to 32 alternatives; past that K 64, so that 64 segments hold 2^24 - 8 columns
+// from any alignment on).
 LogprobPlan logprob_plan(int N, int V, int K) {
     const int chunks = (V + 7 + 511) / 512;
     LogprobPlan p;
@@ -470,7 +471,6 @@ LogprobPlan logprob_plan(int N, int V, int K) {
     if (n < least) n = least;
     const int64_t c = (chunks + n - 1) / n;
     p.group = wide && c / 2 >= 2 * K ? 128 : c >= 2 * K || c > kMaxGroups / 8 ? 64 : 8;
-    if (p.group == 64 && c > kMaxGroups) p.group = 128;
     p.chunk = K ? (p.group == 128 ? 2 : 1) : c >= 256 ? 2 : 1;
     p.segments = int(n);
     p.part_bytes = n > 1 ? size_t(N) * n * (2 + K) * 8 : 0;

@@ -61,7 +61,8 @@ int check_chunk(const wb_kv_cache* c, int N, int R, int Hq, int width) {
 
 int check_logprobs(int N, int V, int K) {
     if (N < 0 || V < 1 || K < 0 || K > V) return WB_EINVAL;
-    return V > kMaxVocabulary || K > kMaxAlternatives ? WB_EUNSUPPORTED : WB_OK;
+    // (64 segments of 512 groups of 512 columns, from an aligned address on, where there are more than 32 alternatives)
+    return V > (K > 32 ? kMaxVocabulary - 8 : kMaxVocabulary) || K > kMaxAlternatives ? WB_EUNSUPPORTED : WB_OK;
 }
 
 size_t work_bytes_of(const wb::AttendPlan& p) {

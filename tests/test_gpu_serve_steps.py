@@ -403,3 +403,40 @@ def test_binding_refusals():
             wb.token_logprobs(**{**good, **kw})
     torch.cuda.synchronize()
     assert (o == 0).all() and (lp == 0).all()
+
+
+@pytest.mark.parametrize("R", [65, 4097, 65536])
+def test_many_requests_some_without_new_tokens(R):
+    """As many requests as there may be, two of three without a new token; each row sees one token, whose value it has."""
+    import linear_attn_decode_amd as wb
+    g = torch.Generator().manual_seed(R)
+    k, v = (rand(g, 5, 2, 8, 64, dtype="f16").cuda() for _ in range(2))
+    new = (torch.rand(R, generator=g) < 0.34).int()
+    new[-1] = 0
+    starts = torch.cat([torch.zeros(1, dtype=torch.int32), new.cumsum(0).int()])
+    N = int(starts[-1])
+    q = rand(g, N + 3, 2, 64, dtype="f16").cuda()
+    o, lse = torch.full_like(q, 7.0), torch.full((N + 3, 2), 7.0, device="cuda")
+    table = (torch.arange(R, dtype=torch.int32) % 5).view(R, 1)
+    wb.kv_attend_chunk(q, k, v, table.cuda(), torch.ones(R, dtype=torch.int32, device="cuda"), starts.cuda(), o, lse=lse)
+    torch.cuda.synchronize()
+    page = table[new.bool(), 0].long().cuda()
+    assert torch.equal(o[:N], v[page, :, 0]) and (o[N:] == 7).all() and (lse[N:] == 7).all()
+
+
+@pytest.mark.parametrize("K", [0, 1, 32, 33, 64])
+def test_largest_vocabulary(K):
+    """2^24 columns (8 fewer with more than 32 alternatives, from any alignment on); the same with every column equal, where
+    no group of columns can be left out."""
+    import linear_attn_decode_amd as wb
+    V = 2 ** 24
+    x = torch.randn((1, V), generator=torch.Generator().manual_seed(K)).bfloat16().cuda()
+    if K > 32:
+        with pytest.raises(RuntimeError, match="EUNSUPPORTED"):
+            wb.token_logprobs(x, torch.tensor([0]).cuda(), torch.empty(1, device="cuda"), top_logprobs=torch.empty((1, K), device="cuda"),
+                              top_ids=torch.empty((1, K), dtype=torch.int32, device="cuda"))
+        x = x[:, 7:V - 1]
+    check_logprobs(x, [x.shape[1] - 1], K)
+    if K > 32:
+        x.fill_(2.5)
+        check_logprobs(x, [12345], K)

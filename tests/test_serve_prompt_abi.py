@@ -186,6 +186,27 @@ def test_logprob_refusals(lib):
         assert call(**kw) == code, kw
 
 
+@pytest.mark.parametrize("K", [1, 2, 5, 16, 31, 32, 33, 50, 64])
+def test_logprob_segments_fit_their_memory(lib, K):
+    """From the workspace's size (sums and K keys a segment, a counter a row): segments a lane each, their keys in one list
+    of 4096, and 512 groups of 1024 columns in a segment at most, or of 512 where K groups of 1024 have more than 4096
+    vectors; from any alignment of the row on."""
+    n = ctypes.c_size_t()
+    most = 2 ** 24 - 8 * (K > 32)
+    assert lib.token_logprobs_work(1, most + 1, K, n) == EUNSUPPORTED
+    for V in [most, most - 1, 2 ** 24 - 600, 2 ** 23 + 1, 2 ** 21 + 5, 2 ** 19 + 1, 2 ** 18, 151001, 128000, 20000, 9000, 700, K]:
+        for N in (1, 2, 3, 7, 40, 255, 256, 257, 5000):
+            if lib.token_logprobs_work(N, V, K, n) == OK:
+                segments = (n.value // N // 8 - 1) // (2 + K) if n.value else 1
+                assert n.value in (0, 8 * N * (segments * (2 + K) + 1)) and segments <= 64 and segments * K <= 4096
+                columns = 1024 if K <= 32 else 512
+                assert K * columns // 8 <= 4096
+                chunks = -(-(V + 7) // columns)
+                assert -(-chunks // segments) <= 512, (N, V, K, segments)
+            else:
+                assert V > most
+
+
 def test_binding_refuses_cpu_tensors_and_sizes_past_32_bits():
     torch = pytest.importorskip("torch")
     z = torch.zeros
