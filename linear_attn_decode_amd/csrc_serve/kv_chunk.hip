@@ -530,8 +530,9 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
             m = m_new;
         }
         float ref = (m == -INFINITY ? 0.f : m * mul) - T::kShift;
-        if (__any(!(fabsf(ref) < 0x1p100f))) {
-            // (scores near the ends of float32's range: their differences first)
+        if (__any(!(fabsf(ref) < 0x1p8f))) {
+            // Scores far from 0: their differences first. (The reference is a rounded product, by which the exponents
+            // are off, up to half of its last place: 2^-17 here, but 2^7 from 2^31 on.)
             const float by = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
