@@ -5,8 +5,8 @@
 // Reading the logits once bounds it (HBM; the exponentials and sums take about as long, 9 operations and
 // an exponential a column). A workgroup takes a row, or, where rows are few, a segment of one; a lane
 // takes vectors of 8 columns and keeps, of d = x log2 e - ref with a whole number ref from the running
-// maximum up, s = sum 2^d and t = sum 2^d d. An exponent is rounded once, relative to itself, a change of
-// ref is an exact factor, and the entropy is log s - t / s without cancellation.
+// maximum up (or, where that is 2^26 and more, d = (x - maximum) log2 e), s = sum 2^d and t = sum 2^d d. An
+// exponent is rounded once, relative to itself, a change of ref is an exact factor, and the entropy is log s - t / s without cancellation.
 // The top K need no second pass over the row: the stream leaves the maximum of every group of 64, 512 or
 // 1024 columns in LDS. K groups by (maximum, then position) hold all of the top K, for any column of
 // another group is behind the maxima of K that are larger, or as large and before it. Those groups are
@@ -24,6 +24,7 @@ constexpr int kMaxTop = 64, kMaxGroups = 512;
 constexpr int kMaxKeys = 4096;                    // in LDS
 constexpr int kOrdered = 128;                     // keys that are ordered by comparing all pairs
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kFar = 0x1p26f;                   // references are whole numbers below it
 
 // Order of values as whole numbers: larger ones first, -0 as 0, NaN as -infinity
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -87,28 +88,31 @@ __device__ __forceinline__ float largest(const float (&x)[8]) {
     return fmaxf(top, -INFINITY);                                  // (NaN throughout)
 }
 
-// s = sum 2^{c x - ref}, t = sum 2^{c x - ref} (c x - ref), ref a whole number (-infinity: nothing yet)
+// s and t of another reference, which is `by` (in powers of two) above theirs if that is negative
+__device__ __forceinline__ void move_sums(float& s, float& t, float by) {
+    // (2^-256 is 0: nothing is left of sums so far below, which the product must not turn into NaN)
+    by = fmaxf(by, -256.f);
+    const float f = __builtin_amdgcn_exp2f(by);
+    t = (t + s * by) * f;
+    s *= f;
+}
+// s = sum 2^{c x - ref}, t = sum 2^{c x - ref} (c x - ref) of a lane's columns and more (ref -infinity: nothing yet)
 struct Sums {
-    float ref = -INFINITY, s = 0.f, t = 0.f;
-    __device__ __forceinline__ void move(float to) {            // to >= ref
-        // (2^-256 is 0: nothing is left of sums so far below, which the product must not turn into NaN)
-        const float by = ref == to ? 0.f : fmaxf(ref - to, -256.f), f = __builtin_amdgcn_exp2f(by);
-        t = (t + s * by) * f;
-        s *= f;
+    double ref = -INFINITY;
+    float s = 0.f, t = 0.f;
+    __device__ __forceinline__ void move(double to) {            // to >= ref
+        move_sums(s, t, ref == to ? 0.f : float(ref - to));
         ref = to;
     }
-    __device__ __forceinline__ void add(const Sums& o) {
-        const float top = fmaxf(ref, o.ref);
-        Sums q = o;
-        move(top);
-        q.move(top);
-        s += q.s;
-        t += q.t;
-    }
     __device__ __forceinline__ void over_lanes() {
-        float top = ref;
+        double top;
+        if (__any(fabs(ref) >= kFar && ref != -INFINITY)) {
+            top = fmax(ref, __shfl_xor(ref, 1));
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+            for (int d = 2; d < 64; d *= 2) top = fmax(top, __shfl_xor(top, d));
+        } else {                                                 // (whole numbers that float32 holds)
+            top = value_of(lanes_reduce<OpMax, 64>(order_of(float(ref))));
+        }
         move(top);
         s = __uint_as_float(lanes_reduce<OpAdd, 64>(__float_as_uint(s)));
         t = __uint_as_float(lanes_reduce<OpAdd, 64>(__float_as_uint(t)));
@@ -221,10 +225,14 @@ __device__ __forceinline__ void first_keys(const uint64_t* keys, int n, int K, u
     order_keys(spare, at_or_above, K, out);
 }
 
+// Wavefronts a SIMD has room for. Float32 chunks of 1024 columns do not fit the registers of eight: 2000 rows of 100000 with
+// 20 alternatives 149 us, 193 with eight (600 rows of 128000 65.4 and 70.0).
+constexpr int waves_per_simd(int type, int J) { return type == WB_F32 && J == 2 ? 6 : 8; }
+
 // A wavefront takes chunks of 64 J vectors at a time. TOP: vectors of a group, whose maximum is kept: 8 (64 columns), 64 J
 // (a chunk), or 0: no alternatives are wanted.
 template <int T, int TOP, int J>
-__global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs A) {
+__global__ void __launch_bounds__(kThreads, waves_per_simd(T, J)) logprobs_kernel(const LogprobArgs A) {
     constexpr int kKeys = TOP ? kMaxKeys : 2;
     __shared__ __attribute__((aligned(16))) uint64_t keys[kKeys];
     __shared__ uint64_t first[TOP ? kMaxTop : 1];
@@ -233,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
     __shared__ int group_at[TOP ? kMaxTop : 1];
     __shared__ uint32_t bound;
     __shared__ int bins[TOP ? 256 : 1];
-    __shared__ float sums[kWaves][3];
+    __shared__ double refs[kWaves];
+    __shared__ float sums[kWaves][2];
     __shared__ int count, is_last;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -248,7 +257,10 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
     const int vectors = (A.V + x.off + 7) / 8, chunks = (vectors + 64 * J - 1) / (64 * J);
     const int c0 = int(int64_t(chunks) * segment / A.segments), c1 = int(int64_t(chunks) * (segment + 1) / A.segments);
 
-    Sums own;
+    // Of the lane, while it reads: s and t about 2^ref (ref a whole number, or -infinity: nothing yet) or, if the
+    // wavefront's references have come to kFar, about e^{scale ref}, where ref is a logit
+    float ref = -INFINITY, s = 0.f, t = 0.f;
+    bool far = false;
     uint32_t next[J][Row<T>::kWords];
     auto fetch = [&](int k) {                           // chunks that are all inside, ahead of their use
         if (k < c1 && x.inside(int64_t(64) * J * k, 64 * J))
@@ -274,16 +286,46 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
                 top = fmaxf(top, y[j][e]);
                 least = fminf(least, y[j][e]);
             }
-        if (top * c > own.ref) own.move(ceilf(top * c));
-        const float less = own.ref == -INFINITY ? 0.f : -own.ref;
+        // A whole-number reference is a rounded product, which the columns' exact ones pass by up to half of its last
+        // place: 2 below kFar, 2^7 and more from 2^31 on, past what the sums hold; and products end at 2^128. Past kFar
+        // differences are taken first, from the largest logit.
+        const float reach = top * c;
+        if (far || __any(!(fabsf(fmaxf(reach, ref)) < kFar))) {
+            const bool was = far;
+            const float up = was ? fmaxf(reach, ref * c) : fmaxf(reach, ref);
+            far = __any(!(fabsf(up) < kFar) && fmaxf(top, ref) > -INFINITY);      // (c x may be -infinity)
+            if (far != was) {
+                const float to = far ? fmaxf(top, ref * __builtin_amdgcn_rcpf(c)) : ceilf(up);
+                move_sums(s, t, far ? __builtin_fmaf(-to, c, ref) : __builtin_fmaf(ref, c, -to));      // (NaN: nothing yet)
+                ref = to;
+            }
+            if (far) {
+                if (top > ref) {
+                    move_sums(s, t, (ref - top) * c);
+                    ref = top;
+                }
+                const float base = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+                for (int j = 0; j < J; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[j][e] -= base;
+                least = -INFINITY;
+            }
+        }
+        if (!far && reach > ref) {
+            const float to = ceilf(reach);
+            move_sums(s, t, ref - to);
+            ref = to;
+        }
+        const float less = far || ref == -INFINITY ? 0.f : -ref;
         if (__any(!(__builtin_fmaf(least, c, less) > -256.f))) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float d = __builtin_fmaf(y[j][e], c, less), p = __builtin_amdgcn_exp2f(d);
-                    own.s += p;
-                    own.t = __builtin_fmaf(p, fmaxf(d, -256.f), own.t);     // (0 times -infinity is not 0)
+                    s += p;
+                    t = __builtin_fmaf(p, fmaxf(d, -256.f), t);     // (0 times -infinity is not 0)
                 }
         } else {
 #pragma unroll
@@ -291,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float d = __builtin_fmaf(y[j][e], c, less), p = __builtin_amdgcn_exp2f(d);
-                    own.s += p;
-                    own.t = __builtin_fmaf(p, d, own.t);
+                    s += p;
+                    t = __builtin_fmaf(p, d, t);
                 }
         }
         if constexpr (TOP) {
@@ -301,17 +343,18 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
             if (lane % kLanes == 0) maxima[group - c0 * kGroups] = best;
         }
     }
+    Sums own{far ? double(ref) * c : double(ref), s, t};
     own.over_lanes();
     if (lane == 0) {
-        sums[wave][0] = own.ref;
-        sums[wave][1] = own.s;
-        sums[wave][2] = own.t;
+        refs[wave] = own.ref;
+        sums[wave][0] = own.s;
+        sums[wave][1] = own.t;
     }
     if (tid == 0) count = 0;
     __syncthreads();
-    own = Sums{sums[0][0], sums[0][1], sums[0][2]};
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) own.add(Sums{sums[w][0], sums[w][1], sums[w][2]});
+    own = Sums{};
+    if (lane < kWaves) own = Sums{refs[lane], sums[lane][0], sums[lane][1]};
+    own.over_lanes();
 
     if constexpr (TOP) {
         const int K = A.K, n = (c1 - c0) * (64 * J / TOP), held = min(K, n);
@@ -385,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
         const int parts = A.segments, words = 2 + (TOP ? A.K : 0);
         uint64_t* part = A.parts + (local * parts + segment) * words;
         if (tid == 0) {
-            put_word(part, uint64_t(__float_as_uint(own.ref)) | uint64_t(__float_as_uint(own.s)) << 32);
-            put_word(part + 1, uint64_t(__float_as_uint(own.t)));
+            put_word(part, __builtin_bit_cast(uint64_t, own.ref));
+            put_word(part + 1, uint64_t(__float_as_uint(own.s)) | uint64_t(__float_as_uint(own.t)) << 32);
         }
         if constexpr (TOP)
             if (tid < A.K) put_word(part + 2 + tid, first[tid]);
@@ -398,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
         part = A.parts + local * parts * words;
         Sums all;
         if (lane < parts) {                       // (64 parts at most)
-            const uint64_t ms = get_word(part + lane * words), tt = get_word(part + lane * words + 1);
-            all = Sums{__uint_as_float(uint32_t(ms)), __uint_as_float(uint32_t(ms >> 32)), __uint_as_float(uint32_t(tt))};
+            const uint64_t r = get_word(part + lane * words), st = get_word(part + lane * words + 1);
+            all = Sums{__builtin_bit_cast(double, r), __uint_as_float(uint32_t(st)), __uint_as_float(uint32_t(st >> 32))};
         }
         all.over_lanes();
         own = all;
@@ -423,11 +466,10 @@ __global__ void __launch_bounds__(kThreads, 8) logprobs_kernel(const LogprobArgs
         }
     }
 
-    // c x - ref - log2 s, in powers of two (a logit whose c x leaves float32's range: by itself)
+    // c x - ref - log2 s, in powers of two
     const float log_s = log2f(own.s);
     auto logprob_of = [&](float value) {
-        const float d = __builtin_fmaf(value, c, own.ref == -INFINITY ? 0.f : -own.ref) - log_s;
-        return fabsf(d) == INFINITY && fabsf(value) < INFINITY ? value * A.scale : d * kLn2;
+        return float((__builtin_fma(double(value), double(c), -own.ref) - log_s) * 0.6931471805599453);
     };
     if (tid == 0) {
         const int64_t token = A.wide ? static_cast<const int64_t*>(A.tokens)[row] : static_cast<const int32_t*>(A.tokens)[row];
