@@ -17,7 +17,8 @@
 // rounding of o itself, and averaged over tokens; a second limb would add half as many products again (the float16 query
 // over an 8-bit cache, which has two bfloat16 limbs, pays 13 %: 855 us against 757). Float16 weights are 2^11 of themselves
 // (kShift; at most 2^15 with the lazy reference): what falls below its smallest step is 2^-36 of the largest. The sum of
-// weights is taken in float32 of the weights before they are rounded.
+// weights is taken in float32 of the weights before they are rounded, each tile's by itself, the tiles' with what their
+// roundings leave.
 //
 // Prompts are bound by the matrix units at the power limit (8192 tokens, 32 / 8 heads of 128, bfloat16: 541 to 580 us,
 // 0.95 to 1.02 PFLOP/s, clocks at 1.8 to 2.05 GHz; the same call over zeros 485 us; a large library product 1.16 to 1.23
@@ -290,6 +291,10 @@ struct Chunk {
     static constexpr int kTile = 1 << tile_log2(D);
     static constexpr int NB = kTile / 32, TB = kTile / 8;            // its blocks of 32 tokens, of 8
     static constexpr int kTileBytes = kTile * D * 2;
+    // A lane's sum of weights in LDS, where its two registers are one too many: 8-bit caches, 8192 tokens of bfloat16 and
+    // float16 queries, heads of 64 402 and 514 us (496 and 606 in registers, with two wavefronts a SIMD in place of three),
+    // of 256 892 and 951 (956 and 1016, more of them spilled); heads of 128 and 16-bit caches are as fast or faster in registers
+    static constexpr bool kSumsInLds = KV == WB_E4M3 && D != 128;
 };
 
 // The kernel's arguments, read again here: held from its start, or through its loop, they would cost registers there
@@ -355,7 +360,14 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
     f32x16 acc[DB];
 #pragma unroll
     for (int i = 0; i < DB; ++i) acc[i] = f32x16{};
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY;
+    __shared__ f32x2 lds_sums[T::kSumsInLds ? kThreads : 1];
+    f32x2 register_sums;
+    auto weights = [&]() -> f32x2& {                          // their sum, in two parts
+        if constexpr (T::kSumsInLds) return lds_sums[tid];
+        else return register_sums;
+    };
+    weights() = f32x2{0.f, 0.f};
 
     // ------------------------------------------------------------------ staging
     // A tile lies in LDS as blocks of 8 tokens by 64 columns, 1 KB each, block (c, g) at 1024 (8 c + g): keys a row of
@@ -524,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
         if (__any((top - m) * mul > kThreshold)) {
             const float m_new = fmaxf(m, top);
             const float keep = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - m_new) * mul);
-            l *= keep;
+            weights() *= keep;
 #pragma unroll
             for (int db = 0; db < DB; ++db) acc[db] *= keep;
             m = m_new;
@@ -541,16 +553,15 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
             ref = -T::kShift;
         }
         u32x4 p[2 * NB], p2[T::kTwoP ? 2 * NB : 1];
+        float tile_l = 0.f;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 float e[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][4 * g + k], mul, -ref));
-                    l += e[k];
-                }
+                for (int k = 0; k < 4; ++k) e[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][4 * g + k], mul, -ref));
+                tile_l += (e[0] + e[1]) + (e[2] + e[3]);
                 if constexpr (E) {
                     const f32x4 vs = scales[buf][1][8 * b + 2 * g + h];
 #pragma unroll
@@ -574,6 +585,13 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
                     y[2 * (g & 1) + 1] = pack2<T::VT>(e[2] - low<T::VT>(h1), e[3] - high<T::VT>(h1));
                 }
             }
+        {
+            // The sum and what its rounding leaves (TwoSum: Knuth, The Art of Computer Programming 2, 4.2.2): one rounding
+            // after the other would take 9e-4 off a row of 131072 equal weights, all on one side
+            const f32x2 l = weights();
+            const float sum = l[0] + tile_l, added = sum - l[0];
+            weights() = f32x2{sum, l[1] + ((l[0] - (sum - added)) + (tile_l - added))};
+        }
         const uint8_t* values = &stored[buf][1][value_at];
 #pragma unroll
         for (int db = 0; db < DB; ++db)
@@ -617,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
 
     // ------------------------------------------------------------------ sums out
     const auto& B = arguments_again();
-    l = w.q.bad || bad_page ? __builtin_nanf("") : add_xor32_f32(l);
+    const float l = w.q.bad || bad_page ? __builtin_nanf("") : add_xor32_f32(weights()[0] + weights()[1]);
     const int j = wave * 32 + col, token = j / B.heads, head = j - token * B.heads;
     if (token >= tokens || head >= min(B.heads, B.G - w.hb * B.heads)) return;
     if (w.parts == 1) {
