@@ -140,7 +140,7 @@ int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes
  * that a row does not see leave no trace in it, whatever they hold; a NaN that it sees gives NaN,
  * an infinity what the formula gives or NaN. A request with a length outside [m, width * page] has
  * o = lse = NaN, and so has a row that sees a token of a page id outside [0, pages) (other rows of
- * its request may). A request whose starts decrease or leave [0, N] has no rows; rows of no
+ * its request may); entries of pages that no row sees (before a window) may hold anything. A request whose starts decrease or leave [0, N] has no rows; rows of no
  * request are left as they were. Equal calls give equal bits.
  * q [N][Hq][D] of type q_dtype (the cache's, or WB_BF16 / WB_F16 for an 8-bit cache), strides
  * q_row and q_head in elements, multiples of 8; o [N][Hq][D] contiguous, of q's type; q and o

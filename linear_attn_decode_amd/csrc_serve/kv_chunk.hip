@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
     const uint8_t* const k0 = static_cast<const uint8_t*>(C.c.k) + (size_t(w.kvh) << log2) * kRowBytes;
     const uint8_t* const v0 = static_cast<const uint8_t*>(C.c.v) + (size_t(w.kvh) << log2) * kRowBytes;
     auto token_of = [&](int t, int j) { return uint32_t(min(t * kTile + 8 * NB * wave + 8 * j, last)); };
+    const uint32_t first_seen = C.window ? uint32_t(max(past + t0 + 1 - C.window, 0)) : 0u;
     uint32_t ids[NB], bad = 0;
     auto load_ids = [&](int t) {
 #pragma unroll
@@ -399,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const uint32_t id = ids[j] < pages ? ids[j] : 0u;
-            bad |= id ^ ids[j];                                  // (not 0 for an id outside the cache)
+            // (not 0 for an id outside the cache; the tokens before the block's first window may be in no page)
+            bad |= token_of(t, j) + 8 > first_seen ? id ^ ids[j] : 0u;
             const uint64_t at = (uint64_t(id) * page_rows + (token_of(t, j) & ((1u << log2) - 1))) * kRowBytes;
             const uint8_t* k = k0 + at;
             const uint8_t* v = v0 + at;

@@ -352,7 +352,8 @@ def kv_attend_chunk(q, k_cache, v_cache, table, lens, starts, o, scale=None, win
     log-sum-exp of the scores. ``starts`` (int32 [R + 1]) and ``lens`` (int32 [R]) are what ``plan_pages``
     gives; the new tokens have been stored by ``kv_append``. Types, strides and alignment of ``q``,
     ``table`` and the cache, and ``scale``, as for ``kv_attend``. Rows of no request are left as they were;
-    a request whose length is out of range, or rows that see a page id out of range, have NaN.
+    a request whose length is out of range, or rows that see a page id out of range, have NaN (pages that
+    no row sees, before a window, may have been given back).
     Outputs overlap no input."""
     c, dev, shape, code = _cache(k_cache, v_cache, k_scale, v_scale)
     kind = q.dtype
