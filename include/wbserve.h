@@ -35,6 +35,8 @@ extern "C" {
 #define WB_F16 1
 #define WB_F32 2
 #define WB_E4M3 3
+/* added to kv_attend_chunk's q_dtype: weights as two 16-bit values */
+#define WB_TWO_LIMBS 256
 
 /* A key-value cache in caller-owned device memory, 16-byte aligned. D is 64, 128 or 256;
  * page a power of two from 8 to 4096; dtype WB_BF16, WB_F16 or WB_E4M3 (then k_scale and
@@ -134,8 +136,11 @@ int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes
  *   lse[row][h] = log sum_t e^{s_t} (float32 [N][Hq], or NULL).
  * Scores, maxima and sums are float32. The weights e^{s_t - ref} (ref within 4 / log2(e) of the
  * running maximum; times the value's scale, for an 8-bit cache) enter the product with v rounded
- * to 16 bits of the cache's type (within 2^-8 of each weight in bfloat16, 2^-11 and 2^-36 of the
- * largest in float16), for a float16 q over an 8-bit cache as two bfloat16 limbs (2^-16); o is
+ * to 16 bits of the cache's type (bfloat16 for an 8-bit one): within 2^-8 of each weight in bfloat16,
+ * 2^-11 and 2^-36 of the largest in float16, which is as large an error of o as its own rounding. With
+ * WB_TWO_LIMBS added to q_dtype, and always for a float16 q over an 8-bit cache, they enter as two
+ * limbs of that type (2^-16; 2^-21 and 2^-36 of the largest in float16), as those of kv_attend do, in a
+ * third more time where products bound the call (prompts; a few percent more for drafted tokens). o is
  * rounded once. A row whose scores are all -infinity has o = 0 and lse = -infinity. Stored values
  * that a row does not see leave no trace in it, whatever they hold; a NaN that it sees gives NaN,
  * an infinity what the formula gives or NaN. A request with a length outside [m, width * page] has

@@ -13,9 +13,11 @@
 // leave registers, and the accumulators hold a row in a lane, so that its rescaling is one factor.
 // The weights' reference moves only when a row's maximum has risen by more than 2^4 (kThreshold): 2^4 is far from the end
 // of either type, and all tiles but a row's first few then go without rescaling the accumulators.
-// Weights enter the second product as one value of 16 bits: within half a step of each, 2^-8 in bfloat16, as large as the
-// rounding of o itself, and averaged over tokens; a second limb would add half as many products again (the float16 query
-// over an 8-bit cache, which has two bfloat16 limbs, pays 13 %: 855 us against 757). Float16 weights are 2^11 of themselves
+// Weights enter the second product as one value of 16 bits, within half a step of each, 2^-8 in bfloat16: the error of o is
+// then 1.1 to 1.45 times that of its own rounding. The caller may have a second limb (2^-16, and no more than the rounding's
+// error), which adds half as many products again: 8192-token prompts of heads of 128 in bfloat16 733 us and 552, 8-bit 845
+// and 683, drafts 97 and 93. A float16 query over an 8-bit cache always has two: bfloat16, which holds the values' scales,
+// keeps 3 bits fewer than its output. Float16 weights are 2^11 of themselves
 // (kShift; at most 2^15 with the lazy reference): what falls below its smallest step is 2^-36 of the largest. The sum of
 // weights is taken in float32 of the weights before they are rounded, each tile's by itself, the tiles' with what their
 // roundings leave.
@@ -278,12 +280,12 @@ __device__ __forceinline__ u32x2 scaled(f32x4 v, float by) {
 constexpr int kWavesPerSimd = 2;
 constexpr int tile_log2(int D) { return D <= 128 ? 6 : 5; }
 
-// KV: the cache's type; QT: the type of q and o; D: columns
-template <int KV, int QT, int D>
+// KV: the cache's type; QT: the type of q and o; D: columns; LIMBS: 16-bit values of a weight
+template <int KV, int QT, int D, int LIMBS>
 struct Chunk {
     static constexpr int ST = QT;                                    // operands of the scores
     static constexpr int VT = KV == WB_E4M3 ? WB_BF16 : KV;          // of the values
-    static constexpr bool kTwoP = KV == WB_E4M3 && QT == WB_F16;
+    static constexpr bool kTwoP = LIMBS == 2;
     static constexpr int KS = D / 16;                                // score products of 32 tokens
     static constexpr int DB = D / 32;                                // blocks of value columns
     static constexpr int CB = D / 64;                                // blocks of 64 columns
@@ -304,9 +306,9 @@ __device__ __forceinline__ const __attribute__((address_space(4))) ChunkArgs& ar
     return *p;
 }
 
-template <int KV, int QT, int D>
+template <int KV, int QT, int D, int LIMBS>
 __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const ChunkArgs A) {
-    using T = Chunk<KV, QT, D>;
+    using T = Chunk<KV, QT, D, LIMBS>;
     using S = Mat32<T::ST>;
     using V = Mat32<T::VT>;
     constexpr int KS = T::KS, DB = T::DB, CB = T::CB, kTile = T::kTile, NB = T::NB, TB = T::TB;
@@ -729,26 +731,31 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
     }
 }
 
-template <int KV, int QT, int D>
+template <int KV, int QT, int D, int LIMBS>
 hipError_t chunk_d(ChunkArgs a, hipStream_t s) {
     constexpr int64_t most = kLaunchItems / kThreads;
     for (; a.launched < a.groups; a.launched += most) {
         const int64_t groups = a.groups - a.launched < most ? a.groups - a.launched : most;
-        chunk_kernel<KV, QT, D><<<unsigned(groups), kThreads, 0, s>>>(a);
+        chunk_kernel<KV, QT, D, LIMBS><<<unsigned(groups), kThreads, 0, s>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (!a.slots) return hipSuccess;
-    join_chunks_kernel<QT, D, Chunk<KV, QT, D>::kShift><<<unsigned(a.slots), kThreads, 0, s>>>(a);
+    join_chunks_kernel<QT, D, Chunk<KV, QT, D, LIMBS>::kShift><<<unsigned(a.slots), kThreads, 0, s>>>(a);
     return hipGetLastError();
+}
+template <int KV, int QT, int LIMBS>
+hipError_t chunk_l(const ChunkArgs& a, hipStream_t s) {
+    switch (a.c.D) {
+        case 64: return chunk_d<KV, QT, 64, LIMBS>(a, s);
+        case 128: return chunk_d<KV, QT, 128, LIMBS>(a, s);
+        default: return chunk_d<KV, QT, 256, LIMBS>(a, s);
+    }
 }
 template <int KV, int QT>
 hipError_t chunk_t(const ChunkArgs& a, hipStream_t s) {
-    switch (a.c.D) {
-        case 64: return chunk_d<KV, QT, 64>(a, s);
-        case 128: return chunk_d<KV, QT, 128>(a, s);
-        default: return chunk_d<KV, QT, 256>(a, s);
-    }
+    if constexpr (KV == WB_E4M3 && QT == WB_F16) return chunk_l<KV, QT, 2>(a, s);
+    else return a.limbs == 2 ? chunk_l<KV, QT, 2>(a, s) : chunk_l<KV, QT, 1>(a, s);
 }
 
 }  // namespace
