@@ -6,7 +6,9 @@
 // an exponential a column). A workgroup takes a row, or, where rows are few, a segment of one; a lane
 // takes vectors of 8 columns and keeps, of d = x log2 e - ref with a whole number ref from the running
 // maximum up (or, where that is 2^26 and more, d = (x - maximum) log2 e), s = sum 2^d and t = sum 2^d d. An
-// exponent is rounded once, relative to itself, a change of ref is an exact factor, and the entropy is log s - t / s without cancellation.
+// exponent is rounded once, relative to itself, a change of ref is an exact factor, and the entropy is
+// log s - t / s. Where one token has nearly all the probability both are about its d, in (-1, 0], and what
+// is left of their difference is within 1e-7 or so of a small entropy: less than 0 is returned as 0.
 // The top K need no second pass over the row: the stream leaves the maximum of every group of 64, 512 or
 // 1024 columns in LDS. K groups by (maximum, then position) hold all of the top K, for any column of
 // another group is behind the maxima of K that are larger, or as large and before it. Those groups are
@@ -469,12 +471,14 @@ __global__ void __launch_bounds__(kThreads, waves_per_simd(T, J)) logprobs_kerne
     // c x - ref - log2 s, in powers of two
     const float log_s = log2f(own.s);
     auto logprob_of = [&](float value) {
-        return float((__builtin_fma(double(value), double(c), -own.ref) - log_s) * 0.6931471805599453);
+        const float lp = float((__builtin_fma(double(value), double(c), -own.ref) - log_s) * 0.6931471805599453);
+        return lp > 0.f ? 0.f : lp;                   // (s is rounded; a NaN stays)
     };
     if (tid == 0) {
         const int64_t token = A.wide ? static_cast<const int64_t*>(A.tokens)[row] : static_cast<const int32_t*>(A.tokens)[row];
         A.logprob[row] = token >= 0 && token < A.V ? logprob_of(x.one(token)) : __builtin_nanf("");
-        if (A.entropy) A.entropy[row] = (log_s - own.t / own.s) * kLn2;
+        const float entropy = (log_s - own.t / own.s) * kLn2;
+        if (A.entropy) A.entropy[row] = entropy < 0.f ? 0.f : entropy;
     }
     if constexpr (TOP)
         if (tid < A.K) {
