@@ -145,8 +145,10 @@ int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes
  * that a row does not see leave no trace in it, whatever they hold; a NaN that it sees gives NaN,
  * an infinity what the formula gives or NaN. A request with a length outside [m, width * page] has
  * o = lse = NaN, and so has a row that sees a token of a page id outside [0, pages) (other rows of
- * its request may); entries of pages that no row sees (before a window) may hold anything. A request whose starts decrease or leave [0, N] has no rows; rows of no
- * request are left as they were. Equal calls give equal bits.
+ * its request may); entries of pages that no row sees (before a window) may hold anything. A request
+ * whose starts decrease or leave [0, N] has no rows; rows of no request are left as they were. (Where
+ * starts decrease, later requests may have rows of earlier ones as well: those hold the result of one of
+ * them, or are left.) Other than that equal calls give equal bits.
  * q [N][Hq][D] of type q_dtype (the cache's, or WB_BF16 / WB_F16 for an 8-bit cache), strides
  * q_row and q_head in elements, multiples of 8; o [N][Hq][D] contiguous, of q's type; q and o
  * 16-byte aligned; table int32 [R][width]; lens int32 [R]; starts int32 [R + 1]. `work` has
@@ -191,8 +193,8 @@ int qk_rotate(const wb_heads* q, const wb_heads* k, int dtype, int N, int D, con
  *   top_ids, top_logprobs [N][K]: the K largest logits' columns and their log probabilities, larger logits
  *   first, equal ones by their column; NaN counts as -infinity in this order (K 0: not wanted).
  * Sums are float32, of differences from the largest logit, so that scale x may be of any size (log probabilities
- * past float32's range are -infinity); no log probability is above 0, no entropy below. A token outside [0, V) (padding) has logprob NaN; logits of -infinity have p = 0; a
- * row that holds a NaN or +infinity, or nothing but -infinity, has NaN in place of its log probabilities and
+ * past float32's range are -infinity); no log probability is above 0, no entropy below. A token outside [0, V)
+ * (padding) has logprob NaN; logits of -infinity have p = 0; a row that holds a NaN or +infinity, or nothing but -infinity, has NaN in place of its log probabilities and
  * entropy. tokens: int32 [N], or int64 with tokens64. logprob, entropy: float32 [N]; top_ids int32,
  * top_logprobs float32. 1 <= V <= 2^24 (2^24 - 8 with K > 32), K <= 64 and V, 2^-100 <= scale <= 2^100 (1 / temperature), N >= 0.
  * `work` as for kv_attend, of token_logprobs_work() bytes. Equal calls give equal bits. No output overlaps an input. */
