@@ -38,7 +38,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kRows = 32 * kWaves;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------------------- where a workgroup works
 // A request: its new tokens (rows first ..+m of q), stored tokens n; span: key tiles of a
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
                 *reinterpret_cast<u32x2*>(o + 32 * db + 8 * g) =
                     scaled<QT>(f32x4{acc[db][4 * g], acc[db][4 * g + 1], acc[db][4 * g + 2], acc[db][4 * g + 3]}, by);
         if (B.lse && h == 0)
-            B.lse[row] = l == 0.f ? -INFINITY : m * (B.scale == 0.f ? 1.f : fabsf(B.scale)) + (logf(l) - T::kShift * kLn2);
+            B.lse[row] = l == 0.f ? -INFINITY : m * (B.scale == 0.f ? 1.f : fabsf(B.scale)) + logf(l * (1.f / (1 << T::kShift)));
     } else {
         const size_t at = size_t(w.slot) * kRows + j;
         float* o = B.part_o + at * D + 4 * h;
@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A
         const size_t row = (size_t(w.q.first) + w.block * A.tokens + token) * A.Hq + w.kvh * A.G + w.hb * A.heads + head;
         const float by = l == 0.f ? 0.f : 1.f / l;
         *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(A.o) + row * D + d) = scaled<QT>(v, by);
-        if (A.lse && d == 0) A.lse[row] = l == 0.f ? -INFINITY : m * natural + (logf(l) - SHIFT * kLn2);
+        if (A.lse && d == 0) A.lse[row] = l == 0.f ? -INFINITY : m * natural + logf(l * (1.f / (1 << SHIFT)));
     }
 }
 
