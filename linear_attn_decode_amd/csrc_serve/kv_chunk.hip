@@ -639,9 +639,19 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
 
     // ------------------------------------------------------------------ sums out
     const auto& B = arguments_again();
-    const float l = w.q.bad || bad_page ? __builtin_nanf("") : add_xor32_f32(weights()[0] + weights()[1]);
+    float l = w.q.bad || bad_page ? __builtin_nanf("") : add_xor32_f32(weights()[0] + weights()[1]);
     const int j = wave * 32 + col, token = j / B.heads, head = j - token * B.heads;
     if (token >= tokens || head >= min(B.heads, B.G - w.hb * B.heads)) return;
+    if (B.scale == 0.f) {                                    // (0 times an infinity or a NaN is a NaN)
+        const uint16_t* q = static_cast<const uint16_t*>(B.q) + (int64_t(w.q.first) + t0 + token) * B.q_row +
+                            int64_t(w.kvh * B.G + w.hb * B.heads + head) * B.q_head + 8 * h;
+        uint32_t any = 0;
+        for (int i = 0; i < KS; ++i) {
+            const u32x4 x = *reinterpret_cast<const u32x4*>(q + 16 * i);
+            any |= not_finite<QT>(x[0]) | not_finite<QT>(x[1]) | not_finite<QT>(x[2]) | not_finite<QT>(x[3]);
+        }
+        if (any | __shfl_xor(any, 32)) l = __builtin_nanf("");
+    }
     if (w.parts == 1) {
         const size_t row = (size_t(w.q.first) + t0 + token) * B.Hq + w.kvh * B.G + w.hb * B.heads + head;
         const float by = l == 0.f ? 0.f : 1.f / l;
