@@ -35,8 +35,8 @@ extern "C" {
 #define WB_F16 1
 #define WB_F32 2
 #define WB_E4M3 3
-/* added to kv_attend_chunk's q_dtype: weights as two 16-bit values */
-#define WB_TWO_LIMBS 256
+/* added to kv_attend_chunk's q_dtype: weights as one 16-bit value, not two */
+#define WB_ONE_LIMB 256
 
 /* A key-value cache in caller-owned device memory, 16-byte aligned. D is 64, 128 or 256;
  * page a power of two from 8 to 4096; dtype WB_BF16, WB_F16 or WB_E4M3 (then k_scale and
@@ -135,12 +135,11 @@ int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes
  *   s_t = scale * q[row][h] . k_t,  o[row][h] = sum_t e^{s_t} v_t / sum_t e^{s_t},
  *   lse[row][h] = log sum_t e^{s_t} (float32 [N][Hq], or NULL).
  * Scores, maxima and sums are float32. The weights e^{s_t - ref} (ref within 4 / log2(e) of the
- * running maximum; times the value's scale, for an 8-bit cache) enter the product with v rounded
- * to 16 bits of the cache's type (bfloat16 for an 8-bit one): within 2^-8 of each weight in bfloat16,
- * 2^-11 and 2^-36 of the largest in float16, which is as large an error of o as its own rounding. With
- * WB_TWO_LIMBS added to q_dtype, and always for a float16 q over an 8-bit cache, they enter as two
- * limbs of that type (2^-16; 2^-21 and 2^-36 of the largest in float16), as those of kv_attend do, in a
- * third more time where products bound the call (prompts; a few percent more for drafted tokens). o is
+ * running maximum; times the value's scale, for an 8-bit cache) enter the product with v as two 16-bit
+ * limbs of the cache's type (bfloat16 for an 8-bit one): within 2^-16 of each weight in bfloat16, 2^-21
+ * and 2^-36 of the largest in float16. With WB_ONE_LIMB added to q_dtype they enter as one (2^-8; 2^-11
+ * and 2^-36 of the largest), but for a float16 q over an 8-bit cache: o then has an error of weights
+ * as large as that of its own rounding, and prompts take a quarter less time (drafted tokens 4 %). o is
  * rounded once. A row whose scores are all -infinity has o = 0 and lse = -infinity. Stored values
  * that a row does not see leave no trace in it, whatever they hold; a NaN that it sees gives NaN,
  * an infinity what the formula gives or NaN. A request with a length outside [m, width * page] has

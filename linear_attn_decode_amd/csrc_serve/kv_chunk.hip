@@ -13,11 +13,11 @@
 // leave registers, and the accumulators hold a row in a lane, so that its rescaling is one factor.
 // The weights' reference moves only when a row's maximum has risen by more than 2^4 (kThreshold): 2^4 is far from the end
 // of either type, and all tiles but a row's first few then go without rescaling the accumulators.
-// Weights enter the second product as one value of 16 bits, within half a step of each, 2^-8 in bfloat16: the error of o is
-// then 1.1 to 1.45 times that of its own rounding. The caller may have a second limb (2^-16, and no more than the rounding's
-// error), which adds half as many products again: 8192-token prompts of heads of 128 in bfloat16 733 us and 552, 8-bit 845
-// and 683, drafts 97 and 93. A float16 query over an 8-bit cache always has two: bfloat16, which holds the values' scales,
-// keeps 3 bits fewer than its output. Float16 weights are 2^11 of themselves
+// Weights enter the second product as two limbs of 16 bits (2^-16 of each in bfloat16), so that the error of o is that of
+// its own rounding. They are half of the value products, a third of the time of prompts: the caller may have one limb
+// (half a step of each weight, 2^-8 in bfloat16: 1.1 to 1.45 times the error) and 8192-token prompts of heads of 128 in 552
+// us, not 733, 8-bit ones in 683, not 845, drafts in 93, not 97. A float16 query over an 8-bit cache always has two:
+// bfloat16, which holds the values' scales, keeps 3 bits fewer than its output. Float16 weights are 2^11 of themselves
 // (kShift; at most 2^15 with the lazy reference): what falls below its smallest step is 2^-36 of the largest. The sum of
 // weights is taken in float32 of the weights before they are rounded, each tile's by itself, the tiles' with what their
 // roundings leave.
@@ -765,7 +765,7 @@ hipError_t chunk_l(const ChunkArgs& a, hipStream_t s) {
 template <int KV, int QT>
 hipError_t chunk_t(const ChunkArgs& a, hipStream_t s) {
     if constexpr (KV == WB_E4M3 && QT == WB_F16) return chunk_l<KV, QT, 2>(a, s);
-    else return a.limbs == 2 ? chunk_l<KV, QT, 2>(a, s) : chunk_l<KV, QT, 1>(a, s);
+    else return a.limbs == 1 ? chunk_l<KV, QT, 1>(a, s) : chunk_l<KV, QT, 2>(a, s);
 }
 
 }  // namespace

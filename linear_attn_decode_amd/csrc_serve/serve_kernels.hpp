@@ -97,7 +97,7 @@ struct ChunkArgs {
     int G = 1;                    // query heads of a key-value head
     int heads = 1, tokens = 1;    // of a block of rows: query heads of new tokens
     int head_blocks = 1;          // blocks of a key-value head's query heads
-    int limbs = 1;                // 16-bit values that a weight enters the second product as
+    int limbs = 2;                // 16-bit values that a weight enters the second product as
     int tile_log2 = 6;            // of the tokens of a key tile
     int part_tiles = 1;           // key tiles of a part at least
     int target = 1;               // parts that all tiles are cut into, about

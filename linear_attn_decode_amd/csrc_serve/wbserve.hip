@@ -256,8 +256,8 @@ int kv_attend_chunk(const wb_kv_cache* c, const void* q, int64_t q_row, int64_t 
     const int v = check_chunk(c, N, R, Hq, width);
     if (v) return v;
     if (window < 0) return WB_EINVAL;
-    const int limbs = q_dtype >= 0 && (q_dtype & WB_TWO_LIMBS) ? 2 : 1;
-    if (limbs == 2) q_dtype ^= WB_TWO_LIMBS;
+    const int limbs = q_dtype >= 0 && (q_dtype & WB_ONE_LIMB) ? 1 : 2;
+    if (limbs == 1) q_dtype ^= WB_ONE_LIMB;
     if (q_dtype != WB_BF16 && q_dtype != WB_F16) return WB_EINVAL;
     if (c->dtype != WB_E4M3 && q_dtype != c->dtype) return WB_EUNSUPPORTED;
     if (N == 0) return WB_OK;

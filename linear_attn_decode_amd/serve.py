@@ -56,7 +56,7 @@ SERVE_SIGNATURES = {
 
 # element types (values of include/wbserve.h)
 BF16, F16, F32, E4M3 = 0, 1, 2, 3
-TWO_LIMBS = 256
+ONE_LIMB = 256
 
 # Set by _load() at the first call. The small calls here are bound by the host (a launch is
 # 3.5 us of the 7 us a call of one kernel takes), so checks are plain attribute reads, the
@@ -345,7 +345,7 @@ def kv_attend(q, k_cache, v_cache, table, lens, o, scale=None, window: int = 0, 
 
 
 def kv_attend_chunk(q, k_cache, v_cache, table, lens, starts, o, scale=None, window: int = 0, lse=None, k_scale=None,
-                    v_scale=None, stream=None, limbs: int = 1):
+                    v_scale=None, stream=None, limbs: int = 2):
     """Attention of chunks of new tokens (prompts, parts of them, drafted tokens, single tokens) over
     the stored ones, which they are the last of: rows ``starts[r]`` .. ``starts[r + 1] - 1`` of ``q``
     [N, Hq, D] are request r's, and each sees the stored tokens up to its own (the last ``window`` of
@@ -355,9 +355,9 @@ def kv_attend_chunk(q, k_cache, v_cache, table, lens, starts, o, scale=None, win
     ``table`` and the cache, and ``scale``, as for ``kv_attend``. Rows of no request are left as they were;
     a request whose length is out of range, or rows that see a page id out of range, have NaN (pages that
     no row sees, before a window, may have been given back). ``limbs``: the 16-bit values that a weight enters
-    the product with the values as: 1 (rounded as ``o`` is, by half a step of bfloat16 or float16) or 2 (2^-16 and
-    less of it, as ``kv_attend`` has them; a third more time for prompts; always 2 for a float16 ``q`` over a
-    float8_e4m3fn cache). Outputs overlap no input."""
+    the product with the values as: 2 (within 2^-16 of it, much as ``kv_attend`` has them) or 1 (rounded as ``o`` is, by half
+    a step of bfloat16 or float16; a quarter less time for prompts; a float16 ``q`` over a float8_e4m3fn cache has 2 all
+    the same). Outputs overlap no input."""
     c, dev, shape, code = _cache(k_cache, v_cache, k_scale, v_scale)
     kind = q.dtype
     if q.dim() != 3 or table.dim() != 2 or kind not in _codes:
@@ -385,7 +385,7 @@ def kv_attend_chunk(q, k_cache, v_cache, table, lens, starts, o, scale=None, win
     n = _chunk_work(code, pages, H, page, D, N, R, Hq, width)
     held = _workspace(n, _torch.uint8, dev, stream) if n else None
     _call("kv_attend_chunk", dev, c, q.data_ptr(), q_row if N > 1 else 0, q_head if Hq > 1 else 0,
-          _codes[kind] if limbs == 1 else _codes[kind] | TWO_LIMBS, N, R, Hq,
+          _codes[kind] if limbs == 2 else _codes[kind] | ONE_LIMB, N, R, Hq,
           table.data_ptr(), width, lens.data_ptr(), starts.data_ptr(), D ** -0.5 if scale is None else scale,
           window if window < _MAX else 0, o.data_ptr(), lsep, held.data_ptr() if n else None, n, _stream_of(dev, stream))
 

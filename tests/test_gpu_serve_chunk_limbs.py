@@ -1,8 +1,8 @@
-"""kv_attend_chunk with weights as two 16-bit limbs (include/wbserve.h: WB_TWO_LIMBS; the binding's limbs=2).
+"""kv_attend_chunk with weights as two 16-bit limbs and as one (include/wbserve.h: WB_ONE_LIMB; the binding's limbs).
 
 Bounds as in tests/test_gpu_serve_chunk.py, with the rounding r of a weight by its two limbs: 2^-16 in bfloat16 (half a step
 of half a step, 2^-8 each), 2^-21 in float16 (2^-22, and 2^-36 of the largest weight where the second limb is below the
-normal numbers)."""
+normal numbers); by one: 2^-8 and 2^-11."""
 import math
 
 import numpy as np
@@ -52,6 +52,8 @@ def run(kv, qt, D, H, G, news, pasts, page, window=0, seed=0, limbs=2):
         A = max(1.0, size.max())
         e_s, sums = (D + 8) * U * A + 2.0 ** -22 * A, (96 + n / 16) * U
         weight = 2.0 ** -21 if kv == "f16" else 2.0 ** -16
+        if limbs == 1 and (kv, qt) != ("e4m3", "f16"):
+            weight = 2.0 ** -11 if kv == "f16" else 2.0 ** -8
         tol = half * np.abs(ro) + W * (2 * e_s + weight + 2 * sums) * (1 + half) + (2.0 ** -25 if qt == "f16" else 2.0 ** -40)
         if kv == "f16":
             tol += n * 2.0 ** -36 * np.abs(v64).max()
@@ -66,15 +68,29 @@ def run(kv, qt, D, H, G, news, pasts, page, window=0, seed=0, limbs=2):
 
 @pytest.mark.parametrize("kv,qt", KINDS)
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_types_and_widths(kv, qt, D):
-    run(kv, qt, D, 2, 4, NEWS, PASTS, 16, seed=D)
-    run(kv, qt, D, 1, 5, [100, 1, 300], [700, 3, 0], 32, window=77, seed=D + 1)
+@pytest.mark.parametrize("limbs", [2, 1])
+def test_types_and_widths(kv, qt, D, limbs):
+    run(kv, qt, D, 2, 4, NEWS, PASTS, 16, seed=D, limbs=limbs)
+    run(kv, qt, D, 1, 5, [100, 1, 300], [700, 3, 0], 32, window=77, seed=D + 1, limbs=limbs)
 
 
 @pytest.mark.parametrize("kv,qt", KINDS)
 @pytest.mark.parametrize("D", [64, 128, 256])
-def test_long_caches_are_split_and_joined(kv, qt, D):
-    run(kv, qt, D, 1, 4, [7, 1], [9000, 4000], 64, seed=3)
+@pytest.mark.parametrize("limbs", [2, 1])
+def test_long_caches_are_split_and_joined(kv, qt, D, limbs):
+    run(kv, qt, D, 1, 4, [7, 1], [9000, 4000], 64, seed=3, limbs=limbs)
+
+
+@pytest.mark.parametrize("kv,qt", KINDS)
+def test_two_limbs_unless_one_is_asked_for(kv, qt):
+    import linear_attn_decode_amd as wb
+    q, k, ks, v, vs, table, lens, starts = problem(kv, qt, 64, 1, 2, [40], [300], 16, 1)
+    outs = [torch.empty_like(q) for _ in range(3)]
+    for o, kw in zip(outs, ({}, dict(limbs=2), dict(limbs=1))):
+        wb.kv_attend_chunk(q, k, v, i32(table), i32(lens), i32(starts), o, k_scale=ks, v_scale=vs, **kw)
+    torch.cuda.synchronize()
+    same = [torch.equal(outs[0].view(torch.int16), o.view(torch.int16)) for o in outs]
+    assert same[1] and same[2] == ((kv, qt) == ("e4m3", "f16"))
 
 
 def test_many_requests():
@@ -132,7 +148,8 @@ def test_two_limbs_are_as_close_as_kv_attend(kv):
 
 @pytest.mark.parametrize("kv", ["bf16", "f16", "e4m3"])
 @pytest.mark.parametrize("D", [64, 256])
-def test_hidden_infinities_leave_no_trace(kv, D):
+@pytest.mark.parametrize("limbs", [2, 1])
+def test_hidden_infinities_leave_no_trace(kv, D, limbs):
     import linear_attn_decode_amd as wb
     qt, page, H = "bf16" if kv == "e4m3" else kv, 16, 2
     q, k, ks, v, vs, table, lens, starts = problem(kv, qt, D, H, 4, [13, 45], [3, 70], page, 4)
@@ -146,7 +163,7 @@ def test_hidden_infinities_leave_no_trace(kv, D):
             later = table[1][100 // page], slice(None), 100 % page     # a token that only later rows of the second request see
             v[later] = torch.full((D,), math.nan).to(v.dtype).cuda()
         o = torch.empty_like(q)
-        wb.kv_attend_chunk(q, k, v, *args, o, k_scale=ks, v_scale=vs, limbs=2)
+        wb.kv_attend_chunk(q, k, v, *args, o, k_scale=ks, v_scale=vs, limbs=limbs)
         torch.cuda.synchronize()
         outs.append(o)
     sees = 13 + 100 - 70                                      # its row
