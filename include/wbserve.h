@@ -193,8 +193,8 @@ int qk_rotate(const wb_heads* q, const wb_heads* k, int dtype, int N, int D, con
  *   first, equal ones by their column; NaN counts as -infinity in this order (K 0: not wanted).
  * Sums are float32, of differences from the largest logit, so that scale x may be of any size (log probabilities
  * past float32's range are -infinity); no log probability is above 0, no entropy below. A token outside [0, V)
- * (padding) has logprob NaN; logits of -infinity have p = 0; a row that holds a NaN or +infinity, or nothing but -infinity, has NaN in place of its log probabilities and
- * entropy. tokens: int32 [N], or int64 with tokens64. logprob, entropy: float32 [N]; top_ids int32,
+ * (padding) has logprob NaN; logits of -infinity have p = 0; a row that holds a NaN or +infinity, or nothing
+ * but -infinity, has NaN in place of its log probabilities and entropy. tokens: int32 [N], or int64 with tokens64. logprob, entropy: float32 [N]; top_ids int32,
  * top_logprobs float32. 1 <= V <= 2^24 (2^24 - 8 with K > 32), K <= 64 and V, 2^-100 <= scale <= 2^100 (1 / temperature), N >= 0.
  * `work` as for kv_attend, of token_logprobs_work() bytes. Equal calls give equal bits. No output overlaps an input. */
 int token_logprobs(const void* logits, int64_t row, int dtype, int N, int V, const void* tokens, int tokens64, float scale,

@@ -14,19 +14,21 @@
 // The weights' reference moves only when a row's maximum has risen by more than 2^4 (kThreshold): 2^4 is far from the end
 // of either type, and all tiles but a row's first few then go without rescaling the accumulators.
 // Weights enter the second product as two limbs of 16 bits (2^-16 of each in bfloat16), so that the error of o is that of
-// its own rounding. They are half of the value products, a third of the time of prompts: the caller may have one limb
-// (half a step of each weight, 2^-8 in bfloat16: 1.1 to 1.45 times the error) and 8192-token prompts of heads of 128 in 552
-// us, not 733, 8-bit ones in 683, not 845, drafts in 93, not 97. A float16 query over an 8-bit cache always has two:
-// bfloat16, which holds the values' scales, keeps 3 bits fewer than its output. Float16 weights are 2^11 of themselves
+// its own rounding. The second limb's products are a third of all: the caller may have one limb (half a step of each
+// weight, 2^-8 in bfloat16: 1.1 to 1.45 times the error) and 8192-token prompts of heads of 128 in 543 us, not 721, 8-bit
+// ones in 684, not 849, drafts in 93, not 97. A float16 query over an 8-bit cache always has two: bfloat16, which holds
+// the values' scales, keeps 3 bits fewer than its output. Float16 weights are 2^11 of themselves
 // (kShift; at most 2^15 with the lazy reference): what falls below its smallest step is 2^-36 of the largest. The sum of
 // weights is taken in float32 of the weights before they are rounded, each tile's by itself, the tiles' with what their
 // roundings leave.
 //
-// Prompts are bound by the matrix units at the power limit (8192 tokens, 32 / 8 heads of 128, bfloat16: 541 to 580 us,
-// 0.95 to 1.02 PFLOP/s, clocks at 1.8 to 2.05 GHz; the same call over zeros 485 us; a large library product 1.16 to 1.23
-// PFLOP/s over random numbers, 1.71 over zeros), in it the exponentials take 7 %, the whole of the softmax 15 %, reading
-// LDS 14 %, staging 16 % (each left out alone). Few rows over long caches are bound by reading the cache: 64 requests of
-// 5 drafted tokens each, 367 MB, 94 us (3.9 TB/s), where the last parts end late and a second launch joins.
+// Prompts (8192 tokens, 32 / 8 heads of 128, bfloat16): 720 to 750 us, 1.10 to 1.15 PFLOP/s with the second limb's products,
+// matrix cores busy 59 % of the cycles; a large library product reaches 1.16 to 1.23. With one limb they take 541 to 580 us
+// (0.95 to 1.02 PFLOP/s), the matrix cores are busy 51 %, and what is not behind products limits them: the softmax 15 %, of
+// which the exponentials 7, reading LDS 14 %, staging 16 % (each left out alone). Power limits both as well (clocks of 1.8
+// to 2.05 GHz), but less than a plain product: over zeros the one-limb call takes 485 us, 12 % less, a library product
+// 30 % less. Few rows over long caches are bound by reading the cache: 64 requests of 5 drafted tokens each, 367 MB, 97 us
+// (3.8 TB/s), where the last parts end late and a second launch joins.
 #include "serve_device.hpp"
 
 namespace wb {
@@ -86,7 +88,8 @@ __device__ __forceinline__ int64_t count_parts(const ChunkArgs& A, int blocks, i
 
 // The work of number `at`, among all parts, or among those of split blocks only. False: there are not so many. Every
 // wavefront finds it for itself. Up to 64 requests are a lane's each, taken by their spans, long ones first, so that
-// what is started last is short (16 ragged requests to 2500 tokens, 8-bit: 111 us, 145 in the order they come). Of
+// what is started last is short (64 ragged caches to 4096, 5 drafted tokens each: 97 us, 102 in the order they come; 16
+// ragged prompts, 8-bit: 123 and 126; 64 caches of one length gain nothing by it, 43 and 38). Of
 // more, a launch before this one has summed the parts (count_requests_kernel), and the sums are searched, 64 places a step.
 template <bool SPLIT_ONLY>
 __device__ __forceinline__ bool find_work(const ChunkArgs& A, int64_t at, Work& w) {
@@ -148,7 +151,7 @@ __device__ __forceinline__ bool find_work(const ChunkArgs& A, int64_t at, Work& 
 }
 
 // before[r]: the parts of requests 0 .. r - 1; behind them, the key tiles of a part. (Of more than 64 requests: requests
-// of 600 tokens, one of them new, 128 of them 64 us, 68 where each wavefront sums them for itself, 4096 1.66 ms and 5.35.)
+// of 600 tokens, one of them new, 128 of them 64 us, 68 where each wavefront sums them for itself, 4096 1.67 ms and 5.35.)
 constexpr int kCountThreads = 1024;
 __global__ void __launch_bounds__(kCountThreads) count_requests_kernel(const ChunkArgs A) {
     __shared__ int64_t sums[kCountThreads / 64];
@@ -267,7 +270,7 @@ __device__ __forceinline__ float hide(float x, int d) {
     return __uint_as_float((gone & 0xFF800000u) | (~gone & __float_as_uint(x)));
 }
 
-// 4 columns of a finished row out to o; the row's log-sum-exp with its first
+// 4 columns of a finished row, by 1 / its sum of weights, in two words of two
 template <int QT>
 __device__ __forceinline__ u32x2 scaled(f32x4 v, float by) {
     return u32x2{pack2<QT>(v[0] * by, v[1] * by), pack2<QT>(v[2] * by, v[3] * by)};
@@ -275,8 +278,9 @@ __device__ __forceinline__ u32x2 scaled(f32x4 v, float by) {
 
 // Key tiles of 64 tokens, of 32 for heads of 256 columns: with 64 such a head's tiles, sums and scores fill a compute
 // unit's memory and registers with one workgroup, whose matrix and vector units then take turns (8192-token prompts,
-// 16 heads of 256, bfloat16: 812 us, 541 with two workgroups). Narrower heads have two either way, and the larger tile has
-// fewer barriers and joins (heads of 128: within 3 % of one another in 16 bits, 8-bit 760 us and 887 with 32).
+// 16 heads of 256, bfloat16: 856 us, 711 with two workgroups). Narrower heads have two either way, and the larger tile has
+// fewer barriers and joins (8192-token prompts of heads of 128: 16 bits within 1 % of one another, 8-bit 849 us and 924
+// with 32; ragged 8-bit 123 and 135; where rows are few and blocks equal, 32 is the faster: drafts 97 and 91).
 constexpr int kWavesPerSimd = 2;
 constexpr int tile_log2(int D) { return D <= 128 ? 6 : 5; }
 
@@ -293,9 +297,9 @@ struct Chunk {
     static constexpr int kTile = 1 << tile_log2(D);
     static constexpr int NB = kTile / 32, TB = kTile / 8;            // its blocks of 32 tokens, of 8
     static constexpr int kTileBytes = kTile * D * 2;
-    // A lane's sum of weights in LDS, where its two registers are one too many: 8-bit caches, 8192 tokens of bfloat16 and
-    // float16 queries, heads of 64 402 and 514 us (496 and 606 in registers, with two wavefronts a SIMD in place of three),
-    // of 256 892 and 951 (956 and 1016, more of them spilled); heads of 128 and 16-bit caches are as fast or faster in registers
+    // A lane's sum of weights in LDS, where its two registers are one too many: 8192 tokens over 8-bit caches, heads of 64
+    // 519 us (607 in registers, with two wavefronts a SIMD in place of three), of 256 948 (1038, more of them spilled);
+    // heads of 128 and 16-bit caches are as fast or faster in registers (heads of 128 in float16 751, 771 in LDS)
     static constexpr bool kSumsInLds = KV == WB_E4M3 && D != 128;
 };
 
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
     constexpr int KS = T::KS, DB = T::DB, CB = T::CB, kTile = T::kTile, NB = T::NB, TB = T::TB;
     constexpr bool E = KV == WB_E4M3;
     constexpr int kRowBytes = D * (E ? 1 : 2);
-    constexpr float kThreshold = 4.f;            // (in powers of two; 0: an 8192-token prompt 589 us, not 563)
+    constexpr float kThreshold = 4.f;            // (in powers of two; 0: an 8192-token prompt 747 us, not 721)
     __shared__ __attribute__((aligned(1024))) uint8_t stored[2][2][T::kTileBytes];        // [buffer][keys, values]
     __shared__ f32x4 scales[2][2][kTile / 4];
     __shared__ uint32_t strange_bits[kTile][DB];                     // of the tile's values: columns of each token
@@ -682,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, kWavesPerSimd) chunk_kernel(const Ch
 
 // Joins the parts of split blocks: as many workgroups as parts, the p-th of a block for the
 // p-th share of its rows, a lane per 4 columns, with the sums of 8 parts on their way at a time (16 new
-// tokens of 16000, 128 parts: 32 us a call; 52 with one part after the other).
+// tokens of 16000, 128 parts: 34 us a call; 59 with one part after the other).
 constexpr int kOnWay = 8;
 template <int QT, int D, int SHIFT>
 __global__ void __launch_bounds__(kThreads) join_chunks_kernel(const ChunkArgs A) {
@@ -771,9 +775,9 @@ hipError_t chunk_t(const ChunkArgs& a, hipStream_t s) {
 }  // namespace
 
 // Tokens of a part at least, where a request's block is split. All tiles are cut into about as many parts as the device
-// holds workgroups (512): twice as many make 64 requests of drafts 102 us, not 94 (the starts of parts, their sums and
-// the join), and windows 64, not 48. (One request's 16 new tokens of 1000: 13.9 us with parts of 128 tokens, 18.0 with 256;
-// of 4000 18.2 and 17.8.)
+// holds workgroups (512): twice as many make 64 requests of drafts 106 us, not 97 (the starts of parts, their sums and
+// the join), and windows 73, not 59. (One request's 16 new tokens of 1000: 14.4 us with parts of 128 tokens, 19.0 with 256;
+// of 4000 18.4 and 18.7.)
 constexpr int kPartTokens = 128;
 
 ChunkPlan chunk_plan(const wb_kv_cache& c, int N, int R, int Hq, int width) {

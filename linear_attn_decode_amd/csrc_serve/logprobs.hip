@@ -15,7 +15,8 @@
 // read again, and columns at or above the least of their maxima kept: a few more than K, as a rule.
 // Where they do not fit (constant rows, or all columns but a few at -infinity), the first K of those
 // groups' vectors are found likewise, and the top K among their 8 K columns.
-// 2047 rows of 151001 bfloat16 logits with 20 alternatives: 121 us, 5.1 TB/s (618 MB); one row of 128000: 14.3 us.
+// 2047 rows of 151001 bfloat16 logits with 5 alternatives: 121 us, 5.1 TB/s (618 MB), with 64 151; one float32 row of
+// 128000 with 20: 13.8 us.
 #include "serve_device.hpp"
 
 namespace wb {
@@ -167,8 +168,8 @@ __device__ __forceinline__ uint32_t largest_values(const uint32_t* values, int n
     return largest_of<8>(values, n, K, places);
 }
 
-// The first K of n distinct keys in order, out[0 .. K) (0 where there are fewer), by all threads of the workgroup, which
-// have all stored their keys. `spare` has room for kOrdered keys, `bins` for 256 counts.
+// The first K of n distinct keys (at most kOrdered) in order, out[0 .. K) (0 where there are fewer), by all threads of the
+// workgroup, which have all stored their keys
 __device__ __forceinline__ void order_keys(const uint64_t* keys, int n, int K, uint64_t* out) {
     // each key's place is the number of larger ones
     const int tid = threadIdx.x;
@@ -187,6 +188,7 @@ __device__ __forceinline__ void order_keys(const uint64_t* keys, int n, int K, u
     }
     __syncthreads();
 }
+// The same of any number of keys. `spare` has room for kOrdered of them, `bins` for 256 counts.
 __device__ __forceinline__ void first_keys(const uint64_t* keys, int n, int K, uint64_t* out, uint64_t* spare, int* bins) {
     const int tid = threadIdx.x;
     if (n <= kOrdered) return order_keys(keys, n, K, out);
@@ -228,7 +230,7 @@ __device__ __forceinline__ void first_keys(const uint64_t* keys, int n, int K, u
 }
 
 // Wavefronts a SIMD has room for. Float32 chunks of 1024 columns do not fit the registers of eight: 2000 rows of 100000 with
-// 20 alternatives 149 us, 193 with eight (600 rows of 128000 65.4 and 70.0).
+// 20 alternatives 151 us, 193 with eight (600 rows of 128000 66.1 and 69.5).
 constexpr int waves_per_simd(int type, int J) { return type == WB_F32 && J == 2 ? 6 : 8; }
 
 // A wavefront takes chunks of 64 J vectors at a time. TOP: vectors of a group, whose maximum is kept: 8 (64 columns), 64 J
@@ -500,11 +502,11 @@ hipError_t logprobs_t(const LogprobArgs& a, unsigned groups, hipStream_t s) {
 }  // namespace
 
 // Segments of a row: enough for 256 workgroups, one a compute unit (with four of them a batch of 32 rows of 128000 and 20
-// alternatives takes 25.5 us, not 18.8, and 128 rows 28.1, not 20.3: every segment finds alternatives of its own), of 16
-// chunks of 512 columns at least, and so that their alternatives can be ordered as one list. A segment's groups, whose maxima are kept: the largest of which there are
-// twice as many as alternatives wanted (or hardly anything could be left out), up to 512, and whose vectors, of the
-// first K groups, fit LDS (K 128 of them up to 32 alternatives; past that K 64, so that 64 segments hold 2^24 - 8 columns
-// from any alignment on).
+// alternatives takes 24.4 us, not 18.0: every segment finds alternatives of its own), of 16 chunks of 512 columns at least,
+// and so that their alternatives can be ordered as one list. A segment's groups, whose maxima are kept: the largest of which
+// there are twice as many as alternatives wanted (or hardly anything could be left out), up to 512, and whose vectors, of
+// the first K groups, fit LDS (K 128 of them up to 32 alternatives; past that K 64, so that 64 segments hold 2^24 - 8
+// columns from any alignment on).
 LogprobPlan logprob_plan(int N, int V, int K) {
     const int chunks = (V + 7 + 511) / 512;
     LogprobPlan p;

@@ -285,13 +285,13 @@ hipError_t launch_rotate(RotateArgs a, int N, hipStream_t s) {
     a.lanes = 4;
     while (a.lanes < units && a.lanes < 64) a.lanes *= 2;
     // Wavefronts of a token: one takes all of its heads, which then share its angles, where there are tokens enough for
-    // 4096 of them (4 a SIMD); else more, down to one head a slot. (40 heads of 128: 4000 tokens 19.3 us, 21.0 with 8192
-    // and 18.4 with 2048; 1000 tokens 7.5, 7.1 and 8.2.)
+    // 4096 of them (4 a SIMD); else more, down to one head a slot. (40 heads of 128: 4000 tokens 18.6 us, 20.2 with 8192
+    // and 17.5 with 2048; 1000 tokens 6.7, 6.8 and 7.4; column by column, 4000 tokens 46, 53 and 67.)
     const int slots = 64 / a.lanes, rounds = (a.q.H + a.k.H + slots - 1) / slots;
     int64_t wanted = (4096 + int64_t(N) - 1) / N;
     a.waves_per_token = int(wanted < rounds ? wanted : rounds);
     // Outputs that the 256 MB last-level cache could not hold are stored past the caches (32773 tokens of 40 heads of 128,
-    // 336 MB: 146 us against 154); what fits is left there for the calls that read it.
+    // 336 MB: 146 us against 153); what fits is left there for the calls that read it.
     a.past = int64_t(N) * (a.q.H + a.k.H) * a.D * (a.dtype == WB_F32 ? 4 : 2) > int64_t(256) << 20;
     const int64_t most = kLaunchItems / (64 * int64_t(a.waves_per_token));      // tokens of a launch
     for (int64_t first = 0; first < N; first += most) {
