@@ -134,7 +134,8 @@ int kv_attend_work(const wb_kv_cache* c, int R, int Hq, int width, size_t* bytes
  * key-value head h / (Hq / H), sees t in [max(0, p + 1 - window), p] (window 0: [0, p]):
  *   s_t = scale * q[row][h] . k_t,  o[row][h] = sum_t e^{s_t} v_t / sum_t e^{s_t},
  *   lse[row][h] = log sum_t e^{s_t} (float32 [N][Hq], or NULL).
- * Scores, maxima and sums are float32. The weights e^{s_t - ref} (ref within 4 / log2(e) of the
+ * Scores, maxima and sums are float32 (a row whose weighted sum of values, of weights to 2^4, passes its range
+ * has infinities). The weights e^{s_t - ref} (ref within 4 / log2(e) of the
  * running maximum; times the value's scale, for an 8-bit cache) enter the product with v as two 16-bit
  * limbs of the cache's type (bfloat16 for an 8-bit one): within 2^-16 of each weight in bfloat16, 2^-21
  * and 2^-36 of the largest in float16. With WB_ONE_LIMB added to q_dtype they enter as one (2^-8; 2^-11
